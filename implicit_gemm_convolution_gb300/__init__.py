@@ -104,6 +104,8 @@ def lib() -> ctypes.CDLL:
             L.om_conv2d_f32_packed_ws.restype = ci
             L.om_conv2d_f32_packed_ws.argtypes = [i64] * 11 + [vp, vp, vp, ci, vp,
                                                   ctypes.c_size_t, vp]
+            from . import decode
+            decode._declare(L)
             _lib = L
     return _lib
 
@@ -332,3 +334,15 @@ def conv2d_ex(x, w, stride: int = 1, padding: int = 0, dilation: int = 1, groups
                                   ACTIVATIONS[activation], out.data_ptr(), _mode(mode), ws[0],
                                   ws[1], _stream_handle(stream)), "om_conv2d_f32_ex")
     return out
+
+
+# the decoding operators need torch when they are first named, not at import
+_DECODE = ("PagedKVCache", "kv_append", "kv_attention", "kv_read", "new_kv_workspace", "rope_table", "w4_matvec")
+
+
+def __getattr__(name):
+    if name in _DECODE:
+        from . import decode
+        globals()[name] = getattr(decode, name)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

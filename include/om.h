@@ -331,6 +331,157 @@ OM_API int om_conv2d_f32_ex(int64_t N, int64_t Cin, int64_t H, int64_t W,
                             void *stream);
 
 /*
+ * ------------------------------------------------ decoding operators
+ * The products and the attention of a language model's decoding step: 4-bit
+ * weights for the products of a few rows, and a paged cache of keys and
+ * values in 8 bits with its append, attention and read back. The pages have no
+ * counterpart. Sums, softmax statistics and scales are 32 bits; activations are
+ * OM_F32, OM_F16 or OM_BF16 (one type per call), computed in 32 bits and
+ * rounded once.
+ */
+typedef enum om_dtype {
+    OM_F32 = 0,
+    OM_F16 = 1,
+    OM_BF16 = 2,
+    OM_I8 = 3,   /* cache codes: whole numbers -127 .. 127 */
+    OM_E4M3 = 4  /* cache codes: 8-bit floats, 4 exponent and 3 mantissa bits, up to 448 */
+} om_dtype;
+
+/*
+ * y[i][j] = sum over p < k of x[i][p] * (u[j][p] - z[j][g]) * s[j][g], g = p / group.
+ *   x: m x k, row stride ldx >= k; y: m x n, row stride ldy >= n; both x_dtype.
+ *   w: n rows of (k + 1) / 2 bytes, row stride ldw bytes; the 4-bit code u[j][p]
+ *      is the low half of byte p / 2 for even p, the high half for odd p.
+ *   scales: n x ceil(k / group) of scale_dtype (OM_F32, OM_F16, OM_BF16), row
+ *      stride lds. zeros: as many bytes 0 .. 15, row stride ldz, or NULL (8 everywhere).
+ *   group: 32, 64 or a multiple of 128 (OM_ERR_UNSUPPORTED otherwise); the last
+ *      group of a row may be short.
+ * Made for few rows (a decoding batch): the weights are read once for each
+ * eight or so rows of x. The difference u - z and its products with x are exact (an
+ * OM_F32 x is taken as three 8-bit parts); sums are 32 bits. Any alignment of
+ * w and zeros; 16-byte aligned w with ldw a multiple of 16 is the fast form.
+ * m or n zero: OM_OK, nothing launched. k == 0: +0 everywhere.
+ */
+OM_API int om_w4_matvec(int64_t m, int64_t n, int64_t k, int64_t group,
+                        const void *x, int64_t ldx, int x_dtype,
+                        const uint8_t *w, int64_t ldw,
+                        const void *scales, int64_t lds, int scale_dtype,
+                        const uint8_t *zeros, int64_t ldz,
+                        void *y, int64_t ldy, void *stream);
+
+/* Frequencies of om_rope_table: base^(-2i/rot), i < rot / 2, and their scaling for
+ * contexts `factor` times longer than the `original` one. */
+typedef enum om_rope_scaling {
+    OM_ROPE_PLAIN = 0,
+    OM_ROPE_LINEAR = 1, /* every frequency / factor */
+    OM_ROPE_NTK = 2,    /* base * factor^(rot / (rot - 2)) */
+    OM_ROPE_YARN = 3    /* frequencies that turn fewer than beta_slow times in `original` positions / factor,
+                           those that turn more than beta_fast times kept, a linear ramp between;
+                           cos and sin times 0.1 ln(factor) + 1 */
+} om_rope_scaling;
+
+/* The pairs a rotation turns: elements (i, i + rot/2), or (2i, 2i + 1). */
+typedef enum om_rope_pairs {
+    OM_ROPE_HALF = 0,
+    OM_ROPE_INTERLEAVED = 1
+} om_rope_pairs;
+
+/*
+ * Fills table [rows][rot / 2][2] (16-byte aligned for om_kv_append) with cos and
+ * sin of position * frequency, evaluated in 64 bits and rounded once. base > 1,
+ * factor >= 1; original, beta_fast > beta_slow > 0 are read for OM_ROPE_YARN only.
+ */
+OM_API int om_rope_table(int64_t rows, int64_t rot, double base, int scaling, double factor,
+                         double original, double beta_fast, double beta_slow, float *table,
+                         void *stream);
+
+/*
+ * A paged cache (the struct is read during the call; the memory is the caller's).
+ *   k, v: codes [pages][heads][page][dim], 16-byte aligned; a value is code * scale.
+ *   k_scale, v_scale: [pages][heads].
+ *   page: 16, 32, 64 or 128 tokens; dim: 64, 128 or 256 (OM_ERR_UNSUPPORTED otherwise).
+ * A batch of sequences reaches it through block_table [seqs][width] (the page of positions
+ * j*page .. j*page + page - 1 of sequence b is block_table[b][j]) and cu [seqs + 1],
+ * not decreasing from 0: sequence b has the tokens cu[b] .. cu[b + 1] - 1 of
+ * the call's `tokens` tokens. Table entries outside [0, pages), positions outside the
+ * table and offsets outside the batch are never followed: such tokens are not
+ * stored, not attended to, and read as NaN. A page belongs to one sequence
+ * while it is written.
+ */
+typedef struct om_kv_cache {
+    void *k, *v;
+    float *k_scale, *v_scale;
+    int64_t pages, heads, page, dim;
+    int dtype; /* OM_I8 or OM_E4M3 */
+} om_kv_cache;
+
+/*
+ * Appends the new tokens of each sequence, its last ones: ctx_len[b] counts the
+ * sequence's tokens WITH them, so they take positions ctx_len[b] - new .. ctx_len[b] - 1.
+ * max_new: at least the largest number of new tokens of a sequence (tokens beyond it
+ * may be left out). q, k, v: [tokens][heads][dim] of dtype with token and head strides in
+ * elements (unit stride along dim).
+ * Queries and keys are turned by their position's row of table [rows][rot/2][2]
+ * (cos, sin): (a, b) -> (a cos - b sin, b cos + a sin) over the pairs of the first rot
+ * elements (a multiple of 8, 0: none), each product and sum rounded to 32
+ * bits; positions outside the table turn to NaN. q_out receives the queries
+ * (q_heads 0: none; q_out may be q itself).
+ * A page's scale becomes the larger of its old one and fl(top * fl(1 / T)), top the
+ * largest magnitude of its new values, T = 127 or 448; the old scale counts
+ * only if the page has earlier tokens of the sequence. Old codes become the nearest code of
+ * code * fl(old / new), new ones of fl(value / scale), ties to even. A value that
+ * is not finite gives its page and head the scale NaN. Every output has one bit pattern.
+ */
+OM_API int om_kv_append(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int64_t max_new,
+                        int64_t q_heads,
+                        const void *q, int64_t q_ts, int64_t q_hs,
+                        const void *k, int64_t k_ts, int64_t k_hs,
+                        const void *v, int64_t v_ts, int64_t v_hs, int dtype,
+                        const float *table, int64_t rows, int64_t rot, int pairs,
+                        const int32_t *block_table, int64_t width,
+                        const int32_t *ctx_len, const int32_t *cu,
+                        void *q_out, int64_t qo_ts, int64_t qo_hs, void *stream);
+
+/*
+ * Reads tokens back as values: token i of sequence b is position start[b] + i.
+ * k_out, v_out: [tokens][heads][dim] contiguous, 16-byte aligned, dtype OM_F32, OM_F16
+ * or OM_BF16; fl(code * scale), rounded once more to a 16-bit type.
+ */
+OM_API int om_kv_read(const om_kv_cache *cache, int64_t seqs, int64_t tokens,
+                      const int32_t *block_table, int64_t width,
+                      const int32_t *start, const int32_t *cu,
+                      void *k_out, void *v_out, int dtype, void *stream);
+
+/*
+ * Bytes of the scratch of om_kv_attention for calls of these heads with at
+ * most max_new queries a sequence (0 for invalid arguments).
+ */
+OM_API size_t om_kv_workspace_bytes(int64_t kv_heads, int64_t q_heads, int64_t dim, int64_t max_new);
+
+/*
+ * Attention of each sequence's queries, its last tokens (positions as in om_kv_append),
+ * to its cached tokens: the query at position p sees positions
+ * max(0, p - window + 1) .. p (window 0: 0 .. p). q_heads must be a multiple of the
+ * cache's heads; query head h reads head h / (q_heads / heads).
+ *   out[t][h] = sum_i softmax_i(scale * q[t][h] . key_i) value_i, of q's dtype;
+ *   lse: NULL, or [tokens][q_heads]: the natural log of the sum of exponentials.
+ * A query that sees no token gives zeros and lse -inf. Memory behind masked tokens
+ * (stale codes, pages outside the window) never reaches an output.
+ * workspace: NULL (each sequence and head by one block), or device memory, 16-byte
+ * aligned, of om_kv_workspace_bytes, zeroed once before its first use: long
+ * sequences are then split evenly over the GPU. Calls that may run at the same time
+ * need distinct workspaces. Results do not depend on timing: the split and the order in
+ * which parts are joined follow from the lengths and the device alone.
+ */
+OM_API int om_kv_attention(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int64_t max_new,
+                           int64_t q_heads,
+                           const void *q, int64_t q_ts, int64_t q_hs, int dtype,
+                           const int32_t *block_table, int64_t width,
+                           const int32_t *ctx_len, const int32_t *cu, float scale, int64_t window,
+                           void *out, int64_t o_ts, int64_t o_hs, float *lse,
+                           void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Synchronises stream, then reads and clears the library's device-wide status
  * words for the current device. Every device-side wait in the library's
  * kernels (mbarrier waits of the TMA and tensor-core pipelines) is bounded;
