@@ -1,7 +1,7 @@
 // decode.h -- problems of the decoding operators (4-bit matrix-vector product,
 // paged 8-bit cache: append, attention, read back), validated by
-// decode_api.cu and run by w4_matvec.cu, kv_cache.cu and kv_attention.cu. Not installed; not
-// part of the public ABI.
+// decode_api.cu and run by w4_matvec.cu, kv_cache.cu and kv_attention.cuh. Not
+// installed; not part of the public ABI.
 #pragma once
 
 #include <cstdint>
@@ -79,8 +79,7 @@ struct KvAttentionProblem {
 constexpr int64_t kKvMaxBlocks = 608;
 constexpr size_t kKvCounterBytes = 4096;
 inline int64_t kv_block_rows(int64_t group, int64_t dim, int64_t max_new) {
-    // in eighths of 2^28 rows nothing overflows; more rows than a block holds
-    // take further blocks
+    // more rows than a block holds take further blocks
     const int64_t rows = max_new > (int64_t(1) << 20) || group > (int64_t(1) << 20) ? int64_t(1) << 20 : group * max_new;
     if (rows <= 8) return 8;
     return rows <= 16 || dim > 128 ? 16 : 32;
@@ -88,7 +87,9 @@ inline int64_t kv_block_rows(int64_t group, int64_t dim, int64_t max_new) {
 inline size_t kv_workspace_bytes(int64_t group, int64_t dim, int64_t max_new) {
     return kKvCounterBytes + static_cast<size_t>(2 * kKvMaxBlocks * kv_block_rows(group, dim, max_new) * (dim + 2) * 4);
 }
-cudaError_t launch_kv_attention(const KvAttentionProblem &p, cudaStream_t s);
+cudaError_t launch_kv_attention_f32(const KvAttentionProblem &p, cudaStream_t s);
+cudaError_t launch_kv_attention_f16(const KvAttentionProblem &p, cudaStream_t s);
+cudaError_t launch_kv_attention_bf16(const KvAttentionProblem &p, cudaStream_t s);
 
 cudaError_t launch_rope_table(int64_t rows, int64_t rot, double base, int scaling, double factor,
                               double original, double beta_fast, double beta_slow, float *table,

@@ -269,7 +269,9 @@ int om_kv_attention(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int6
         for (int j = 0; j < i; ++j)
             if (overlaps(w[i], w[j])) return OM_ERR_ALIAS;
     }
-    return from_cuda(om::launch_kv_attention(p, static_cast<cudaStream_t>(stream)));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (dtype == OM_F32) return from_cuda(om::launch_kv_attention_f32(p, s));
+    return from_cuda(dtype == OM_F16 ? om::launch_kv_attention_f16(p, s) : om::launch_kv_attention_bf16(p, s));
 }
 
 }  // extern "C"
