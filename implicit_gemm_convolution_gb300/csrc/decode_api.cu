@@ -248,6 +248,9 @@ int om_kv_attention(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int6
     const int bst = check_batch(seqs, tokens, block_table, width, c.page, ctx_len, cu);
     if (bst != OM_OK) return bst;
     if (q_heads > 65535 || tokens * q_heads > kLim31) return OM_ERR_TOO_LARGE;
+    // pieces of 64 positions of every key head and eight query rows, at most
+    const __int128 units = static_cast<__int128>(width * c.page / 64 + 1) * c.heads * (tokens * (q_heads / c.heads) / 8 + seqs);
+    if (units > kLim31 - (1 << 20)) return OM_ERR_TOO_LARGE;
     om::KvAttentionProblem p{c, seqs, tokens, max_new, q_heads, {q, q_ts, q_hs}, {out, o_ts, o_hs}, dtype, lse,
                              block_table, width, ctx_len, cu, scale, window, workspace};
     int st = check_heads(p.q, tokens, q_heads, c.dim, dtype, false);

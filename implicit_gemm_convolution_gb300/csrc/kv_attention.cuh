@@ -49,8 +49,6 @@ struct Shape {
     static constexpr int kValueChunks = DIM / 8 / kValueBytes;
     static constexpr int kSteps = DIM / 16;                  // k-steps of S, row tiles of O
     static constexpr int kTileBytes = 2 * kTile * DIM;
-    static constexpr int kStages = DIM == 64 ? 6 : (DIM == 128 ? 4 : 3);
-    static constexpr int kRing = kStages * kTileBytes;       // of one warp
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes) {
@@ -82,8 +80,7 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 __device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
@@ -124,292 +121,502 @@ __device__ __forceinline__ uint32_t widen(uint32_t w) {  // bytes 0, 1 (or 2, 3)
         memcpy(&r, &h, 4);
         return r;
     } else {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(HIGH ? w >> 16 : w & 0xffffu), __NV_E4M3);
-        return static_cast<uint32_t>(h.x) | static_cast<uint32_t>(h.y) << 16;
+        uint32_t r;
+        if constexpr (HIGH)
+            asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, b;\n\t}" : "=r"(r) : "r"(w));
+        else
+            asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\t}" : "=r"(r) : "r"(w));
+        return r;
     }
 }
 
 struct Args {
     KvAttentionProblem p;
-    int pairs;  // outputs are aligned for stores of two
+    bool out_fours, q_fours;  // outputs and queries are aligned for stores and loads of four
 };
 
-// What a block does for one sequence.
+// What a block does for one sequence. Units and positions are below 2^31.
 struct Sequence {
-    int64_t b, t0;         // first token of the batch
-    int64_t ctx, limit;    // tokens, and positions the table reaches
-    int queries;
-    int row_blocks;
-    int64_t first_unit, units;
+    int b, t0;  // t0: its first token in the batch
+    int queries, row_blocks;
+    int first_unit, units;
+    int64_t start;  // position of the first query
+    int limit;      // positions before it are in the cache
 };
 
 template <int ROWS>
 __device__ __forceinline__ Sequence sequence_of(const KvAttentionProblem &p, int64_t b, int group) {
     Sequence s;
-    int64_t t1;
-    token_range(p.cu, b, p.tokens, &s.t0, &t1);
-    s.b = b;
-    s.ctx = p.ctx[b];
-    s.queries = static_cast<int>(t1 - s.t0);
-    s.row_blocks = static_cast<int>((static_cast<int64_t>(s.queries) * group + ROWS - 1) / ROWS);
-    s.limit = p.width * p.c.page;
-    const int64_t hi = s.ctx < s.limit ? s.ctx : s.limit;
-    int64_t lo = 0;
-    if (p.window > 0) lo = s.ctx - s.queries - p.window + 1;
-    if (lo < 0) lo = 0;
+    int64_t t0, t1;
+    token_range(p.cu, b, p.tokens, &t0, &t1);
+    const int64_t ctx = p.ctx[b], reach = p.width * p.c.page;
+    s.b = static_cast<int>(b);
+    s.t0 = static_cast<int>(t0);
+    s.queries = static_cast<int>(t1 - t0);
+    s.row_blocks = (s.queries * group + ROWS - 1) / ROWS;
+    s.start = ctx - s.queries;
+    s.limit = static_cast<int>(max(min(ctx, reach), static_cast<int64_t>(0)));
+    const int lo = p.window > 0 ? static_cast<int>(max(s.start - p.window + 1, static_cast<int64_t>(0))) : 0;
     s.first_unit = lo / kUnit;
-    s.units = (hi + kUnit - 1) / kUnit - s.first_unit;
-    if (s.units < 1) s.units = 1;  // rows that see nothing are written too
+    s.units = max((s.limit + kUnit - 1) / kUnit - s.first_unit, 1);  // rows that see nothing are written too
     return s;
 }
 
-// Joins two partial results of the same columns: (m, l, O) with O of 2^(x - m) weights.
-template <int N>
-__device__ __forceinline__ float weight_of(float m, float top) {
-    return m == -INFINITY ? 0.0f : ex2(m - top);
-}
+// What the output of a finished item needs: its units and its rows.
+struct Part {
+    int begin, end;
+    int t0, h, row0, rows;
+};
 
-template <typename T>
-__device__ __forceinline__ void store_pair(T *dst, float a, float b, bool pairs) {
-    if (!pairs) {
-        dst[0] = from_float<T>(a);
-        dst[1] = from_float<T>(b);
-    } else if constexpr (sizeof(T) == 4) {
-        *reinterpret_cast<float2 *>(dst) = make_float2(a, b);
-    } else {
-        T e[2] = {from_float<T>(a), from_float<T>(b)};
-        uint32_t w;
-        memcpy(&w, e, 4);
-        *reinterpret_cast<uint32_t *>(dst) = w;
+// Finished rows, [row][DIM + 4] floats in shared memory, to the outputs; every thread of the block.
+template <typename T, int DIM>
+__device__ __forceinline__ void write_rows(const Args &a, const Part &part, int group, const float *stage) {
+    constexpr int kQuads = DIM / 4;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < part.rows * kQuads; i += kThreads) {
+        const int col = i / kQuads, d = i % kQuads * 4, r = part.row0 + col;
+        T *dst = static_cast<T *>(const_cast<void *>(a.p.out.p)) + (part.t0 + r / group) * a.p.out.ts +
+                 (static_cast<int64_t>(part.h) * group + r % group) * a.p.out.hs + d;
+        const float4 f = *reinterpret_cast<const float4 *>(stage + col * (DIM + 4) + d);
+        const float v[4] = {f.x, f.y, f.z, f.w};
+        if (a.out_fours)
+            store4<T, true>(dst, v);
+        else
+            store4<T, false>(dst, v);
     }
 }
 
-template <typename T, int KV, int DIM, int NT>
-__global__ void __launch_bounds__(kThreads) kv_attention_kernel(const __grid_constant__ Args a) {
+__device__ __forceinline__ void write_lse(const KvAttentionProblem &p, const Part &part, int group, int col, float top, float sum) {
+    const int r = part.row0 + col;
+    if (p.lse && col < part.rows)
+        p.lse[(part.t0 + r / group) * p.q_heads + static_cast<int64_t>(part.h) * group + r % group] =
+            sum == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(top - kBias, log2f(sum)), 0.6931471805599453f);
+}
+
+template <typename T, int DIM, int NT>
+struct Config {
     using S = Shape<DIM>;
-    constexpr int kRows = 8 * NT;
-    constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
+    // 11-bit parts of queries and of weights: a float16 query is one part as it is, but its
+    // output is as exact as one rounded weight, so its weights take two
+    static constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
+    static constexpr int kWeightParts = std::is_same_v<T, __nv_bfloat16> ? 1 : 2;
     // query fragments stay in registers where they fit beside the sums
-    constexpr bool kQShared = NT * kParts * S::kSteps > 16;
+    static constexpr bool kQShared = NT * kParts * S::kSteps > 16;
+    static constexpr int kQBytes = kParts * S::kSteps * NT * 256;
+    static constexpr int kStages = DIM == 64 ? 6 : (DIM == 128 && NT == 4 ? 4 : 3);
+    static constexpr int kJoin = S::kSteps * NT * 128 + NT * 128;  // floats of one warp's state
+    // the next segment's copies start before the join of the warps, which then has memory of its own
+    static constexpr bool kEarly = NT == 1;
+    static constexpr int kRing = kStages * S::kTileBytes;  // of one warp
+    static constexpr int kSmem = kWarps * kRing + kQBytes + (kEarly ? 2 * kJoin * 4 : 0);
+    static constexpr int64_t kSlot = 8 * NT * (DIM + 2);
+    // a weight for each part and row, then the finished rows, fit in the ring
+    static constexpr int kMostParts = (kWarps * kRing / 4 - 8 * NT * (DIM + 4) - 4) / (8 * NT);
+    static constexpr int kMaxBlocks = kMostParts < kKvMaxBlocks ? kMostParts : kKvMaxBlocks;
+    static_assert(8 * NT * (DIM + 4) <= 2 * kJoin, "finished rows fit where the warps are joined");
+    static_assert(kEarly || 2 * kJoin * 4 <= kWarps * kRing, "the join fits in the ring");
+    static_assert(2 * kThreads * 4 <= kQBytes, "the sums of the parts' join fit where the queries were");
+};
+
+template <typename T, int KV, int DIM, int NT>
+__global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_constant__ Args a) {
+    using S = Shape<DIM>;
+    using C = Config<T, DIM, NT>;
+    constexpr int kRows = 8 * NT;
+    constexpr int kParts = C::kParts;
+    constexpr bool kQShared = C::kQShared;
     constexpr int kFrag = S::kSteps * NT;  // float4 of O per lane
     const KvAttentionProblem &p = a.p;
+    unsigned *const counters = static_cast<unsigned *>(p.workspace);
+    float *const slots = reinterpret_cast<float *>(static_cast<uint8_t *>(p.workspace) + kKvCounterBytes);
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, g = lane / 4, c = lane % 4;
     const int group = static_cast<int>(p.q_heads / p.c.heads);
-    const int page = static_cast<int>(p.c.page), heads = static_cast<int>(p.c.heads);
+    const int page = static_cast<int>(p.c.page), page_log = 31 - __clz(page), heads = static_cast<int>(p.c.heads);
 
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float row_factor[kRows];
-    __shared__ long long scan[kWarps];
-    __shared__ int is_last;
-    uint8_t *const ring = smem + warp * S::kRing;
-    const uint32_t ring_at = smem_u32(ring);
-    uint2 *const q_shared = reinterpret_cast<uint2 *>(smem + kWarps * S::kRing);  // [part][step][nt][lane]
+    __shared__ int2 row_seen[kRows];  // a row sees the positions in (x, y]
+    __shared__ int scan[kWarps], found_before;
+    __shared__ Sequence found;
+    __shared__ Part pending[2];  // parts of items of this block: its first and its last segment's
+    __shared__ int arrived_last[2];
+    const uint32_t ring_at = smem_u32(smem + warp * C::kRing);
+    uint2 *const q_shared = reinterpret_cast<uint2 *>(smem + kWarps * C::kRing);  // [part][step][nt][lane]
+    float *const join = reinterpret_cast<float *>(C::kEarly ? smem + kWarps * C::kRing + C::kQBytes : smem);
 
     // ---- this block's share of the units of all items (sequence, key head, row block)
-    long long total = 0;
-    for (int64_t b = threadIdx.x; b < p.seqs; b += kThreads) {
-        const Sequence s = sequence_of<kRows>(p, b, group);
-        total += static_cast<long long>(heads) * s.row_blocks * s.units;
+    const int seqs = static_cast<int>(p.seqs);
+    int total = 0;
+#pragma unroll 1
+    for (int i = threadIdx.x; i < seqs; i += kThreads) {
+        const Sequence s = sequence_of<kRows>(p, i, group);
+        total += heads * s.row_blocks * s.units;
     }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    total = __reduce_add_sync(0xffffffffu, total);
     if (lane == 0) scan[warp] = total;
     __syncthreads();
     total = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) total += scan[w];
     const bool split = p.workspace != nullptr;
-    long long per = (total + gridDim.x - 1) / gridDim.x;
-    if (per < kMinUnits) per = kMinUnits;
-    const long long u0 = blockIdx.x * per, u1 = u0 + per < total ? u0 + per : total;
-    if (u0 >= total) return;
+    const int per = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), kMinUnits);
+    if (static_cast<int64_t>(blockIdx.x) * per >= total) return;
+    const int u0 = blockIdx.x * per, u1 = min(u0 + per, total);
 
     // the sequence that unit u0 belongs to, and the units before it
-    int64_t b = 0;
-    long long before = 0;
-    for (int64_t base = 0;; base += kThreads) {
-        const int64_t mine = base + threadIdx.x;
-        long long n = 0;
-        if (mine < p.seqs) {
-            const Sequence s = sequence_of<kRows>(p, mine, group);
-            n = static_cast<long long>(heads) * s.row_blocks * s.units;
+    int before = 0;
+#pragma unroll 1
+    for (int base = 0;; base += kThreads) {
+        Sequence s;
+        int n = 0;
+        if (base + static_cast<int>(threadIdx.x) < seqs) {
+            s = sequence_of<kRows>(p, base + threadIdx.x, group);
+            n = heads * s.row_blocks * s.units;
         }
-        long long up = n;
+        int up = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const long long x = __shfl_up_sync(0xffffffffu, up, o);
+            const int x = __shfl_up_sync(0xffffffffu, up, o);
             if (lane >= o) up += x;
         }
         __syncthreads();
         if (lane == 31) scan[warp] = up;
         __syncthreads();
-        long long chunk = 0, lower = 0;
+        int chunk = 0, lower = 0;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
             if (w < warp) lower += scan[w];
             chunk += scan[w];
         }
-        up += lower;  // units up to and with this thread's sequence, in the chunk
-        if (before + chunk > u0) {
-            __shared__ long long found[2];
-            if (before + up > u0 && before + up - n <= u0) {
-                found[0] = mine;
-                found[1] = before + up - n;
-            }
-            __syncthreads();
-            b = found[0];
-            before = found[1];
-            break;
+        up += before + lower;  // units up to and with this thread's sequence
+        if (up > u0 && up - n <= u0) {
+            found = s;
+            found_before = up - n;
         }
         before += chunk;
+        if (before > u0) break;
     }
+    __syncthreads();
+    Sequence seq = found;
+    before = found_before;
 
-    Sequence seq = sequence_of<kRows>(p, b, group);
-    long long u = u0;
-    while (u < u1) {
-        while (u >= before + static_cast<long long>(heads) * seq.row_blocks * seq.units) {
-            before += static_cast<long long>(heads) * seq.row_blocks * seq.units;
-            seq = sequence_of<kRows>(p, ++b, group);
-        }
-        const long long item = (u - before) / seq.units;
-        const long long item_start = before + item * seq.units, item_end = item_start + seq.units;
-        const int h = static_cast<int>(item / seq.row_blocks), rb = static_cast<int>(item % seq.row_blocks);
-        long long stop = item_end < u1 ? item_end : u1;
-        if (!split) {  // whole items, by the block that has their first unit
-            if (u > item_start) {
-                u = stop;
-                continue;
+    // ---- the segment at hand: a range of one item's units
+    Part part{};
+    int u = u0, stop = u0;
+    int hi = 0, lo_last = 0, all_see = 0, w0 = 0, w1 = 0, n_parts = 0;
+    bool whole = false, at_start = false;
+    // pages: lane i holds page pb + i (0) and pb + 32 + i (1), with their scales
+    int pb = 0, pages_end = 0, id0 = -1, id1 = -1;
+    float ka0 = 0.0f, va0 = 0.0f, ka1 = 0.0f, va1 = 0.0f;
+    // the next tile to copy
+    int f_pos = 0, f_id = -1;
+    uint32_t f_dst = 0;
+    const int64_t page_bytes = static_cast<int64_t>(heads) * page * DIM;
+    const uint8_t *k_lane = nullptr, *f_k = nullptr;
+    const int64_t v_lane = static_cast<const uint8_t *>(p.c.v) - static_cast<const uint8_t *>(p.c.k) + 2 * c * DIM + g * S::kValueBytes -
+                           (g * DIM + c * 16);  // from a lane's place among the keys to its place among the values
+    bool f_new = true;
+    auto load_id = [&](int j) -> int {
+        const int id = j < pages_end ? p.block_table[seq.b * p.width + j] : -1;
+        return id < p.c.pages ? id : -1;
+    };
+    auto load_scales = [&](int id, float *ka, float *va) {
+        const int64_t at = static_cast<int64_t>(id) * heads + part.h;
+        *ka = id < 0 ? 0.0f : p.c.k_scale[at];
+        *va = id < 0 ? 0.0f : p.c.v_scale[at];
+    };
+    auto fetch = [&]() {
+        if (f_pos < w1) {
+            if (f_new || (f_pos & (page - 1)) == 0) {
+                const int off = (f_pos >> page_log) - pb;
+                f_id = __shfl_sync(0xffffffffu, off < 32 ? id0 : id1, off & 31);
+                f_k = k_lane + (f_id < 0 ? 0 : f_id * page_bytes + (f_pos & (page - 1)) * DIM);
+                f_new = false;
             }
-            stop = item_end;
+            // values behind the last visible position are taken as zero: a weight of zero would
+            // not hide a NaN among them
+            const int left = f_id < 0 ? 0 : hi - f_pos, key_bytes = f_id < 0 ? 0 : 16;
+            const uint8_t *const f_v = f_k + v_lane;
+            const uint32_t vdst = f_dst + kTile * DIM - (S::kValueBytes == 16 ? 0 : lane * 8);
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+                for (int i = 0; i < S::kKeyChunks; ++i) cp16(f_dst + (r * S::kKeyChunks + i) * 512, f_k + r * 8 * DIM + i * 64, key_bytes);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = (r & 1) + (r & 2) * 4;
+                const int bytes = 2 * c + t < left ? S::kValueBytes : 0;
+#pragma unroll
+                for (int i = 0; i < S::kValueChunks; ++i) {
+                    const uint32_t d = vdst + (r * S::kValueChunks + i) * 32 * S::kValueBytes;
+                    if constexpr (S::kValueBytes == 16)
+                        cp16(d, f_v + t * DIM + i * 128, bytes);
+                    else
+                        cp8(d, f_v + t * DIM + i * 128, bytes);
+                }
+            }
+            f_k += kTile * DIM;
+            f_pos += kTile;
+            f_dst = f_dst == ring_at + lane * 16 + (C::kStages - 1) * S::kTileBytes ? ring_at + lane * 16 : f_dst + S::kTileBytes;
         }
-        const int64_t pos0 = (seq.first_unit + (u - item_start)) * kUnit;
-        const int n_tiles = static_cast<int>(stop - u);  // of each warp
+        cp_commit();
+    };
 
-        // ---- rows of this block: their positions and what they see
-        const int row0 = rb * kRows;
-        const int rows = min(kRows, seq.queries * group - row0);
-        const int64_t start = seq.ctx - seq.queries;  // position of the first query
-        const int64_t p_first = start + row0 / group, p_last = start + (row0 + rows - 1) / group;
-        const int64_t hi = p_last + 1 < seq.limit ? p_last + 1 : seq.limit;
-        const int64_t lo = p.window > 0 && p_first - p.window + 1 > 0 ? p_first - p.window + 1 : 0;
-        const int64_t lo_last = p.window > 0 && p_last - p.window + 1 > 0 ? p_last - p.window + 1 : 0;
-        int64_t w0 = pos0 + static_cast<int64_t>(warp) * n_tiles * kTile;
-        int64_t w1 = w0 + static_cast<int64_t>(n_tiles) * kTile;
-        if (w0 < lo) w0 = lo / kTile * kTile;
-        if (w1 > hi) w1 = hi;
-        const int tiles = w1 > w0 ? static_cast<int>((w1 - w0 + kTile - 1) / kTile) : 0;
+    // the next segment's queries: 16 threads a row
+    constexpr int kEach = DIM / 16;
+    const int q_row = threadIdx.x / 16, q_d = threadIdx.x % 16 * kEach;
+    float qv[C::kEarly ? kEach : 1];
+    auto load_queries = [&](int nt, float *v) {
+        const int r = part.row0 + nt * 8 + q_row;
+        if (nt * 8 + q_row < part.rows) {
+            const T *src = static_cast<const T *>(p.q.p) + (part.t0 + r / group) * p.q.ts +
+                           (static_cast<int64_t>(part.h) * group + r % group) * p.q.hs + q_d;
+            if (a.q_fours) {
+#pragma unroll
+                for (int e = 0; e < kEach; e += 4) load4<T, true>(src + e, v + e);
+            } else {
+#pragma unroll
+                for (int e = 0; e < kEach; e += 4) load4<T, false>(src + e, v + e);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) v[e] = 0.0f;
+        }
+    };
 
-        // ---- pages: lane i holds page pb + i (cur) and pb + 32 + i (next), with their scales
-        const int32_t *const row_table = p.block_table + seq.b * p.width;
-        int64_t pb = w0 / page;
-        auto load_id = [&](int64_t j) -> int {
-            int id = -1;
-            if (j < p.width && j * page < hi) id = row_table[j];
-            return id < p.c.pages && id >= 0 ? id : -1;
-        };
-        int id0 = -1, id1 = -1;
-        float ka0 = 0.0f, va0 = 0.0f, ka1 = 0.0f, va1 = 0.0f;
-        if (tiles > 0) {
+    float o[S::kSteps][NT][4], m[NT][2], l[NT][2], vmax = FLT_MIN;
+    bool have = false;
+#pragma unroll 1
+    for (;;) {
+        // ---- the next segment: its rows, its page ids and its first copies, which are on their way
+        // during the join and the stores of the last one
+        const Part last = part;
+        const bool last_whole = whole, last_at_start = at_start;
+        bool more = false;
+        for (u = stop; u < u1; u = stop) {
+            int n;
+            while (u >= before + (n = heads * seq.row_blocks * seq.units)) {
+                before += n;
+                seq = sequence_of<kRows>(p, seq.b + 1, group);
+            }
+            const int item = (u - before) / seq.units;
+            part.begin = before + item * seq.units;
+            part.end = part.begin + seq.units;
+            stop = min(part.end, u1);
+            if (!split) {  // whole items, by the block that has their first unit
+                if (u > part.begin) continue;
+                stop = part.end;
+            }
+            part.h = item / seq.row_blocks;
+            part.row0 = (item - part.h * seq.row_blocks) * kRows;
+            more = true;
+            break;
+        }
+        auto begin_segment = [&]() {
+            part.t0 = seq.t0;
+            part.rows = min(kRows, seq.queries * group - part.row0);
+            whole = u == part.begin && stop == part.end;
+            at_start = u == u0;
+            const int64_t p_first = seq.start + part.row0 / group, p_last = seq.start + (part.row0 + part.rows - 1) / group;
+            hi = static_cast<int>(max(min(p_last + 1, static_cast<int64_t>(seq.limit)), static_cast<int64_t>(0)));
+            const int lo = p.window > 0 ? static_cast<int>(max(p_first - p.window + 1, static_cast<int64_t>(0))) : 0;
+            lo_last = p.window > 0 ? static_cast<int>(max(p_last - p.window + 1, static_cast<int64_t>(0))) : 0;
+            // a tile that starts in [lo_last, all_see] is seen by every row as a whole
+            all_see = static_cast<int>(min(p_first, static_cast<int64_t>(hi) - 1)) - (kTile - 1);
+            const int pos0 = (seq.first_unit + (u - part.begin)) * kUnit, each = (stop - u) * kTile;
+            w0 = pos0 + warp * each;
+            w1 = min(w0 + each, hi);
+            if (w0 < lo) w0 = lo / kTile * kTile;
+            pb = w0 >> page_log;
+            pages_end = w0 < w1 ? (hi + page - 1) >> page_log : 0;  // inside the table: hi is
             id0 = load_id(pb + lane);
             id1 = load_id(pb + 32 + lane);
-        }
-        const int first_row = static_cast<int>(w0 % page);  // of the first tile, in its page
-        const int64_t head_bytes = static_cast<int64_t>(page) * DIM;
-        auto fetch = [&](int tile) {
-            if (tile < tiles) {
-                const int row = first_row + tile * kTile, off = row / page - static_cast<int>(pb - w0 / page);
-                const int id = __shfl_sync(0xffffffffu, off < 32 ? id0 : id1, off & 31);
-                const int64_t at = (static_cast<int64_t>(id < 0 ? 0 : id) * heads + h) * head_bytes + (id < 0 ? 0 : row % page) * DIM;
-                const uint8_t *ks = static_cast<const uint8_t *>(p.c.k) + at + g * DIM + c * 16;
-                const uint8_t *vs = static_cast<const uint8_t *>(p.c.v) + at + 2 * c * DIM + g * S::kValueBytes;
-                const uint32_t dst = ring_at + tile % S::kStages * S::kTileBytes;
-                const int key_bytes = id < 0 ? 0 : 16;
+            if constexpr (C::kEarly) load_queries(0, qv);
+            k_lane = static_cast<const uint8_t *>(p.c.k) + static_cast<int64_t>(part.h) * page * DIM + g * DIM + c * 16;
+            f_pos = w0;
+            f_new = true;
+            f_dst = ring_at + lane * 16;
+#pragma unroll 1
+            for (int i = 0; i < C::kStages - 1; ++i) fetch();
+            load_scales(id0, &ka0, &va0);
+        };
+        if (C::kEarly && more) begin_segment();
+
+        if (have) {
+            // ---- sums over the lanes that share a column; value scales back into the sums
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int i = 0; i < S::kKeyChunks; ++i)
-                        cp16(dst + (r * S::kKeyChunks + i) * 512 + lane * 16, ks + r * 8 * DIM + i * 64, key_bytes);
-                // values behind the last visible position are taken as zero: a weight of
-                // zero would not hide a NaN among them
-                const int left = id < 0 ? 0 : static_cast<int>(min(hi - w0 - static_cast<int64_t>(tile) * kTile, static_cast<int64_t>(kTile)));
+                for (int j = 0; j < 2; ++j) {
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int t = 2 * c + (r & 1) + (r & 2) * 4;
+                    for (int x = 4; x < 32; x <<= 1) l[nt][j] = __fadd_rn(l[nt][j], __shfl_xor_sync(0xffffffffu, l[nt][j], x));
 #pragma unroll
-                    for (int i = 0; i < S::kValueChunks; ++i) {
-                        const uint32_t d = dst + kTile * DIM + (r * S::kValueChunks + i) * 32 * S::kValueBytes + lane * S::kValueBytes;
-                        const uint8_t *s = vs + ((r & 1) + (r & 2) * 4) * DIM + i * 128;
-                        if constexpr (S::kValueBytes == 16)
-                            cp16(d, s, t < left ? 16 : 0);
-                        else
-                            cp8(d, s, t < left ? 8 : 0);
+                    for (int st = 0; st < S::kSteps; ++st) {
+                        o[st][nt][j] = __fmul_rn(o[st][nt][j], vmax);
+                        o[st][nt][j + 2] = __fmul_rn(o[st][nt][j + 2], vmax);
+                    }
+                }
+            // ---- join the warps: 2, 3 into 0, 1, then 1 into 0, in the fragments' own layout
+#pragma unroll 1
+            for (int step = 2; step >= 1; step >>= 1) {
+                __syncthreads();
+                if (warp >= step && warp < 2 * step) {
+                    float4 *dst = reinterpret_cast<float4 *>(join + (warp - step) * C::kJoin) + lane;
+#pragma unroll
+                    for (int st = 0; st < S::kSteps; ++st)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+                            dst[(st * NT + nt) * 32] = make_float4(o[st][nt][0], o[st][nt][1], o[st][nt][2], o[st][nt][3]);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) dst[(kFrag + nt) * 32] = make_float4(m[nt][0], m[nt][1], l[nt][0], l[nt][1]);
+                }
+                __syncthreads();
+                if (warp < step) {
+                    const float4 *from = reinterpret_cast<const float4 *>(join + warp * C::kJoin) + lane;
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) {
+                        const float4 x = from[(kFrag + nt) * 32];
+                        const float om[2] = {x.x, x.y}, ol[2] = {x.z, x.w};
+                        float wa[2], wb[2];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const float top = fmaxf(m[nt][j], om[j]);
+                            wa[j] = m[nt][j] == -INFINITY ? 0.0f : ex2(m[nt][j] - top);
+                            wb[j] = om[j] == -INFINITY ? 0.0f : ex2(om[j] - top);
+                            m[nt][j] = top;
+                            l[nt][j] = __fmaf_rn(l[nt][j], wa[j], __fmul_rn(ol[j], wb[j]));
+                        }
+#pragma unroll
+                        for (int st = 0; st < S::kSteps; ++st) {
+                            const float4 y = from[(st * NT + nt) * 32];
+                            o[st][nt][0] = __fmaf_rn(o[st][nt][0], wa[0], __fmul_rn(y.x, wb[0]));
+                            o[st][nt][1] = __fmaf_rn(o[st][nt][1], wa[1], __fmul_rn(y.y, wb[1]));
+                            o[st][nt][2] = __fmaf_rn(o[st][nt][2], wa[0], __fmul_rn(y.z, wb[0]));
+                            o[st][nt][3] = __fmaf_rn(o[st][nt][3], wa[1], __fmul_rn(y.w, wb[1]));
+                        }
                     }
                 }
             }
-            cp_commit();
-        };
-        __syncthreads();  // the ring's other uses (the joins) are over
+            if (last_whole) {
+                __syncthreads();
+                if (warp == 0) {
 #pragma unroll
-        for (int i = 0; i < S::kStages - 1; ++i) fetch(i);
-        auto load_scales = [&](int id, float *ka, float *va) {
-            *ka = id < 0 ? 0.0f : p.c.k_scale[static_cast<int64_t>(id) * heads + h];
-            *va = id < 0 ? 0.0f : p.c.v_scale[static_cast<int64_t>(id) * heads + h];
-        };
-        load_scales(id0, &ka0, &va0);
-        int next_scaled = 0;
-
-        // ---- query fragments: column n = row of the block, k-step s of lane c: elements d .. d+3
-        uint32_t qf[kQShared ? 1 : kParts][kQShared ? 1 : S::kSteps][kQShared ? 1 : NT][2];
+                    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            if (kQShared && nt % kWarps != warp) continue;
-            const int r = row0 + nt * 8 + g;
-            const bool live = nt * 8 + g < rows;
-            const T *src = static_cast<const T *>(p.q.p) + (live ? (seq.t0 + r / group) * p.q.ts + (static_cast<int64_t>(h) * group + r % group) * p.q.hs : 0);
-            unsigned top = 0;
+                        for (int j = 0; j < 2; ++j) {
+                            const int col = nt * 8 + 2 * c + j;
+                            const float inv = l[nt][j] == 0.0f ? 0.0f : __fdiv_rn(1.0f, l[nt][j]);
+                            // d of (step st, lane group g): consecutive in a lane
+                            float *dst = join + col * (DIM + 4) + g * (DIM >= 128 ? 16 : 8);
 #pragma unroll
-            for (int i = 0; i < S::kKeyChunks; ++i)
+                            for (int st = 0; st < S::kSteps; ++st)
+                                *reinterpret_cast<float2 *>(dst + (DIM >= 128 ? st / 8 * 128 + st % 8 * 2 : st * 2)) =
+                                    make_float2(__fmul_rn(o[st][nt][j], inv), __fmul_rn(o[st][nt][j + 2], inv));
+                            if (g == 0) write_lse(p, last, group, col, m[nt][j], l[nt][j]);
+                        }
+                }
+                __syncthreads();
+                write_rows<T, DIM>(a, last, group, join);
+            } else if (warp == 0) {
+                // a part of an item: kept for the block that joins them. A block has at most
+                // two, one that starts with its share (slot 2j) and one that ends with it (2j + 1).
+                float *const dst = slots + (2 * static_cast<int64_t>(blockIdx.x) + !last_at_start) * C::kSlot;
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (live) top = max(top, __float_as_uint(to_float(src[i * 64 + c * 16 + e])) & 0x7fffffffu);
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // the row's largest element to [2^13, 2^14)
-            int e = static_cast<int>(top >> 23) - 127;
-            e = e < -100 ? -100 : e;
-            const float up = __uint_as_float(static_cast<unsigned>(13 - e + 127) << 23);
-            const float down = __uint_as_float(static_cast<unsigned>(e - 13 + 127) << 23);
-            if (c == 0 && (kQShared || warp == 0)) row_factor[nt * 8 + g] = __fmul_rn(down, __fmul_rn(p.scale, kLog2e));
+                for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-            for (int s = 0; s < S::kSteps; ++s) {
-                float v[4];
+                    for (int st = 0; st < S::kSteps; ++st)
+                        reinterpret_cast<float4 *>(dst)[(st * NT + nt) * 32 + lane] = make_float4(o[st][nt][0], o[st][nt][1], o[st][nt][2], o[st][nt][3]);
+                    if (g == 0) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    v[j] = live ? __fmul_rn(to_float(src[s / 4 * 64 + c * 16 + s % 4 * 4 + j]), up) : 0.0f;
-                uint32_t w[2] = {pack_half(v[0], v[1]), pack_half(v[2], v[3])};
-#pragma unroll
-                for (int part = 0; part < kParts; ++part) {
-                    if constexpr (kQShared) {
-                        q_shared[((part * S::kSteps + s) * NT + nt) * 32 + lane] = make_uint2(w[0], w[1]);
-                    } else {
-                        qf[part][s][nt][0] = w[0];
-                        qf[part][s][nt][1] = w[1];
+                        for (int j = 0; j < 2; ++j) {
+                            dst[kRows * DIM + nt * 8 + 2 * c + j] = m[nt][j];
+                            dst[kRows * DIM + kRows + nt * 8 + 2 * c + j] = l[nt][j];
+                        }
                     }
-                    const float2 x = unpack_half(w[0]), y = unpack_half(w[1]);
-                    w[0] = pack_half(v[0] - x.x, v[1] - x.y);
-                    w[1] = pack_half(v[2] - y.x, v[3] - y.y);
+                }
+                if (lane == 0) pending[n_parts] = last;
+            }
+            n_parts += !last_whole;
+        }
+        if (!more) break;
+        have = true;
+        if constexpr (!C::kEarly) {
+            __syncthreads();  // the ring is the copies' again
+            begin_segment();
+        }
+
+        // ---- queries: 16 threads a row scale it by a power of two and lay its parts out as fragments:
+        // column n = row of the block, step s of lane c: four elements from 64 (s / 4) + 16 c + 4 (s % 4)
+        {
+            const int row = q_row;
+#pragma unroll 1
+            for (int nt = 0; nt < NT; ++nt) {
+                const int r = part.row0 + nt * 8 + row;
+                const bool live = nt * 8 + row < part.rows;
+                float v[kEach];
+                if constexpr (C::kEarly) {
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) v[e] = qv[e];
+                } else {
+                    load_queries(nt, v);
+                }
+                unsigned top = 0;
+#pragma unroll
+                for (int e = 0; e < kEach; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+#pragma unroll
+                for (int x = 1; x < 16; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+                // the row's largest element to [2^13, 2^14)
+                int e2 = static_cast<int>(top >> 23) - 127;
+                e2 = e2 < -100 ? -100 : e2;
+                const float up = __uint_as_float(static_cast<unsigned>(13 - e2 + 127) << 23);
+                if (threadIdx.x % 16 == 0) {
+                    const float down = __uint_as_float(static_cast<unsigned>(e2 - 13 + 127) << 23);
+                    row_factor[nt * 8 + row] = __fmul_rn(down, __fmul_rn(p.scale, kLog2e));
+                    const int64_t at = seq.start + (live ? r : part.row0) / group;
+                    row_seen[nt * 8 + row] = make_int2(p.window > 0 ? static_cast<int>(max(at - p.window, static_cast<int64_t>(-1))) : -1,
+                                                       static_cast<int>(max(min(at, static_cast<int64_t>(hi) - 1), static_cast<int64_t>(-1))));
+                }
+#pragma unroll
+                for (int e = 0; e < kEach; e += 4) {
+                    const int d = q_d + e, step = d / 64 * 4 + d % 16 / 4, to = row * 4 + d % 64 / 16;
+                    float x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = __fmul_rn(v[e + i], up);
+#pragma unroll
+                    for (int part_i = 0; part_i < kParts; ++part_i) {
+                        const uint2 w = make_uint2(pack_half(x[0], x[1]), pack_half(x[2], x[3]));
+                        q_shared[((part_i * S::kSteps + step) * NT + nt) * 32 + to] = w;
+                        if (part_i + 1 < kParts) {
+                            const float2 y = unpack_half(w.x), z = unpack_half(w.y);
+                            x[0] -= y.x;
+                            x[1] -= y.y;
+                            x[2] -= z.x;
+                            x[3] -= z.y;
+                        }
+                    }
                 }
             }
         }
         __syncthreads();
         float factor[NT][2];
+        uint2 qf[kQShared ? 1 : kParts][kQShared ? 1 : S::kSteps][kQShared ? 1 : NT];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+            const float2 f = *reinterpret_cast<const float2 *>(row_factor + nt * 8 + 2 * c);
+            factor[nt][0] = f.x;
+            factor[nt][1] = f.y;
+            if constexpr (!kQShared) {
 #pragma unroll
-            for (int j = 0; j < 2; ++j) factor[nt][j] = row_factor[nt * 8 + 2 * c + j];
+                for (int i = 0; i < kParts; ++i)
+#pragma unroll
+                    for (int s = 0; s < S::kSteps; ++s) qf[i][s][nt] = q_shared[((i * S::kSteps + s) * NT + nt) * 32 + lane];
+            }
+        }
 
         // ---- one pass over the warp's positions
-        float o[S::kSteps][NT][4], m[NT][2], l[NT][2], vmax = FLT_MIN;
+        // raise: where the maximum goes up; less: what weights are taken relative to
+        float raise[NT][2], less[NT][2];
+        vmax = FLT_MIN;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -418,76 +625,106 @@ __global__ void __launch_bounds__(kThreads) kv_attention_kernel(const __grid_con
                 for (int j = 0; j < 4; ++j) o[s][nt][j] = 0.0f;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                m[nt][j] = -INFINITY;
-                l[nt][j] = 0.0f;
+                m[nt][j] = raise[nt][j] = -INFINITY;
+                l[nt][j] = less[nt][j] = 0.0f;
             }
         }
-        for (int tile = 0; tile < tiles; ++tile) {
-            fetch(tile + S::kStages - 1);
-            cp_wait<S::kStages - 1>();
-            const int off = (first_row + tile * kTile) / page - static_cast<int>(pb - w0 / page);
-            const int id = __shfl_sync(0xffffffffu, id0, off);
-            const float ka = __shfl_sync(0xffffffffu, ka0, off), va = __shfl_sync(0xffffffffu, va0, off);
-            if (off >= 16 && !next_scaled) {  // the ids have arrived long ago
-                load_scales(id1, &ka1, &va1);
-                next_scaled = 1;
+        float kf[NT][2], vr = 0.0f;
+        bool next_scaled = false;
+        bool page_ok = false, odd_scale = false;
+        uint32_t src = ring_at + lane * 16;
+        bool c_new = true;
+#pragma unroll 1
+        for (int pos = w0; pos < w1; pos += kTile) {
+            fetch();
+            cp_wait<C::kStages - 1>();
+            if (c_new || (pos & (page - 1)) == 0) {  // a page's first tile
+                c_new = false;
+                int off = (pos >> page_log) - pb;
+                if (off == 32) {
+                    if (!next_scaled) load_scales(id1, &ka1, &va1);
+                    next_scaled = false;
+                    pb += 32;
+                    off = 0;
+                    id0 = id1;
+                    ka0 = ka1;
+                    va0 = va1;
+                    id1 = load_id(pb + 32 + lane);
+                } else if (off >= 16 && !next_scaled) {  // the ids have arrived long ago
+                    load_scales(id1, &ka1, &va1);
+                    next_scaled = true;
+                }
+                page_ok = __shfl_sync(0xffffffffu, id0, off) >= 0;
+                const float ka = __shfl_sync(0xffffffffu, ka0, off), va = __shfl_sync(0xffffffffu, va0, off);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) kf[nt][j] = __fmul_rn(ka, factor[nt][j]);
+                odd_scale = !(fabsf(va) <= FLT_MAX);  // an infinite scale counts as NaN
+                if (!odd_scale && fabsf(va) > vmax) {  // sums relative to the largest scale so far
+                    const float r = __fdividef(vmax, fabsf(va));
+                    vmax = fabsf(va);
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int st = 0; st < S::kSteps; ++st)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) o[st][nt][j] = __fmul_rn(o[st][nt][j], r);
+                }
+                vr = odd_scale ? __int_as_float(0x7FC00000) : __fdividef(va, vmax);
             }
-            const uint32_t src = ring_at + tile % S::kStages * S::kTileBytes;
 
-            float s[NT][4];
+            float s[NT][4], s1[NT][4];  // two chains of products
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[nt][j] = 0.0f;
+                for (int j = 0; j < 4; ++j) s[nt][j] = s1[nt][j] = 0.0f;
 #pragma unroll
             for (int i = 0; i < S::kKeyChunks; ++i) {
-                const uint4 ra = lds16(src + i * 512 + lane * 16);
-                const uint4 rc = lds16(src + (S::kKeyChunks + i) * 512 + lane * 16);
+                const uint4 ra = lds16(src + i * 512);
+                const uint4 rc = lds16(src + (S::kKeyChunks + i) * 512);
                 const uint32_t x[4] = {ra.x, ra.y, ra.z, ra.w}, y[4] = {rc.x, rc.y, rc.z, rc.w};
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const uint32_t xa = prepare_codes<KV>(x[w]), ya = prepare_codes<KV>(y[w]);
                     const uint32_t frag[4] = {widen<KV, 0>(xa), widen<KV, 0>(ya), widen<KV, 1>(xa), widen<KV, 1>(ya)};
 #pragma unroll
-                    for (int part = 0; part < kParts; ++part)
+                    for (int part_i = 0; part_i < kParts; ++part_i)
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
+                            float *const to = w & 1 ? s1[nt] : s[nt];
                             if constexpr (kQShared) {
-                                const uint2 q = q_shared[((part * S::kSteps + i * 4 + w) * NT + nt) * 32 + lane];
-                                mma(s[nt], frag, q.x, q.y);
+                                const uint2 q = q_shared[((part_i * S::kSteps + i * 4 + w) * NT + nt) * 32 + lane];
+                                mma(to, frag, q.x, q.y);
                             } else {
-                                mma(s[nt], frag, qf[part][i * 4 + w][nt][0], qf[part][i * 4 + w][nt][1]);
+                                mma(to, frag, qf[part_i][i * 4 + w][nt].x, qf[part_i][i * 4 + w][nt].y);
                             }
                         }
                 }
             }
             // x = (q . c) a scale log2(e); what a row does not see becomes -infinity
-            const int64_t t0 = w0 + static_cast<int64_t>(tile) * kTile;
-            const bool inside = id >= 0 && t0 >= lo_last && t0 + kTile - 1 <= p_first && t0 + kTile <= hi;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[nt][j] = __fmul_rn(s[nt][j], __fmul_rn(ka, factor[nt][j & 1]));
-            if (!inside) {
+                for (int j = 0; j < 4; ++j) s[nt][j] = __fmul_rn(__fadd_rn(s[nt][j], s1[nt][j]), kf[nt][j & 1]);
+            if (!(page_ok && pos >= lo_last && pos <= all_see)) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt) {
+                    const int2 seen[2] = {row_seen[nt * 8 + 2 * c], row_seen[nt * 8 + 2 * c + 1]};
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        const int64_t t = t0 + g + (j & 2) * 4;
-                        const int64_t pos = start + (row0 + nt * 8 + 2 * c + (j & 1)) / group;
-                        if (id < 0 || t > pos || t >= hi || (p.window > 0 && t <= pos - p.window)) s[nt][j] = -INFINITY;
+                        const int t = pos + g + (j & 2) * 4;
+                        if (!page_ok || t <= seen[j & 1].x || t > seen[j & 1].y) s[nt][j] = -INFINITY;
                     }
+                }
             }
             // the maximum is raised only when a weight would pass the slack
             bool high = false;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) high |= s[nt][j] > m[nt][j & 1] + kSlack;
-            const bool scaled = fabsf(va) <= FLT_MAX;  // an infinite scale counts as NaN
-            if (__any_sync(0xffffffffu, high) || (scaled && fabsf(va) > vmax)) {
-                const float vnew = scaled ? fmaxf(vmax, fabsf(va)) : vmax, vr = __fdividef(vmax, vnew);
-                vmax = vnew;
+                for (int j = 0; j < 2; ++j) high |= fmaxf(s[nt][j], s[nt][j + 2]) > raise[nt][j];
+            if (__any_sync(0xffffffffu, high)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -499,45 +736,47 @@ __global__ void __launch_bounds__(kThreads) kv_attention_kernel(const __grid_con
                         const float top = fmaxf(m[nt][j], x);
                         const float r = m[nt][j] == -INFINITY ? 0.0f : ex2(m[nt][j] - top);
                         m[nt][j] = top;
+                        raise[nt][j] = top + kSlack;
+                        less[nt][j] = top == -INFINITY ? 0.0f : top - kBias;
                         l[nt][j] = __fmul_rn(l[nt][j], r);
-                        const float ro = __fmul_rn(r, vr);
 #pragma unroll
                         for (int st = 0; st < S::kSteps; ++st) {
-                            o[st][nt][j] = __fmul_rn(o[st][nt][j], ro);
-                            o[st][nt][j + 2] = __fmul_rn(o[st][nt][j + 2], ro);
+                            o[st][nt][j] = __fmul_rn(o[st][nt][j], r);
+                            o[st][nt][j + 2] = __fmul_rn(o[st][nt][j + 2], r);
                         }
                     }
             }
-            const float vr = scaled ? __fdividef(va, vmax) : __int_as_float(0x7FC00000);
-            uint32_t pf[kParts][NT][2];
+            uint32_t pf[C::kWeightParts][NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float w[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float ref = m[nt][j & 1] == -INFINITY ? 0.0f : m[nt][j & 1];
-                    const float e = ex2(__fadd_rn(__fsub_rn(s[nt][j], ref), kBias));
+                    const float e = ex2(__fsub_rn(s[nt][j], less[nt][j & 1]));
                     l[nt][j & 1] = __fadd_rn(l[nt][j & 1], e);
-                    w[j] = e == 0.0f ? 0.0f : __fmul_rn(e, vr);  // a hidden position, whatever its scale
+                    w[j] = __fmul_rn(e, vr);
+                    if (odd_scale && e == 0.0f) w[j] = 0.0f;  // hidden: its scale does not count
                 }
                 uint32_t x[2] = {pack_half(w[0], w[1]), pack_half(w[2], w[3])};
 #pragma unroll
-                for (int part = 0; part < kParts; ++part) {
-                    pf[part][nt][0] = transpose8(x[0]);
-                    pf[part][nt][1] = transpose8(x[1]);
-                    const float2 y = unpack_half(x[0]), z = unpack_half(x[1]);
-                    x[0] = pack_half(w[0] - y.x, w[1] - y.y);
-                    x[1] = pack_half(w[2] - z.x, w[3] - z.y);
+                for (int part_i = 0; part_i < C::kWeightParts; ++part_i) {
+                    pf[part_i][nt][0] = transpose8(x[0]);
+                    pf[part_i][nt][1] = transpose8(x[1]);
+                    if (part_i + 1 < C::kWeightParts) {
+                        const float2 y = unpack_half(x[0]), z = unpack_half(x[1]);
+                        x[0] = pack_half(w[0] - y.x, w[1] - y.y);
+                        x[1] = pack_half(w[2] - z.x, w[3] - z.y);
+                    }
                 }
             }
-            const uint32_t vsrc = src + kTile * DIM;
+            const uint32_t vsrc = src + kTile * DIM - (S::kValueBytes == 16 ? 0 : lane * 8);
 #pragma unroll
             for (int i = 0; i < S::kValueChunks; ++i) {
                 constexpr int kWords = S::kValueBytes / 4;
                 uint32_t v[4][kWords];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const uint32_t at = vsrc + (r * S::kValueChunks + i) * 32 * S::kValueBytes + lane * S::kValueBytes;
+                    const uint32_t at = vsrc + (r * S::kValueChunks + i) * 32 * S::kValueBytes;
                     if constexpr (kWords == 4) {
                         const uint4 x = lds16(at);
                         v[r][0] = x.x; v[r][1] = x.y; v[r][2] = x.z; v[r][3] = x.w;
@@ -557,198 +796,113 @@ __global__ void __launch_bounds__(kThreads) kv_attention_kernel(const __grid_con
                         const uint32_t frag[4] = {widen<KV, 0>(x), widen<KV, 1>(x), widen<KV, 0>(y), widen<KV, 1>(y)};
                         const int st = i * 2 * kWords + 2 * w + half;
 #pragma unroll
-                        for (int part = 0; part < kParts; ++part)
+                        for (int part_i = 0; part_i < C::kWeightParts; ++part_i)
 #pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) mma(o[st][nt], frag, pf[part][nt][0], pf[part][nt][1]);
+                            for (int nt = 0; nt < NT; ++nt) mma(o[st][nt], frag, pf[part_i][nt][0], pf[part_i][nt][1]);
                     }
                 }
             }
-            // the next tile's page may be the first of the next 32
-            if ((first_row + (tile + 1) * kTile) / page - static_cast<int>(pb - w0 / page) >= 32) {
-                if (!next_scaled) load_scales(id1, &ka1, &va1);
-                next_scaled = 0;
-                pb += 32;
-                id0 = id1;
-                ka0 = ka1;
-                va0 = va1;
-                id1 = load_id(pb + 32 + lane);
-            }
+            src = src == ring_at + lane * 16 + (C::kStages - 1) * S::kTileBytes ? ring_at + lane * 16 : src + S::kTileBytes;
         }
         cp_wait<0>();
+    }
+    if (n_parts == 0) return;
 
-        // ---- sums over the lanes that share a column; value scales back into the sums
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-#pragma unroll
-                for (int x = 4; x < 32; x <<= 1) l[nt][j] = __fadd_rn(l[nt][j], __shfl_xor_sync(0xffffffffu, l[nt][j], x));
-#pragma unroll
-                for (int st = 0; st < S::kSteps; ++st) {
-                    o[st][nt][j] = __fmul_rn(o[st][nt][j], vmax);
-                    o[st][nt][j + 2] = __fmul_rn(o[st][nt][j + 2], vmax);
-                }
-            }
-
-        // ---- join the warps: 2, 3 into 0, 1, then 1 into 0, in the fragments' own layout
-        float *const join = reinterpret_cast<float *>(smem);
-        constexpr int kJoin = kFrag * 128 + 4 * NT * 32;  // floats of one warp's state
-        static_assert(2 * kJoin * 4 <= kWarps * S::kRing, "the join fits in the ring");
-#pragma unroll
-        for (int step = 2; step >= 1; step >>= 1) {
-            __syncthreads();
-            if (warp >= step && warp < 2 * step) {
-                float *dst = join + (warp - step) * kJoin;
-#pragma unroll
-                for (int st = 0; st < S::kSteps; ++st)
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        reinterpret_cast<float4 *>(dst)[(st * NT + nt) * 32 + lane] = make_float4(o[st][nt][0], o[st][nt][1], o[st][nt][2], o[st][nt][3]);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    reinterpret_cast<float4 *>(dst)[(kFrag + nt) * 32 + lane] = make_float4(m[nt][0], m[nt][1], l[nt][0], l[nt][1]);
-            }
-            __syncthreads();
-            if (warp < step) {
-                const float4 *from = reinterpret_cast<const float4 *>(join + warp * kJoin);
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-                    const float4 x = from[(kFrag + nt) * 32 + lane];
-                    const float om[2] = {x.x, x.y}, ol[2] = {x.z, x.w};
-                    float wa[2], wb[2];
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const float top = fmaxf(m[nt][j], om[j]);
-                        wa[j] = m[nt][j] == -INFINITY ? 0.0f : ex2(m[nt][j] - top);
-                        wb[j] = om[j] == -INFINITY ? 0.0f : ex2(om[j] - top);
-                        m[nt][j] = top;
-                        l[nt][j] = __fmaf_rn(l[nt][j], wa[j], __fmul_rn(ol[j], wb[j]));
-                    }
-#pragma unroll
-                    for (int st = 0; st < S::kSteps; ++st) {
-                        const float4 y = from[(st * NT + nt) * 32 + lane];
-                        o[st][nt][0] = __fmaf_rn(o[st][nt][0], wa[0], __fmul_rn(y.x, wb[0]));
-                        o[st][nt][1] = __fmaf_rn(o[st][nt][1], wa[1], __fmul_rn(y.y, wb[1]));
-                        o[st][nt][2] = __fmaf_rn(o[st][nt][2], wa[0], __fmul_rn(y.z, wb[0]));
-                        o[st][nt][3] = __fmaf_rn(o[st][nt][3], wa[1], __fmul_rn(y.w, wb[1]));
-                    }
-                }
-            }
+    // ---- an item's parts are joined, in their order, by the block that arrives last at its counter
+    // (that of the item's first block). Nobody waits. The code runs once: it is kept short, its
+    // instructions come from memory.
+    if (warp == 0) {
+        __threadfence();
+        __syncwarp();
+        if (lane < n_parts) {
+            const int first = pending[lane].begin / per, count = (pending[lane].end - 1) / per - first;
+            const bool here = static_cast<int>(atomicAdd(counters + first, 1u)) == count;
+            if (here) counters[first] = 0;  // for the next call
+            arrived_last[lane] = here;
         }
-
-        // d of (step st, lane group g, row 0 or 8 of the tile): consecutive in a lane
-        auto dim_of = [&](int st) {
-            return DIM >= 128 ? st / 8 * 128 + g * 16 + st % 8 * 2 : g * 8 + st * 2;
-        };
-        auto write_row = [&](int col, int st, float x, float y) {  // outputs d, d + 1 of a row
-            const int r = row0 + col;
-            T *dst = static_cast<T *>(const_cast<void *>(p.out.p)) + (seq.t0 + r / group) * p.out.ts +
-                     (static_cast<int64_t>(h) * group + r % group) * p.out.hs + dim_of(st);
-            store_pair<T>(dst, x, y, a.pairs);
-        };
-        auto write_lse = [&](int col, float top, float sum) {
-            const int r = row0 + col;
-            if (p.lse)
-                p.lse[(seq.t0 + r / group) * p.q_heads + static_cast<int64_t>(h) * group + r % group] =
-                    sum == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(top - kBias, log2f(sum)), 0.6931471805599453f);
-        };
-
-        const bool whole = u == item_start && stop == item_end;
-        if (whole) {
-            if (warp == 0) {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int j = 0; j < 2; ++j) {
-                        const int col = nt * 8 + 2 * c + j;
-                        if (col >= rows) continue;
-                        const float inv = l[nt][j] == 0.0f ? 0.0f : __fdiv_rn(1.0f, l[nt][j]);
-#pragma unroll
-                        for (int st = 0; st < S::kSteps; ++st)
-                            write_row(col, st, __fmul_rn(o[st][nt][j], inv), __fmul_rn(o[st][nt][j + 2], inv));
-                        if (g == 0) write_lse(col, m[nt][j], l[nt][j]);
-                    }
-            }
-        } else {
-            // ---- a part of an item: stored; the block that arrives last joins the parts in
-            // their order. Part j of blocks first .. last is in slot 2j, or 2j + 1 where the
-            // item starts inside block j's share.
-            unsigned *const counters = static_cast<unsigned *>(p.workspace);
-            float *const slots = reinterpret_cast<float *>(static_cast<uint8_t *>(p.workspace) + kKvCounterBytes);
-            constexpr int64_t kSlot = static_cast<int64_t>(kRows) * (DIM + 2);
-            const int first = static_cast<int>(item_start / per), last = static_cast<int>((item_end - 1) / per);
-            if (warp == 0) {
-                float *dst = slots + (2 * static_cast<int64_t>(blockIdx.x) + (u > u0)) * kSlot;
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                    for (int st = 0; st < S::kSteps; ++st)
-                        reinterpret_cast<float4 *>(dst)[(st * NT + nt) * 32 + lane] = make_float4(o[st][nt][0], o[st][nt][1], o[st][nt][2], o[st][nt][3]);
-                    if (g == 0) {
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            dst[kRows * DIM + nt * 8 + 2 * c + j] = m[nt][j];
-                            dst[kRows * DIM + kRows + nt * 8 + 2 * c + j] = l[nt][j];
-                        }
-                    }
-                }
-                __threadfence();
-                __syncwarp();
-                if (lane == 0) {
-                    const int here = static_cast<int>(atomicAdd(counters + first, 1u)) == last - first;
-                    if (here) counters[first] = 0;  // for the next call
-                    is_last = here;
-                }
-            }
-            __syncthreads();
-            if (is_last) {
-                __threadfence();
-                auto slot_of = [&](int j) { return slots + (2 * static_cast<int64_t>(j) + (j == first && item_start > j * per)) * kSlot; };
-                for (int f = threadIdx.x; f < kFrag * 32; f += kThreads) {  // f % 32 == lane
-                    const int st = f / 32 / NT, nt = f / 32 % NT, col = nt * 8 + 2 * c;
-                    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f};
-                    for (int j = first; j <= last; ++j) {
-                        const float *from = slot_of(j) + kRows * DIM;
-                        top[0] = fmaxf(top[0], __ldcg(from + col));
-                        top[1] = fmaxf(top[1], __ldcg(from + col + 1));
-                    }
-                    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        __threadfence();
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < n_parts; ++i) {
+        if (!arrived_last[i]) continue;
+        const Part done = pending[i];
+        const int first = done.begin / per, n = (done.end - 1) / per - first + 1;
+        // part j of the item; the first one starts inside its block's share or with it
+        const float *const base = slots + 2 * static_cast<int64_t>(first) * C::kSlot, *const base0 = base + (done.begin > first * per) * C::kSlot;
+        auto slot_of = [&](int j) { return j == 0 ? base0 : base + 2 * static_cast<int64_t>(j) * C::kSlot; };
+        constexpr int kSets = kThreads / kRows;  // threads of a row
+        float *const part_top = reinterpret_cast<float *>(q_shared), *const part_sum = part_top + kThreads;
+        float *const weight = reinterpret_cast<float *>(smem);  // [part][row], where the ring was
+        const int row = threadIdx.x % kRows, set = threadIdx.x / kRows;
+        __syncthreads();
+        float best = -INFINITY;
 #pragma unroll 4
-                    for (int j = first; j <= last; ++j) {
-                        const float *from = slot_of(j);
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(from) + f);
-                        const float ma = __ldcg(from + kRows * DIM + col), mb = __ldcg(from + kRows * DIM + col + 1);
-                        const float la = __ldcg(from + kRows * DIM + kRows + col), lb = __ldcg(from + kRows * DIM + kRows + col + 1);
-                        const float wa = ma == -INFINITY ? 0.0f : ex2(ma - top[0]), wb = mb == -INFINITY ? 0.0f : ex2(mb - top[1]);
-                        sum[0] = __fmaf_rn(la, wa, sum[0]);
-                        sum[1] = __fmaf_rn(lb, wb, sum[1]);
-                        acc.x = __fmaf_rn(y.x, wa, acc.x);
-                        acc.y = __fmaf_rn(y.y, wb, acc.y);
-                        acc.z = __fmaf_rn(y.z, wa, acc.z);
-                        acc.w = __fmaf_rn(y.w, wb, acc.w);
-                    }
-                    const float ia = sum[0] == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum[0]), ib = sum[1] == 0.0f ? 0.0f : __fdiv_rn(1.0f, sum[1]);
-                    if (col < rows) {
-                        write_row(col, st, __fmul_rn(acc.x, ia), __fmul_rn(acc.z, ia));
-                        if (st == 0 && g == 0) write_lse(col, top[0], sum[0]);
-                    }
-                    if (col + 1 < rows) {
-                        write_row(col + 1, st, __fmul_rn(acc.y, ib), __fmul_rn(acc.w, ib));
-                        if (st == 0 && g == 0) write_lse(col + 1, top[1], sum[1]);
+        for (int j = set; j < n; j += kSets) {
+            const float mj = __ldcg(slot_of(j) + kRows * DIM + row);
+            weight[j * kRows + row] = mj;
+            best = fmaxf(best, mj);
+        }
+        part_top[threadIdx.x] = best;
+        __syncthreads();
+#pragma unroll
+        for (int s = 0; s < kSets; ++s) best = fmaxf(best, part_top[s * kRows + row]);
+        float mass = 0.0f;
+#pragma unroll 4
+        for (int j = set; j < n; j += kSets) {
+            const float mj = weight[j * kRows + row], w = mj == -INFINITY ? 0.0f : ex2(mj - best);
+            mass = __fmaf_rn(__ldcg(slot_of(j) + kRows * DIM + kRows + row), w, mass);
+            weight[j * kRows + row] = w;
+        }
+        part_sum[threadIdx.x] = mass;
+        __syncthreads();
+        mass = 0.0f;
+#pragma unroll
+        for (int s = 0; s < kSets; ++s) mass = __fadd_rn(mass, part_sum[s * kRows + row]);
+        if (set == 0) {
+            part_top[row] = mass;
+            write_lse(p, done, group, row, best, mass);
+        }
+        __syncthreads();
+        float *const stage = weight + (n * kRows + 3) / 4 * 4;
+        const int pairs = (done.rows + 1) / 2;  // of columns that are rows
+#pragma unroll 1
+        for (int i = threadIdx.x; i < S::kSteps * 8 * pairs; i += kThreads) {
+            const int pair = i % pairs, st = i / pairs / 8, gg = i / pairs % 8, col = 2 * pair;
+            const int f = (st * NT + pair / 4) * 32 + gg * 4 + pair % 4;
+            float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            constexpr int kAhead = 32;  // loads in flight: what the join waits for is their latency
+#pragma unroll 1
+            for (int j0 = 0; j0 < n; j0 += kAhead) {
+                float4 y[kAhead];
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j)
+                    if (j0 + j < n) y[j] = __ldcg(reinterpret_cast<const float4 *>(slot_of(j0 + j)) + f);
+#pragma unroll
+                for (int j = 0; j < kAhead; ++j) {
+                    if (j0 + j < n) {
+                        const float2 w = *reinterpret_cast<const float2 *>(weight + (j0 + j) * kRows + col);
+                        acc.x = __fmaf_rn(y[j].x, w.x, acc.x);
+                        acc.y = __fmaf_rn(y[j].y, w.y, acc.y);
+                        acc.z = __fmaf_rn(y[j].z, w.x, acc.z);
+                        acc.w = __fmaf_rn(y[j].w, w.y, acc.w);
                     }
                 }
             }
+            const float sa = part_top[col], sb = part_top[col + 1];
+            const float ia = sa == 0.0f ? 0.0f : __fdiv_rn(1.0f, sa), ib = sb == 0.0f ? 0.0f : __fdiv_rn(1.0f, sb);
+            float *dst = stage + col * (DIM + 4) + (DIM >= 128 ? st / 8 * 128 + gg * 16 + st % 8 * 2 : gg * 8 + st * 2);
+            *reinterpret_cast<float2 *>(dst) = make_float2(__fmul_rn(acc.x, ia), __fmul_rn(acc.z, ia));
+            *reinterpret_cast<float2 *>(dst + DIM + 4) = make_float2(__fmul_rn(acc.y, ib), __fmul_rn(acc.w, ib));
         }
-        u = stop;
+        __syncthreads();
+        write_rows<T, DIM>(a, done, group, stage);
     }
 }
 
 template <typename T, int KV, int DIM, int NT>
 cudaError_t launch(const Args &a, cudaStream_t s) {
-    using S = Shape<DIM>;
-    constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
-    constexpr bool kQShared = NT * kParts * S::kSteps > 16;
-    constexpr int kSmem = kWarps * S::kRing + (kQShared ? kParts * S::kSteps * NT * 32 * 8 : 0);
+    constexpr int kSmem = Config<T, DIM, NT>::kSmem;
     static int blocks_per_sm = 0;
     if (blocks_per_sm == 0) {
         cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<T, KV, DIM, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
@@ -763,7 +917,7 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
     const int64_t rows = p.tokens * (p.q_heads / p.c.heads);
     const __int128 units = static_cast<__int128>((p.width * p.c.page + kUnit - 1) / kUnit) * p.c.heads * (rows / (8 * NT) + p.seqs);
     int64_t grid = static_cast<int64_t>(num_sms()) * blocks_per_sm;
-    if (grid > kKvMaxBlocks) grid = kKvMaxBlocks;
+    if (grid > Config<T, DIM, NT>::kMaxBlocks) grid = Config<T, DIM, NT>::kMaxBlocks;
     if (units < grid * kMinUnits) grid = static_cast<int64_t>((units + kMinUnits - 1) / kMinUnits);
     if (grid < 1) grid = 1;
     kv_attention_kernel<T, KV, DIM, NT><<<static_cast<unsigned>(grid), kThreads, kSmem, s>>>(a);
@@ -794,8 +948,8 @@ cudaError_t by_codes(const Args &a, cudaStream_t s) {
 
 template <typename T>
 cudaError_t run_kv_attention(const KvAttentionProblem &p, cudaStream_t s) {
-    const bool pairs = reinterpret_cast<uintptr_t>(p.out.p) % (2 * sizeof(T)) == 0 && p.out.ts % 2 == 0 && p.out.hs % 2 == 0;
-    return by_codes<T>(Args{p, pairs}, s);
+    auto fours = [](const Heads &x) { return reinterpret_cast<uintptr_t>(x.p) % (4 * sizeof(T)) == 0 && x.ts % 4 == 0 && x.hs % 4 == 0; };
+    return by_codes<T>(Args{p, fours(p.out), fours(p.q)}, s);
 }
 
 }  // namespace
