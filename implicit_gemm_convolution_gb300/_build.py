@@ -24,7 +24,7 @@ LIB_PATH = os.path.join(LIB_DIR, "libom_gpu.so")
 
 SOURCES = ["om_api.cu", "simple_kernels.cu", "sgemm_tiled.cu", "conv_implicit.cu", "conv_rows.cu",
            "conv_direct.cu", "gemv.cu", "gemm_tf32x3.cu", "gemm_no_alloc.cu", "selftest.cu",
-           "decode_api.cu", "w4_matvec.cu", "kv_cache.cu", "kv_attention_f32.cu",
+           "decode_api.cu", "w4_matvec_f32.cu", "w4_matvec_f16.cu", "w4_matvec_bf16.cu", "kv_cache.cu", "kv_attention_f32.cu",
            "kv_attention_f16.cu", "kv_attention_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-fmad=false", "-Xptxas", "--fmad=false",

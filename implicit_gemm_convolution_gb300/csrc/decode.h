@@ -1,6 +1,6 @@
 // decode.h -- problems of the decoding operators (4-bit matrix-vector product,
 // paged 8-bit cache: append, attention, read back), validated by
-// decode_api.cu and run by w4_matvec.cu, kv_cache.cu and kv_attention.cuh. Not
+// decode_api.cu and run by w4_matvec.cuh, kv_cache.cu and kv_attention.cuh. Not
 // installed; not part of the public ABI.
 #pragma once
 
@@ -27,7 +27,9 @@ struct W4Problem {
     void *y;
     int64_t ldy;
 };
-cudaError_t launch_w4_matvec(const W4Problem &p, cudaStream_t s);
+cudaError_t launch_w4_matvec_f32(const W4Problem &p, cudaStream_t s);
+cudaError_t launch_w4_matvec_f16(const W4Problem &p, cudaStream_t s);
+cudaError_t launch_w4_matvec_bf16(const W4Problem &p, cudaStream_t s);
 
 // A token-major, head-strided operand: element (t, h, d) at t*ts + h*hs + d.
 struct Heads {

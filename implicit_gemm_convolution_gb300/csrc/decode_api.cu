@@ -132,12 +132,14 @@ int om_w4_matvec(int64_t m, int64_t n, int64_t k, int64_t group, const void *x, 
     if (!float_type(x_dtype) || !float_type(scale_dtype)) return OM_ERR_UNSUPPORTED;
     if (group != 32 && group != 64 && group % 128 != 0) return OM_ERR_UNSUPPORTED;
     if (m == 0 || n == 0) return OM_OK;
-    if (m > 65535 || n > kLim31 || k > kLim31 || group > kLim31) return OM_ERR_TOO_LARGE;
+    // 16 rows of weights and scales are below 2^31 bytes
+    const int64_t row_lim = int64_t(1) << 26;
+    if (m > 65535 || n > kLim31 - 256 || k > row_lim || group > kLim31) return OM_ERR_TOO_LARGE;
     const int64_t groups = (k + group - 1) / group, wb = (k + 1) / 2;
     if (ldy < n || (k > 0 && (ldx < k || ldw < wb || lds < groups || (zeros && ldz < groups)))) return OM_ERR_INVALID_ARG;
     if (!y || (k > 0 && (!x || !w || !scales))) return OM_ERR_NULL_PTR;
     const int64_t big = int64_t(1) << 40;
-    if (ldy > big || ldx > big || ldw > big || lds > big || (zeros && ldz > big)) return OM_ERR_TOO_LARGE;
+    if (ldy > big || ldx > big || ldw > row_lim || lds > row_lim / 4 || (zeros && ldz > row_lim)) return OM_ERR_TOO_LARGE;
     const int64_t xb = type_bytes(x_dtype), sb = type_bytes(scale_dtype);
     if (!aligned(y, xb) || !aligned(x, xb) || !aligned(scales, sb)) return OM_ERR_ALIGNMENT;
     const Block ry = rows_of(y, m, n, ldy, xb);
@@ -146,7 +148,9 @@ int om_w4_matvec(int64_t m, int64_t n, int64_t k, int64_t group, const void *x, 
                   (zeros && overlaps(ry, rows_of(zeros, n, groups, ldz, 1)))))
         return OM_ERR_ALIAS;
     const om::W4Problem p{m, n, k, group, x, ldx, x_dtype, w, ldw, scales, lds, scale_dtype, zeros, ldz, y, ldy};
-    return from_cuda(om::launch_w4_matvec(p, static_cast<cudaStream_t>(stream)));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (x_dtype == OM_F32) return from_cuda(om::launch_w4_matvec_f32(p, st));
+    return from_cuda(x_dtype == OM_F16 ? om::launch_w4_matvec_f16(p, st) : om::launch_w4_matvec_bf16(p, st));
 }
 
 int om_rope_table(int64_t rows, int64_t rot, double base, int scaling, double factor, double original,

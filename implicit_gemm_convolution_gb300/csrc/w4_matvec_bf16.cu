@@ -1,0 +1,6 @@
+// w4_matvec_bf16.cu -- products of a few rows with 4-bit weights, bfloat16 activations.
+#include "w4_matvec.cuh"
+
+namespace om {
+cudaError_t launch_w4_matvec_bf16(const W4Problem &p, cudaStream_t s) { return run_w4_matvec<__nv_bfloat16>(p, s); }
+}  // namespace om
