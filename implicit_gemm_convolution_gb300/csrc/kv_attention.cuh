@@ -37,6 +37,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 16;              // positions of a warp's step
 constexpr int kUnit = kTile * kWarps;  // positions of a unit of work
 constexpr int kMinUnits = 4;           // a block takes at least so many units
+constexpr int kWholeUnits = 12;        // items of no more units are not split: joining parts takes longer than that many units
 constexpr float kLog2e = 1.4426950408889634f;
 // Weights carry a factor of 2^6 and may exceed the running maximum's by 2^8 before it is
 // raised: below 2^14, inside 16-bit range, with the small ones above its subnormals.
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float row_factor[kRows];
     __shared__ int2 row_seen[kRows];  // a row sees the positions in (x, y]
-    __shared__ int scan[kWarps], found_before;
+    __shared__ int scan[kWarps], scan_longest[kWarps], found_before;
     __shared__ Sequence found;
     __shared__ Part pending[2];  // parts of items of this block: its first and its last segment's
     __shared__ int arrived_last[2];
@@ -246,19 +247,27 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
 
     // ---- this block's share of the units of all items (sequence, key head, row block)
     const int seqs = static_cast<int>(p.seqs);
-    int total = 0;
+    int total = 0, longest = 0;
 #pragma unroll 1
     for (int i = threadIdx.x; i < seqs; i += kThreads) {
         const Sequence s = sequence_of<kRows>(p, i, group);
         total += heads * s.row_blocks * s.units;
+        longest = max(longest, s.units);
     }
     total = __reduce_add_sync(0xffffffffu, total);
-    if (lane == 0) scan[warp] = total;
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 0) {
+        scan[warp] = total;
+        scan_longest[warp] = longest;
+    }
     __syncthreads();
-    total = 0;
+    total = longest = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) total += scan[w];
-    const bool split = p.workspace != nullptr;
+    for (int w = 0; w < kWarps; ++w) {
+        total += scan[w];
+        longest = max(longest, scan_longest[w]);
+    }
+    const bool split = p.workspace != nullptr && longest > kWholeUnits;
     const int per = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), kMinUnits);
     if (static_cast<int64_t>(blockIdx.x) * per >= total) return;
     const int u0 = blockIdx.x * per, u1 = min(u0 + per, total);

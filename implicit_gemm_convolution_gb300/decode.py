@@ -51,6 +51,17 @@ def _declare(L: ctypes.CDLL) -> None:
                                                     vp, ctypes.c_size_t, vp]
 
 
+_functions = None
+
+
+def _lib():
+    """The loaded library (a name of this module once loaded: the calls here are short)."""
+    global _functions
+    if _functions is None:
+        _functions = lib()
+    return _functions
+
+
 def _stream(stream, t):
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(t.get_device()) or None
@@ -71,6 +82,7 @@ def _cuda(t, name, dim, dtypes):
 
 
 _I32 = (torch.int32,)
+_int32 = torch.int32
 
 
 def w4_matvec(x, weight, scales, zeros=None, group: int = 128, out=None, stream=None):
@@ -84,32 +96,32 @@ def w4_matvec(x, weight, scales, zeros=None, group: int = 128, out=None, stream=
     _cuda(weight, "weight", 2, (torch.uint8,))
     _cuda(scales, "scales", 2, DTYPES)
     m, k = x.shape
-    n = weight.shape[0]
+    n, wb = weight.shape
     if group < 1:
         raise ValueError("group must be positive")
-    shape = (n, -(-k // group))
-    if weight.shape[1] != (k + 1) // 2 or scales.shape != shape:
+    groups = -(-k // group)
+    if wb != (k + 1) // 2 or scales.shape != (n, groups):
         raise ValueError("weight, scales and x have different sizes")
     zp, ldz = None, 0
     if zeros is not None:
         _cuda(zeros, "zeros", 2, (torch.uint8,))
-        if zeros.shape != shape:
+        if zeros.shape != (n, groups):
             raise ValueError("zeros and scales have different shapes")
-        zp, ldz = zeros.data_ptr(), zeros.stride(0) if n > 1 else shape[1]
+        zp, ldz = zeros.data_ptr(), zeros.stride(0) if n > 1 else groups
+    dtype = x.dtype
     if out is None:
-        out = torch.empty((m, n), dtype=x.dtype, device=x.device)
+        out = torch.empty((m, n), dtype=dtype, device=x.device)
+        ldy = n
     else:
-        _cuda(out, "out", 2, (x.dtype,))
+        _cuda(out, "out", 2, (dtype,))
         if out.shape != (m, n):
             raise ValueError("out has the wrong shape")
+        ldy = out.stride(0) if m > 1 else n
     if n > 1:
-        ldw, lds = weight.stride(0), scales.stride(0)
-    else:
-        ldw, lds = weight.shape[1], shape[1]
-    ldx, ldy = (x.stride(0), out.stride(0)) if m > 1 else (k, n)
-    st = lib().om_w4_matvec(m, n, k, group, x.data_ptr(), ldx, DTYPES[x.dtype], weight.data_ptr(), ldw,
-                            scales.data_ptr(), lds, DTYPES[scales.dtype], zp, ldz, out.data_ptr(), ldy,
-                            _stream(stream, x))
+        wb, groups = weight.stride(0), scales.stride(0)
+    st = _lib().om_w4_matvec(m, n, k, group, x.data_ptr(), x.stride(0) if m > 1 else k, DTYPES[dtype], weight.data_ptr(), wb,
+                             scales.data_ptr(), groups, DTYPES[scales.dtype], zp, ldz, out.data_ptr(), ldy,
+                             _stream(stream, x))
     if st:
         raise OmError(st, "om_w4_matvec")
     return out
@@ -156,21 +168,29 @@ class PagedKVCache:
 
 
 def _batch(block_table, lens, cu, lens_name):
-    _cuda(block_table, "block_table", 2, _I32)
-    _cuda(lens, lens_name, 1, _I32)
-    _cuda(cu, "cu", 1, _I32)
-    seqs, width = block_table.shape
-    if lens.shape[0] != seqs or cu.shape[0] != seqs + 1:
-        raise ValueError(f"block_table, {lens_name} and cu are of different batches")
-    if seqs > 1 and block_table.stride(0) != width:
+    """Pointers and sizes of a batch's lookups: (block_table, width, lens, cu), sequences."""
+    if not (block_table.is_cuda and lens.is_cuda and cu.is_cuda and block_table.dtype is lens.dtype is cu.dtype is _int32
+            and block_table.dim() == 2 and lens.dim() == 1 and cu.dim() == 1 and block_table.is_contiguous() and lens.is_contiguous()
+            and cu.is_contiguous()):
+        _cuda(block_table, "block_table", 2, _I32)
+        _cuda(lens, lens_name, 1, _I32)
+        _cuda(cu, "cu", 1, _I32)
         raise ValueError("block_table must be contiguous")
-    return seqs, width
+    seqs, width = block_table.shape
+    if lens.numel() != seqs or cu.numel() != seqs + 1:
+        raise ValueError(f"block_table, {lens_name} and cu are of different batches")
+    return (block_table.data_ptr(), width, lens.data_ptr(), cu.data_ptr()), seqs
 
 
-def _heads(t, name, tokens, heads, dim, dtype):
-    _cuda(t, name, 3, (dtype,))
-    if t.shape != (tokens, heads, dim):
-        raise ValueError(f"{name} must have the shape {(tokens, heads, dim)}")
+def _heads(t, name, shape, dtype):
+    """Pointer, token stride and head stride of a (tokens, heads, dim) operand."""
+    if not t.is_cuda or t.dtype is not dtype or t.shape != shape:
+        _cuda(t, name, 3, (dtype,))
+        raise ValueError(f"{name} must have the shape {tuple(shape)}")
+    ts, hs, one = t.stride()
+    if one != 1:
+        raise ValueError(f"{name} needs unit stride in its last dimension")
+    return t.data_ptr(), ts, hs
 
 
 def kv_append(cache, q, k, v, table, block_table, ctx_len, cu, max_new: int, pairs: str = "half", q_out=None,
@@ -183,31 +203,33 @@ def kv_append(cache, q, k, v, table, block_table, ctx_len, cu, max_new: int, pai
     tokens of a sequence. q_out may be q.
     """
     _cuda(k, "k", 3, DTYPES)
-    tokens, heads, dim = k.shape[0], cache.heads, cache.dim
-    _heads(k, "k", tokens, heads, dim, k.dtype)
-    _heads(v, "v", tokens, heads, dim, k.dtype)
-    seqs, width = _batch(block_table, ctx_len, cu, "ctx_len")
+    dtype, tokens, dim = k.dtype, k.shape[0], cache.dim
+    shape = (tokens, cache.heads, dim)
+    ka, va = _heads(k, "k", shape, dtype), _heads(v, "v", shape, dtype)
+    batch, seqs = _batch(block_table, ctx_len, cu, "ctx_len")
     if pairs not in ROPE_PAIRS:
         raise ValueError(f"unknown pairs {pairs!r}")
     qa, oa, q_heads = (None, 0, 0), (None, 0, 0), 0
     if q is not None:
+        if q.dim() != 3:
+            raise ValueError("q must have 3 dimensions")
         q_heads = q.shape[1]
-        _heads(q, "q", tokens, q_heads, dim, k.dtype)
+        shape = (tokens, q_heads, dim)
+        qa = _heads(q, "q", shape, dtype)
         if q_out is None:
-            q_out = torch.empty((tokens, q_heads, dim), dtype=q.dtype, device=q.device)
+            q_out = torch.empty(shape, dtype=dtype, device=q.device)
+            oa = q_out.data_ptr(), q_heads * dim, dim
         else:
-            _heads(q_out, "q_out", tokens, q_heads, dim, k.dtype)
-        qa = q.data_ptr(), q.stride(0), q.stride(1)
-        oa = q_out.data_ptr(), q_out.stride(0), q_out.stride(1)
+            oa = _heads(q_out, "q_out", shape, dtype)
     tp, rows, rot = None, 0, 0
     if table is not None:
         _cuda(table, "table", 3, (torch.float32,))
-        if table.shape[2] != 2 or not table.is_contiguous():
+        rows, rot, two = table.shape
+        if two != 2 or not table.is_contiguous():
             raise ValueError("table must be a contiguous (rows, rot // 2, 2) tensor")
-        tp, rows, rot = table.data_ptr(), table.shape[0], 2 * table.shape[1]
-    st = lib().om_kv_append(cache._ref, seqs, tokens, max_new, q_heads, *qa, k.data_ptr(), k.stride(0), k.stride(1),
-                            v.data_ptr(), v.stride(0), v.stride(1), DTYPES[k.dtype], tp, rows, rot, ROPE_PAIRS[pairs],
-                            block_table.data_ptr(), width, ctx_len.data_ptr(), cu.data_ptr(), *oa, _stream(stream, k))
+        tp, rot = table.data_ptr(), 2 * rot
+    st = _lib().om_kv_append(cache._ref, seqs, tokens, max_new, q_heads, *qa, *ka, *va, DTYPES[dtype], tp, rows, rot, ROPE_PAIRS[pairs],
+                             *batch, *oa, _stream(stream, k))
     if st:
         raise OmError(st, "om_kv_append")
     return q_out
@@ -217,26 +239,27 @@ def kv_read(cache, block_table, start, cu, max_tokens: int, tokens: int, dtype=t
             stream=None):
     """Reads `tokens` tokens back as values: token i of sequence b is position
     start[b] + i. Returns keys and values, (tokens, heads, dim) of dtype."""
-    seqs, width = _batch(block_table, start, cu, "start")
+    batch, seqs = _batch(block_table, start, cu, "start")
     if dtype not in DTYPES:
         raise TypeError("dtype must be float32, float16 or bfloat16")
     if tokens < 0 or max_tokens < 0:
         raise ValueError("tokens and max_tokens must not be negative")
     shape = (tokens, cache.heads, cache.dim)
-    outs = []
-    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-        if t is None:
-            t = torch.empty(shape, dtype=dtype, device=block_table.device)
-        else:
-            _heads(t, name, *shape, dtype)
-            if not t.is_contiguous():
-                raise ValueError(f"{name} must be contiguous")
-        outs.append(t)
-    st = lib().om_kv_read(cache._ref, seqs, tokens, block_table.data_ptr(), width, start.data_ptr(), cu.data_ptr(),
-                          outs[0].data_ptr(), outs[1].data_ptr(), DTYPES[dtype], _stream(stream, block_table))
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=block_table.device)
+    else:
+        _heads(k_out, "k_out", shape, dtype)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=block_table.device)
+    else:
+        _heads(v_out, "v_out", shape, dtype)
+    if not (k_out.is_contiguous() and v_out.is_contiguous()):
+        raise ValueError("k_out and v_out must be contiguous")
+    st = _lib().om_kv_read(cache._ref, seqs, tokens, *batch, k_out.data_ptr(), v_out.data_ptr(), DTYPES[dtype],
+                           _stream(stream, block_table))
     if st:
         raise OmError(st, "om_kv_read")
-    return outs[0], outs[1]
+    return k_out, v_out
 
 
 def new_kv_workspace(cache, q_heads: int, max_new: int):
@@ -258,14 +281,17 @@ def kv_attention(cache, q, block_table, ctx_len, cu, max_new: int, scale=None, w
     and head is one block's work. Returns (tokens, q heads, dim) of q's type.
     """
     _cuda(q, "q", 3, DTYPES)
-    tokens, q_heads, dim = q.shape
+    dtype, shape = q.dtype, q.shape
+    tokens, q_heads, dim = shape
     if dim != cache.dim:
         raise ValueError("q and the cache have different head dimensions")
-    seqs, width = _batch(block_table, ctx_len, cu, "ctx_len")
+    ts, hs, _ = q.stride()
+    batch, seqs = _batch(block_table, ctx_len, cu, "ctx_len")
     if out is None:
-        out = torch.empty((tokens, q_heads, dim), dtype=q.dtype, device=q.device)
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+        oa = out.data_ptr(), q_heads * dim, dim
     else:
-        _heads(out, "out", tokens, q_heads, dim, q.dtype)
+        oa = _heads(out, "out", shape, dtype)
     lp = None
     if lse is not None:
         _cuda(lse, "lse", 2, (torch.float32,))
@@ -275,10 +301,8 @@ def kv_attention(cache, q, block_table, ctx_len, cu, max_new: int, scale=None, w
     ws, ws_bytes = None, 0
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    st = lib().om_kv_attention(cache._ref, seqs, tokens, max_new, q_heads, q.data_ptr(), q.stride(0), q.stride(1),
-                               DTYPES[q.dtype], block_table.data_ptr(), width, ctx_len.data_ptr(), cu.data_ptr(),
-                               dim ** -0.5 if scale is None else scale, window, out.data_ptr(), out.stride(0),
-                               out.stride(1), lp, ws, ws_bytes, _stream(stream, q))
+    st = _lib().om_kv_attention(cache._ref, seqs, tokens, max_new, q_heads, q.data_ptr(), ts, hs, DTYPES[dtype], *batch,
+                                dim ** -0.5 if scale is None else scale, window, *oa, lp, ws, ws_bytes, _stream(stream, q))
     if st:
         raise OmError(st, "om_kv_attention")
     return out
