@@ -45,7 +45,9 @@ struct Config {
     static constexpr int kScaleAt = kRowTile * kRowPieces * 16, kZeroAt = kScaleAt + kRowTile * kScaleWords * 4;
     static constexpr int kStages = NT == 1 ? 3 : 2;
     static constexpr int kStage = kZeroAt + kRowTile * kZeroWords * 4;
+    static_assert(kStage % 128 == 0, "places of words in a stage are whole multiples of 128 bytes apart");
     static constexpr int kRing = kStages * kStage;                 // of one warp
+    static constexpr int kJoinWarps = kTokens;                     // that join a tile's sums: two lanes an output
     static constexpr int kJoins = NT == 1 ? 2 : 1;                 // buffers of the sums of all warps
     static constexpr int kJoin = kJoins * kWarps * NT * 32 * 16;
     static constexpr int kAcc = kMaxTiles * kRowTile * kTokens * 4;
@@ -107,7 +109,7 @@ struct Args {
     int slab;      // units whose x a block holds at once
     int wide;      // a group's halves of a unit (128 codes), for groups of 128 codes and more
     int split;     // warps that share 16 rows: 4, 8 or 16
-    bool x_vector;  // rows of x are aligned for 16-byte loads
+    int x_bytes;   // alignment of the rows of x: 16, 4 or 2 bytes
 };
 
 // The exponent that scales a row whose largest magnitude has these bits.
@@ -128,6 +130,25 @@ __device__ __forceinline__ void split3(float x, uint16_t *part) {
     part[0] = static_cast<uint16_t>(b >> 16);
     part[1] = static_cast<uint16_t>(b1 >> 16);
     part[2] = static_cast<uint16_t>(__float_as_uint(r2) >> 16);
+}
+
+// The first `valid` of eight elements as they lie in memory, zeros behind them.
+template <typename T>
+__device__ __noinline__ void load_part(const T *src, int valid, uint32_t *raw) {
+    uint32_t v[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        v[e] = 0;
+        if (e < valid) {
+            if constexpr (sizeof(T) == 4) v[e] = __float_as_uint(src[e]);
+            else v[e] = reinterpret_cast<const uint16_t *>(src)[e];
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        if constexpr (sizeof(T) == 4) raw[e] = v[e];
+        else if (e % 2 == 0) raw[e / 2] = v[e] | v[e + 1] << 16;
+    }
 }
 
 template <typename T, int NT, int GB, bool ALIGNED>
@@ -284,112 +305,132 @@ __global__ void __launch_bounds__(kThreads, 1) w4_matvec_kernel(const __grid_con
             const bool fresh = pass == t_begin || a.units > a.slab;  // x has to be laid out
             __syncthreads();  // the last slab's x has been used
             if (kWhole && fresh && threadIdx.x < C::kTokens) row_top[threadIdx.x] = 0;
-#pragma unroll 1
-            for (int i = 0; i < C::kStages; ++i) fetch();
 
-            // ---- x: eight consecutive elements in the order of a word's codes, zero behind k
-            if (fresh) {
-                const int pieces = slab_units * (kUnit / 8), count = pieces * tokens;  // pieces is a multiple of 16
-                auto load8 = [&](int i, float *v) {
-                    const int tok = i / pieces, k0 = slab * kUnit + (i - tok * pieces) * 8;
-                    const T *src = x + tok * p.ldx + k0;
-                    if (a.x_vector && k0 + 8 <= k) {
-                        load4<T, true>(src, v);
-                        load4<T, true>(src + 4, v + 4);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) v[e] = k0 + e < k ? to_float(src[e]) : 0.0f;
-                    }
-                };
-                if constexpr (kWhole) {  // a row's largest element sets its power of two: no part of x is lost at the ends of the range
-                    __syncthreads();
-#pragma unroll 1
-                    for (int i = threadIdx.x; i < count; i += kThreads) {
-                        float v[8];
-                        load8(i, v);
-                        unsigned top = 0;
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
-                        top = __reduce_max_sync(0xffffu << (lane & 16), top);
-                        if ((lane & 15) == 0) atomicMax(&row_top[i / pieces], top);
-                    }
-                    __syncthreads();
-                }
-#pragma unroll 1
-                for (int i = threadIdx.x; i < count; i += kThreads) {
-                    const int tok = i / pieces, piece = i - tok * pieces;
-                    float v[8];
-                    load8(i, v);
-                    uint8_t *dst = xs + tok * C::kParts * x_stride + piece * 16;
-                    if constexpr (kWhole) {
-                        const float up = ldexpf(1.0f, 1 - exponent(row_top[tok]));
-                        uint16_t parts[8][3];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) split3(v[e] * up, parts[e]);
-#pragma unroll
-                        for (int j = 0; j < 3; ++j) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) w[e] = parts[e][j] | static_cast<uint32_t>(parts[e + 4][j]) << 16;
-                            *reinterpret_cast<uint4 *>(dst + j * x_stride) = make_uint4(w[0], w[1], w[2], w[3]);
-                        }
-                    } else {
-                        uint32_t w[4];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const T pair[2] = {from_float<T>(v[e]), from_float<T>(v[e + 4])};
-                            memcpy(&w[e], pair, 4);
-                        }
-                        *reinterpret_cast<uint4 *>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-                    }
-                }
-            }
-            __syncthreads();
-
-            // ---- units
+            // One loop runs the copies ahead, then x once they are on their way, then unit after unit:
+            // its code comes from memory, and a block runs little more than it once.
             uint32_t mask, magic;  // in registers: an instruction takes one constant
             asm volatile("mov.b32 %0, 0x000f000f;\n\tmov.b32 %1, %2;" : "=r"(mask), "=r"(magic) : "n"(kMagic));
             const uint8_t *x_lane[NT];  // of x: the columns behind the last one repeat it
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) x_lane[nt] = xs + min(nt * 8 + g, cols - 1) * x_stride + c * 16;
-            int stage = 0;
-#pragma unroll 1
-            for (int tile = team; tile < pass_tiles; tile += teams) {
-                float total[NT][4];
+            int tile = team, unit_i = 0, stage = 0;
+            float total[NT][4];
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) total[nt][j] = 0.0f;
+                for (int j = 0; j < 4; ++j) total[nt][j] = 0.0f;
 #pragma unroll 1
-                for (int i = 0; i < mine; ++i) {
-                    const int unit = part + i * a.split;  // of the slab
+            for (int step = -C::kStages; step < 0 || tile < pass_tiles; ++step) {
+            if (step < 0) {
+                fetch();
+                if (step < -1) continue;
+                // ---- x: eight consecutive elements in the order of a word's codes, zero behind k; a thread takes
+                // some such pieces at a time, whose loads are in flight together. For 32-bit x once before that: a row's
+                // largest element sets its power of two, so that no part of x is lost at the ends of the range.
+                if (fresh) {
+                    constexpr int kBatch = kWhole ? 2 : 4, kRaw = kWhole ? 8 : 4;
+                    const int pieces = slab_units * (kUnit / 8), count = pieces * tokens;  // pieces is a multiple of 32
+                    uint32_t raw[kBatch][kRaw];
+                    if (kWhole) __syncthreads();
+#pragma unroll 1
+                    for (int base = 0, look = kWhole; base < count; base += kBatch * kThreads) {
+                        if (!kWhole || look || count > kBatch * kThreads) {  // else they are still there
+#pragma unroll
+                            for (int j = 0; j < kBatch; ++j) {
+                                const int i = base + j * kThreads + threadIdx.x, tok = i / pieces, k0 = slab * kUnit + (i - tok * pieces) * 8;
+                                const T *src = x + tok * p.ldx + k0;
+                                if (i < count && k0 + 8 <= k && a.x_bytes == 16) {
+#pragma unroll
+                                    for (int e = 0; e < kRaw; e += 4) {
+                                        const uint4 v = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint32_t *>(src) + e);
+                                        raw[j][e] = v.x;
+                                        raw[j][e + 1] = v.y;
+                                        raw[j][e + 2] = v.z;
+                                        raw[j][e + 3] = v.w;
+                                    }
+                                } else if (i < count && k0 + 8 <= k && a.x_bytes >= 4) {
+#pragma unroll
+                                    for (int e = 0; e < kRaw; ++e) raw[j][e] = reinterpret_cast<const uint32_t *>(src)[e];
+                                } else if (i >= count || k0 >= k) {
+#pragma unroll
+                                    for (int e = 0; e < kRaw; ++e) raw[j][e] = 0;
+                                } else {
+                                    uint32_t part_of[kRaw];
+                                    load_part<T>(src, k - k0, part_of);
+#pragma unroll
+                                    for (int e = 0; e < kRaw; ++e) raw[j][e] = part_of[e];
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < kBatch; ++j) {
+                            const int i = base + j * kThreads + threadIdx.x;
+                            if (i >= count) break;
+                            const int tok = i / pieces;
+                            uint8_t *dst = xs + tok * C::kParts * x_stride + (i - tok * pieces) * 16;
+                            if constexpr (kWhole) {
+                                if (look) {
+                                    unsigned top = 0;
+#pragma unroll
+                                    for (int e = 0; e < 8; ++e) top = max(top, raw[j][e] & 0x7fffffffu);
+                                    top = __reduce_max_sync(0xffffffffu, top);
+                                    if (lane == 0) atomicMax(&row_top[tok], top);
+                                } else {
+                                    const float up = __uint_as_float(static_cast<unsigned>(128 - exponent(row_top[tok])) << 23);
+                                    uint32_t w[3][4];
+#pragma unroll
+                                    for (int e = 0; e < 4; ++e) {
+                                        uint16_t lo[3], hi[3];
+                                        split3(__uint_as_float(raw[j][e]) * up, lo);
+                                        split3(__uint_as_float(raw[j][e + 4]) * up, hi);
+#pragma unroll
+                                        for (int q = 0; q < 3; ++q) w[q][e] = lo[q] | static_cast<uint32_t>(hi[q]) << 16;
+                                    }
+#pragma unroll
+                                    for (int q = 0; q < 3; ++q) *reinterpret_cast<uint4 *>(dst + q * x_stride) = make_uint4(w[q][0], w[q][1], w[q][2], w[q][3]);
+                                }
+                            } else {
+                                *reinterpret_cast<uint4 *>(dst) = make_uint4(__byte_perm(raw[j][0], raw[j][2], 0x5410), __byte_perm(raw[j][0], raw[j][2], 0x7632),
+                                                                             __byte_perm(raw[j][1], raw[j][3], 0x5410), __byte_perm(raw[j][1], raw[j][3], 0x7632));
+                            }
+                        }
+                        if (look && base + kBatch * kThreads >= count) {
+                            look = 0;
+                            base = -kBatch * kThreads;
+                            __syncthreads();
+                        }
+                    }
+                }
+                __syncthreads();
+                continue;
+            }
+                // ---- a unit
+                if (mine > 0) {
+                    const int unit = part + unit_i * a.split;  // of the slab
                     asm volatile("cp.async.wait_group %0;" ::"n"(C::kStages - 1) : "memory");
                     __syncwarp();
-                    const uint32_t src = ring + stage * C::kStage;
+                    const uint8_t *const held = smem + warp * C::kRing + stage * C::kStage;
                     const int grp = group_of(slab + unit);
                     // lane c has the scales and zero points of groups c and c + 4 of rows g and g + 8
                     constexpr int kHeld = kGroups == 8 ? 2 : 1;
-                    uint32_t held_s[kHeld][2], held_z[kHeld];
+                    float held_s[kHeld][2];
+                    uint32_t held_z[kHeld];
 #pragma unroll
                     for (int j = 0; j < kHeld; ++j) {
-                        const int mine_j = min(c, kGroups - 1) + 4 * j;
+                        const int of = min(c, kGroups - 1) + 4 * j;
                         uint32_t z[2] = {8, 8};
 #pragma unroll
                         for (int r = 0; r < 2; ++r) {
-                            const uint32_t at = src + C::kScaleAt + (g + 8 * r) * (C::kScaleWords * 4) + ((s_row[r] + grp * scale_bytes) & 3) + mine_j * scale_bytes;
-                            if (scale_bytes == 4) {
-                                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(held_s[j][r]) : "r"(at) : "memory");
-                            } else {
-                                asm volatile("{\n\t.reg .u16 h;\n\tld.shared.u16 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(held_s[j][r]) : "r"(at) : "memory");
-                                held_s[j][r] = p.s_dtype == OM_F16 ? __float_as_uint(__half2float(__ushort_as_half(static_cast<uint16_t>(held_s[j][r])))) : held_s[j][r] << 16;
-                            }
-                            if (p.z) {
-                                const uint32_t zat = src + C::kZeroAt + (g + 8 * r) * (C::kZeroWords * 4) + ((z_row[r] + grp) & 3) + mine_j;
-                                asm volatile("{\n\t.reg .u16 h;\n\tld.shared.u8 h, [%1];\n\tcvt.u32.u16 %0, h;\n\t}" : "=r"(z[r]) : "r"(zat) : "memory");
-                            }
+                            const uint8_t *const at = held + C::kScaleAt + (g + 8 * r) * (C::kScaleWords * 4) + ((s_row[r] + grp * scale_bytes) & 3) + of * scale_bytes;
+                            if (scale_bytes == 4) held_s[j][r] = *reinterpret_cast<const float *>(at);
+                            else if (p.s_dtype == OM_F16) held_s[j][r] = __half2float(*reinterpret_cast<const __half *>(at));
+                            else held_s[j][r] = __uint_as_float(static_cast<uint32_t>(*reinterpret_cast<const uint16_t *>(at)) << 16);
+                            if (p.z) z[r] = held[C::kZeroAt + (g + 8 * r) * (C::kZeroWords * 4) + ((z_row[r] + grp) & 3) + of];
                         }
                         held_z[j] = kMagic | z[0] | z[1] << 16;
                     }
+                    // ALIGNED: the word of block 0; stages are whole multiples of 128 bytes
+                    const uint32_t w_lane = ALIGNED ? g * 128 + (g & 7) * 16 + c * 4 : g * 144 + c * 4;
                     float acc[NT][4];
                     uint32_t off0 = 0, off1 = 0;
                     float s0 = 0.0f, s1 = 0.0f;
@@ -400,26 +441,23 @@ __global__ void __launch_bounds__(kThreads, 1) w4_matvec_kernel(const __grid_con
                             if (GB == 4 && a.wide > 1 && b == 4)  // a wide group: the same one, or the next
                                 j = static_cast<int>(static_cast<unsigned>((slab + unit) * 2 + 1) / static_cast<unsigned>(a.wide)) - grp;
                             const int from = (lane & ~3) + j % 4;
-                            s0 = __uint_as_float(__shfl_sync(0xffffffffu, held_s[b / GB / 4][0], from));
-                            s1 = __uint_as_float(__shfl_sync(0xffffffffu, held_s[b / GB / 4][1], from));
+                            s0 = __shfl_sync(0xffffffffu, held_s[b / GB / 4][0], from);
+                            s1 = __shfl_sync(0xffffffffu, held_s[b / GB / 4][1], from);
                             const uint32_t z = p.z ? __shfl_sync(0xffffffffu, held_z[b / GB / 4], from) : kMagic | 0x00080008u;
                             off0 = __byte_perm(z, 0, 0x1010);
                             off1 = __byte_perm(z, 0, 0x3232);
                         }
                         uint32_t w0, w1;
                         if constexpr (ALIGNED) {
-                            const uint32_t at = src + g * 128 + (((b ^ g) & 7) * 16) + c * 4;
-                            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w0) : "r"(at) : "memory");
-                            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w1) : "r"(at + 1024) : "memory");  // (g + 8) ^ b: the same place
+                            const uint8_t *const at = held + (w_lane ^ (b * 16));
+                            w0 = *reinterpret_cast<const uint32_t *>(at);
+                            w1 = *reinterpret_cast<const uint32_t *>(at + 1024);  // (g + 8) ^ b: the same place
                         } else {
-                            auto word = [&](uint32_t at, int off) {
-                                uint32_t lo, hi;
-                                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(lo) : "r"(at + (off & ~3)) : "memory");
-                                asm volatile("ld.shared.u32 %0, [%1];" : "=r"(hi) : "r"(at + ((off + 3) & ~3)) : "memory");
-                                return __funnelshift_r(lo, hi, off * 8);
+                            auto word = [&](const uint8_t *at, int off) {
+                                return __funnelshift_r(*reinterpret_cast<const uint32_t *>(at + (off & ~3)), *reinterpret_cast<const uint32_t *>(at + ((off + 3) & ~3)), off * 8);
                             };
-                            w0 = word(src + g * 144 + c * 4 + b * 16, skew[0]);
-                            w1 = word(src + g * 144 + c * 4 + b * 16 + 8 * 144, skew[1]);
+                            w0 = word(held + w_lane + b * 16, skew[0]);
+                            w1 = word(held + w_lane + b * 16 + 8 * 144, skew[1]);
                         }
                         uint32_t f[2][4] = {{widen<0>(w0, mask, magic), widen<0>(w1, mask, magic), widen<1>(w0, mask, magic), widen<1>(w1, mask, magic)},
                                             {widen<2>(w0, mask, magic), widen<2>(w1, mask, magic), widen<3>(w0, mask, magic), widen<3>(w1, mask, magic)}};
@@ -446,6 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_matvec_kernel(const __grid_con
                     __syncwarp();  // the stage has been read by every lane
                     fetch();
                     stage = stage == C::kStages - 1 ? 0 : stage + 1;
+                    if (++unit_i < mine) continue;
+                    unit_i = 0;
                 }
                 // ---- the team's sums of the tile
                 if constexpr (C::kJoins == 1) team_barrier();  // the last tile's sums have been read
@@ -454,18 +494,27 @@ __global__ void __launch_bounds__(kThreads, 1) w4_matvec_kernel(const __grid_con
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) sums[(warp * NT + nt) * 32 + lane] = make_float4(total[nt][0], total[nt][1], total[nt][2], total[nt][3]);
                 team_barrier();
-                for (int id = part * 32 + lane; id < kRowTile * tokens; id += a.split * 32) {
-                    const int r = id % kRowTile, tok = id / kRowTile;
+                // two lanes an output, each half of the warps; the joining warps take turns
+                int first = part - turn * C::kJoinWarps;
+                first = (first % a.split + a.split) % a.split;
+                for (int id = first * 32 + lane; id < 2 * kRowTile * tokens; id += a.split * 32) {
+                    const int r = id % kRowTile, half = id / kRowTile % 2, tok = id / (2 * kRowTile);
                     float sum = 0.0f;
 #pragma unroll
                     for (int j = 0; j < C::kParts; ++j) {
                         const int cc = tok * C::kParts + j;
                         const float *from = reinterpret_cast<const float *>(sums + team * a.split * NT * 32 + (cc / 8) * 32 + (r % 8) * 4 + cc % 8 / 2) + (cc & 1) + (r / 8) * 2;
-#pragma unroll 4
-                        for (int w = 0; w < a.split; ++w) sum += from[w * NT * 128];
+#pragma unroll
+                        for (int w = 0; w < 8; ++w)
+                            if (w < a.split / 2) sum += from[(half * (a.split / 2) + w) * NT * 128];
                     }
+                    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                    if (half) continue;
                     sum *= 1.0f / kCode;
-                    if constexpr (kWhole) sum *= ldexpf(1.0f, exponent(row_top[tok]) - 1);
+                    if constexpr (kWhole) {  // 2^(e - 1): e can be -126
+                        const int e = exponent(row_top[tok]);
+                        sum *= e > -126 ? __uint_as_float(static_cast<unsigned>(e + 126) << 23) : __uint_as_float(0x00400000u);
+                    }
                     // the rows' sums of earlier slabs
                     float *const kept = acc_rows + (tile * C::kTokens + tok) * kRowTile + r;
                     if (slab > 0) sum += *kept;
@@ -476,6 +525,11 @@ __global__ void __launch_bounds__(kThreads, 1) w4_matvec_kernel(const __grid_con
                         if (row < n) y[tok * p.ldy + row] = from_float<T>(sum);
                     }
                 }
+                tile += teams;
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) total[nt][j] = 0.0f;
             }
             asm volatile("cp.async.wait_group 0;" ::: "memory");
         }
@@ -544,7 +598,8 @@ cudaError_t run_w4_matvec(const W4Problem &p, cudaStream_t s) {
     a.tiles = static_cast<int>((p.n + kRowTile - 1) / kRowTile);
     a.units = static_cast<int>((p.k + kUnit - 1) / kUnit);
     a.wide = p.group >= 128 ? static_cast<int>(p.group / 128) : 1;
-    a.x_vector = reinterpret_cast<uintptr_t>(p.x) % 16 == 0 && (p.m == 1 || p.ldx * sizeof(T) % 16 == 0);
+    const uintptr_t x_low = reinterpret_cast<uintptr_t>(p.x) | (p.m == 1 ? 0 : static_cast<uintptr_t>(p.ldx) * sizeof(T));
+    a.x_bytes = x_low % 16 == 0 ? 16 : (x_low % 4 == 0 ? 4 : 2);
     constexpr int kParts = std::is_same_v<T, float> ? 3 : 1;
     if (p.m <= 8 / kParts) return by_group<T, 1>(a, s);
     return by_group<T, 2>(a, s);
