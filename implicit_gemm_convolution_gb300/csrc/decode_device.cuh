@@ -68,29 +68,39 @@ __device__ __forceinline__ void store4(T *p, const float *v) {
 }
 
 // Codes. OM_I8: whole numbers -127 .. 127; OM_E4M3: 8-bit floats up to 448.
+// The nearest codes of four finite values, ties to even, clamped to the range; byte i is value i's.
 template <int KV>
-__device__ __forceinline__ float code_top() {
-    return KV == OM_I8 ? 127.0f : 448.0f;
-}
-
-// The nearest code of a finite value, ties to even, clamped to the range.
-template <int KV>
-__device__ __forceinline__ uint32_t encode(float x) {
-    x = fminf(fmaxf(x, -code_top<KV>()), code_top<KV>());
+__device__ __forceinline__ uint32_t encode4(float x, float y, float z, float w) {
     if constexpr (KV == OM_I8) {
-        return static_cast<uint32_t>(__float2int_rn(x)) & 0xffu;
+        // adding 1.5 * 2^23 rounds to a whole number, whose low byte is the code
+        auto code = [](float v) { return __float_as_uint(__fadd_rn(fminf(fmaxf(v, -127.0f), 127.0f), 12582912.0f)); };
+        return __byte_perm(__byte_perm(code(x), code(y), 0x0040), __byte_perm(code(z), code(w), 0x0040), 0x5410);
     } else {
-        return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(z, w), __NV_SATFINITE, __NV_E4M3);
+        return lo | hi << 16;
     }
 }
 
+// The values of a word's four codes.
 template <int KV>
-__device__ __forceinline__ float decode(uint32_t byte) {
+__device__ __forceinline__ void decode4(uint32_t w, float *v) {
     if constexpr (KV == OM_I8) {
-        return static_cast<float>(static_cast<int8_t>(byte & 0xffu));
+        // 2^23 + (code + 128), by its bits, less 2^23 + 128: exact
+        w ^= 0x80808080u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = __fsub_rn(__uint_as_float(__byte_perm(w, 0x4b000000u, 0x7650 + i)), 8388736.0f);
     } else {
-        const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<__nv_fp8_storage_t>(byte & 0xffu), __NV_E4M3);
-        return __half2float(__half(h));
+        uint32_t h[2];
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}" : "=r"(h[0]), "=r"(h[1]) : "r"(w));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            __half2 x;
+            memcpy(&x, &h[i], 4);
+            const float2 f = __half22float2(x);
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
+        }
     }
 }
 
@@ -101,18 +111,6 @@ __device__ __forceinline__ void token_range(const int32_t *cu, int64_t b, int64_
     const int64_t a = cu[b], e = cu[b + 1];
     *lo = a < 0 ? 0 : (a > tokens ? tokens : a);
     *hi = e < *lo ? *lo : (e > tokens ? tokens : e);
-}
-
-// The sequence that token t belongs to, or seqs when none does; every thread of
-// the block takes part. The count of sequences that end at or before t: one
-// round of loads for up to blockDim.x sequences.
-__device__ __forceinline__ int64_t block_sequence_of(const int32_t *cu, int64_t seqs, int64_t t) {
-    int64_t b = 0;
-    for (int64_t i = 0; i < seqs; i += blockDim.x) {
-        const int64_t j = i + threadIdx.x;
-        b += __syncthreads_count(j < seqs && cu[j + 1] <= t);
-    }
-    return b;
 }
 
 }  // namespace om

@@ -29,13 +29,8 @@ __device__ __forceinline__ int unit_offset(int u, int rot, bool interleaved, int
     return 8 * u;
 }
 
-// Rotates the four pairs of unit u by the table row of position pos:
-// (a, b) -> (a c - b s, b c + a s), every product and sum rounded. Positions
-// the table does not hold give NaN.
-__device__ __forceinline__ void rotate_unit(float *v, const float *table, int64_t rows, int rot,
-                                            bool interleaved, int64_t pos, int u) {
-    if (8 * u >= rot) return;
-    float cs[8];
+// The table's cos and sin of unit u's four pairs at position pos; NaN for positions the table does not hold.
+__device__ __forceinline__ void load_turn(float *cs, const float *table, int64_t rows, int rot, int64_t pos, int u) {
     if (pos >= 0 && pos < rows) {
         const float4 *t = reinterpret_cast<const float4 *>(table + pos * rot + 8 * u);
         const float4 lo = __ldg(t), hi = __ldg(t + 1);
@@ -45,20 +40,30 @@ __device__ __forceinline__ void rotate_unit(float *v, const float *table, int64_
 #pragma unroll
         for (int i = 0; i < 8; ++i) cs[i] = __int_as_float(0x7FC00000);
     }
+}
+
+__device__ __forceinline__ void turn_pair(float &a, float &b, float c, float s) {
+    const float x = a, y = b;
+    a = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
+    b = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
+}
+
+// Turns the four pairs of a unit: (a, b) -> (a c - b s, b c + a s), every product and sum rounded.
+__device__ __forceinline__ void turn(float *v, const float *cs, bool interleaved) {
+    if (interleaved) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float &a = interleaved ? v[2 * i] : v[i];
-        float &b = interleaved ? v[2 * i + 1] : v[4 + i];
-        const float c = cs[2 * i], s = cs[2 * i + 1], x = a, y = b;
-        a = __fsub_rn(__fmul_rn(x, c), __fmul_rn(y, s));
-        b = __fadd_rn(__fmul_rn(y, c), __fmul_rn(x, s));
+        for (int i = 0; i < 4; ++i) turn_pair(v[2 * i], v[2 * i + 1], cs[2 * i], cs[2 * i + 1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) turn_pair(v[i], v[4 + i], cs[2 * i], cs[2 * i + 1]);
     }
 }
 
 struct AppendArgs {
     KvAppendProblem p;
     int64_t slots;         // pages a sequence's new tokens can touch
-    int64_t cache_blocks;  // blocks that write the cache; the others rotate queries, one token each
+    int64_t cache_blocks;  // blocks that write the cache; the others rotate queries
+    int tokens;            // that such a block takes
 };
 
 template <typename T, bool ALIGNED>
@@ -70,13 +75,14 @@ __device__ __forceinline__ void load_unit(const T *row, int first, int second, f
 // One block per (page the new tokens touch, head, keys or values): the page's
 // largest new magnitude first, then its scale, its old codes under the new scale and
 // its new codes. No two blocks write the same page and head, so there is
-// nothing to order between them.
+// nothing to order between them. A thread keeps its first four units in registers in between.
 template <typename T, int KV, bool ALIGNED>
 __device__ void append_page(const AppendArgs &a, int64_t block) {
+    constexpr int kKept = 4;
     const KvAppendProblem &p = a.p;
     const int kind = static_cast<int>(block & 1);
     const int64_t heads = p.c.heads, page = p.c.page;
-    const int dim = static_cast<int>(p.c.dim);
+    const int dim = static_cast<int>(p.c.dim), per_row = dim / 8, row_log = 31 - __clz(per_row);
     const int64_t h = (block >> 1) % heads, slot = (block >> 1) / heads;
     const int64_t b = slot / a.slots, j = slot % a.slots;
     int64_t t0, t1;
@@ -86,104 +92,197 @@ __device__ void append_page(const AppendArgs &a, int64_t block) {
     const int64_t pidx = (start > 0 ? start / page : 0) + j, p_lo = pidx * page;
     if (p_lo >= ctx || pidx >= p.width) return;
     const int64_t id = p.block_table[b * p.width + pidx];
-    if (id < 0 || id >= p.c.pages) return;
     const int64_t lo = start > p_lo ? start : p_lo, hi = ctx < p_lo + page ? ctx : p_lo + page;
     const int had = static_cast<int>(lo - p_lo);
-    const int units = static_cast<int>(hi - lo) * (dim / 8);
+    const int units = static_cast<int>(hi - lo) * per_row;
 
     const Heads &src = kind ? p.v : p.k;
     const int rot = kind ? 0 : static_cast<int>(p.rot);
     const bool inter = p.interleaved != 0;
     const T *rows = static_cast<const T *>(src.p) + (t0 + lo - start) * src.ts + h * src.hs;
-    float *scale = (kind ? p.c.v_scale : p.c.k_scale) + id * heads + h;
-    uint8_t *codes = static_cast<uint8_t *>(kind ? p.c.v : p.c.k) + (id * heads + h) * page * dim;
-
-    __shared__ unsigned warp_top[kThreads / 32];
+    auto load = [&](int i, float *v) {  // unit i, rotated
+        const int t = i >> row_log, u = i & (per_row - 1);
+        int second;
+        const int first = unit_offset(u, rot, inter, &second);
+        load4<T, ALIGNED>(rows + t * src.ts + first, v);
+        load4<T, ALIGNED>(rows + t * src.ts + second, v + 4);
+        if (8 * u < rot) {
+            float cs[8];
+            load_turn(cs, p.table, p.rows, rot, lo + t, u);
+            turn(v, cs, inter);
+        }
+    };
     // magnitudes compare as their bits: a NaN is above infinity, which is
     // above every finite value
     unsigned top = 0;
-    for (int i = threadIdx.x; i < units; i += kThreads) {
-        const int t = i / (dim / 8), u = i % (dim / 8);
-        int second;
-        const int first = unit_offset(u, rot, inter, &second);
+    float kept[kKept][8];
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+        const int i = threadIdx.x + k * kThreads;
+        if (i < units) load(i, kept[k]);
+    }
+#pragma unroll
+    for (int k = 0; k < kKept; ++k)
+        if (static_cast<int>(threadIdx.x) + k * kThreads < units)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(kept[k][e]) & 0x7fffffffu);
+#pragma unroll 1
+    for (int i = threadIdx.x + kKept * kThreads; i < units; i += kThreads) {
         float v[8];
-        load_unit<T, ALIGNED>(rows + t * src.ts, first, second, v);
-        rotate_unit(v, p.table, p.rows, rot, inter, lo + t, u);
+        load(i, v);
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
     }
+    if (id < 0 || id >= p.c.pages) return;  // by the whole block
+    float *scale = (kind ? p.c.v_scale : p.c.k_scale) + id * heads + h;
+    uint8_t *codes = static_cast<uint8_t *>(kind ? p.c.v : p.c.k) + (id * heads + h) * page * dim;
+    const float old = had > 0 ? fabsf(*scale) : 0.0f;
+    // old codes, in case the scale grows: their load's latency is beside the scale's
+    uint4 *const old_codes = reinterpret_cast<uint4 *>(codes);
+    const int old_words = had * dim / 16;
+    uint4 ahead[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+        if (static_cast<int>(threadIdx.x) + k * kThreads < old_words) ahead[k] = old_codes[threadIdx.x + k * kThreads];
+
+    __shared__ unsigned warp_top[kThreads / 32];
     top = __reduce_max_sync(0xffffffffu, top);
     if ((threadIdx.x & 31) == 0) warp_top[threadIdx.x / 32] = top;
-    const float old = had > 0 ? fabsf(*scale) : 0.0f;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) top = max(top, warp_top[w]);
 
     // A page with a value that is not finite gets the scale NaN and codes 0:
     // every read of it shows.
-    const bool finite_new = top < 0x7f800000u;
     const float want = __fmul_rn(__uint_as_float(top), KV == OM_I8 ? 1.0f / 127.0f : 1.0f / 448.0f);
-    const bool finite = finite_new && __float_as_uint(old) < 0x7f800000u;
+    const bool finite = top < 0x7f800000u && __float_as_uint(old) < 0x7f800000u;
     const float grown = finite ? fmaxf(old, want) : __int_as_float(0x7FC00000);
-    if (threadIdx.x == 0) *scale = grown;
+    if (threadIdx.x == 0) *scale = grown;  // every thread has read the old one: the barrier above
 
     if (had > 0 && (grown != old || !finite)) {
         const float ratio = finite ? __fdiv_rn(old, grown) : 0.0f;  // grown > old >= 0
-        uint4 *c = reinterpret_cast<uint4 *>(codes);
-        for (int i = threadIdx.x; i < had * dim / 16; i += kThreads) {
-            uint4 w4 = c[i];
+        auto rescale = [&](int i, uint4 w4) {
             uint32_t *w = &w4.x;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                uint32_t r = 0;
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    r |= encode<KV>(finite ? __fmul_rn(decode<KV>(w[q] >> (8 * e)), ratio) : 0.0f) << (8 * e);
-                w[q] = r;
+                float v[4];
+                decode4<KV>(w[q], v);
+                w[q] = finite ? encode4<KV>(__fmul_rn(v[0], ratio), __fmul_rn(v[1], ratio), __fmul_rn(v[2], ratio), __fmul_rn(v[3], ratio)) : 0;
             }
-            c[i] = w4;
-        }
+            old_codes[i] = w4;
+        };
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+            if (static_cast<int>(threadIdx.x) + k * kThreads < old_words) rescale(threadIdx.x + k * kThreads, ahead[k]);
+#pragma unroll 1
+        for (int i = threadIdx.x + 2 * kThreads; i < old_words; i += kThreads) rescale(i, old_codes[i]);
     }
-    for (int i = threadIdx.x; i < units; i += kThreads) {
-        const int t = i / (dim / 8), u = i % (dim / 8);
+    auto store = [&](int i, const float *v) {
+        const int t = i >> row_log;
         int second;
-        const int first = unit_offset(u, rot, inter, &second);
-        float v[8];
-        load_unit<T, ALIGNED>(rows + t * src.ts, first, second, v);
-        rotate_unit(v, p.table, p.rows, rot, inter, lo + t, u);
+        const int first = unit_offset(i & (per_row - 1), rot, inter, &second);
         uint32_t w[2] = {0, 0};
         if (finite && grown > 0.0f) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) w[e / 4] |= encode<KV>(__fdiv_rn(v[e], grown)) << (8 * (e % 4));
+            for (int e = 0; e < 2; ++e)
+                w[e] = encode4<KV>(__fdiv_rn(v[4 * e], grown), __fdiv_rn(v[4 * e + 1], grown), __fdiv_rn(v[4 * e + 2], grown), __fdiv_rn(v[4 * e + 3], grown));
         }
         uint8_t *dst = codes + (had + t) * dim;
         *reinterpret_cast<uint32_t *>(dst + first) = w[0];
         *reinterpret_cast<uint32_t *>(dst + second) = w[1];
+    };
+#pragma unroll
+    for (int k = 0; k < kKept; ++k) {
+        const int i = threadIdx.x + k * kThreads;
+        if (i < units) store(i, kept[k]);
+    }
+#pragma unroll 1
+    for (int i = threadIdx.x + kKept * kThreads; i < units; i += kThreads) {
+        float v[8];
+        load(i, v);
+        store(i, v);
     }
 }
 
-// One block per token rotates its queries.
+// The sequence of each of a block's `count` tokens t, t + 1, ..., and their offset in it (-1: none), in
+// shared memory; every thread of the block takes part.
+constexpr int kMostTokens = 32;
+struct Places {
+    int seq[kMostTokens];
+    int64_t at[kMostTokens];
+};
+__device__ __forceinline__ void find_tokens(Places *places, const int32_t *cu, int64_t seqs, int64_t tokens, int64_t t, int count) {
+    for (int i = threadIdx.x; i < count; i += blockDim.x) {
+        places->seq[i] = 0;
+        places->at[i] = -1;
+    }
+    __syncthreads();
+    // a sequence that overlaps the block's tokens writes its own
+    for (int64_t b = threadIdx.x; b < seqs; b += blockDim.x) {
+        int64_t lo, hi;
+        token_range(cu, b, tokens, &lo, &hi);
+        for (int64_t i = max(lo, t); i < min(hi, t + count); ++i) {
+            places->seq[i - t] = static_cast<int>(b);
+            places->at[i - t] = i - lo;
+        }
+    }
+    __syncthreads();
+}
+
+// Some tokens' queries; four units of a thread in flight.
 template <typename T, bool ALIGNED>
-__device__ void rotate_queries(const AppendArgs &a, int64_t t) {
+__device__ void rotate_queries(const AppendArgs &a, int64_t block) {
     const KvAppendProblem &p = a.p;
-    const int dim = static_cast<int>(p.c.dim), rot = static_cast<int>(p.rot);
-    const int64_t b = block_sequence_of(p.cu, p.seqs, t);
+    const int dim = static_cast<int>(p.c.dim), rot = static_cast<int>(p.rot), per_row = dim / 8;
+    const int64_t t = block * a.tokens;
+    const int count = static_cast<int>(min(static_cast<int64_t>(a.tokens), p.tokens - t));
+    __shared__ Places places;
+    find_tokens(&places, p.cu, p.seqs, p.tokens, t, count);
+    const bool inter = p.interleaved != 0;
     // a token that no sequence owns has no position: its queries become NaN
-    const int64_t pos = b < p.seqs && t >= p.cu[b]
-                            ? static_cast<int64_t>(p.ctx[b]) - (p.cu[b + 1] < p.tokens ? p.cu[b + 1] : p.tokens) + t
-                            : -1;
-    const T *src = static_cast<const T *>(p.q.p) + t * p.q.ts;
-    T *dst = static_cast<T *>(const_cast<void *>(p.q_out.p)) + t * p.q_out.ts;
-    const int units = static_cast<int>(p.q_heads) * (dim / 8);
-    for (int i = threadIdx.x; i < units; i += kThreads) {
-        const int h = i / (dim / 8), u = i % (dim / 8);
-        int second;
-        const int first = unit_offset(u, rot, p.interleaved != 0, &second);
-        float v[8];
-        load_unit<T, ALIGNED>(src + h * p.q.hs, first, second, v);
-        rotate_unit(v, p.table, p.rows, rot, p.interleaved != 0, pos, u);
-        store4<T, ALIGNED>(dst + h * p.q_out.hs + first, v);
-        store4<T, ALIGNED>(dst + h * p.q_out.hs + second, v + 4);
+    if (threadIdx.x < count) {
+        const int64_t at = places.at[threadIdx.x], b = places.seq[threadIdx.x];
+        int64_t lo, hi;
+        token_range(p.cu, b, p.tokens, &lo, &hi);
+        places.at[threadIdx.x] = at < 0 ? -1 : static_cast<int64_t>(p.ctx[b]) - (hi - lo) + at;
+    }
+    __syncthreads();
+    const int units = static_cast<int>(p.q_heads) * per_row, row_log = 31 - __clz(per_row);
+    constexpr int kAhead = 4;
+#pragma unroll 1
+    for (int tok = 0; tok < count; ++tok) {
+        const T *const src = static_cast<const T *>(p.q.p) + (t + tok) * p.q.ts;
+        T *const dst = static_cast<T *>(const_cast<void *>(p.q_out.p)) + (t + tok) * p.q_out.ts;
+        const int64_t pos = places.at[tok];
+#pragma unroll 1
+        for (int base = threadIdx.x; base < units; base += kAhead * kThreads) {
+            float v[kAhead][8];
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = base + k * kThreads, u = i & (per_row - 1);
+                if (i >= units) break;
+                int second;
+                const int first = unit_offset(u, rot, inter, &second);
+                const T *const row = src + (i >> row_log) * p.q.hs;
+                load4<T, ALIGNED>(row + first, v[k]);
+                load4<T, ALIGNED>(row + second, v[k] + 4);
+            }
+#pragma unroll
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = base + k * kThreads, u = i & (per_row - 1);
+                if (i >= units) break;
+                int second;
+                const int first = unit_offset(u, rot, inter, &second);
+                if (8 * u < rot) {
+                    float cs[8];
+                    load_turn(cs, p.table, p.rows, rot, pos, u);
+                    turn(v[k], cs, inter);
+                }
+                T *const row = dst + (i >> row_log) * p.q_out.hs;
+                store4<T, ALIGNED>(row + first, v[k]);
+                store4<T, ALIGNED>(row + second, v[k] + 4);
+            }
+        }
     }
 }
 
@@ -196,40 +295,79 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
         rotate_queries<T, ALIGNED>(a, block - a.cache_blocks);
 }
 
-// One block per token: 16 codes of one head's keys or values per thread.
+struct ReadArgs {
+    KvReadProblem p;
+    int tokens;  // of a block
+    int slice;   // 16-byte pieces of codes of a round, a power of two
+};
+
+// Some tokens, in rounds of up to 32 KB of codes: all of a round's copies into shared memory are in flight together
+// (neighbouring tokens of one head after the other, as they lie in the cache); then neighbouring lanes
+// store neighbouring 16 bytes of values.
+constexpr int kReadThreads = 256, kMostSlice = 2048;
 template <typename T, int KV>
-__global__ void __launch_bounds__(kThreads) kv_read_kernel(const __grid_constant__ KvReadProblem p) {
-    const int64_t t = blockIdx.x;
-    const int64_t b = block_sequence_of(p.cu, p.seqs, t);
-    const int64_t heads = p.c.heads, page = p.c.page;
-    const int dim = static_cast<int>(p.c.dim);
-    int64_t id = -1, pos = -1;
-    if (b < p.seqs && t >= p.cu[b]) {
-        pos = static_cast<int64_t>(p.start[b]) + t - p.cu[b];
-        if (pos >= 0 && pos / page < p.width) id = p.block_table[b * p.width + pos / page];
-        if (id >= p.c.pages) id = -1;
+__global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const __grid_constant__ ReadArgs a) {
+    const KvReadProblem &p = a.p;
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * a.tokens, page = p.c.page;
+    const int heads = static_cast<int>(p.c.heads), dim = static_cast<int>(p.c.dim);
+    const int count = static_cast<int>(min(static_cast<int64_t>(a.tokens), p.tokens - t));
+    extern __shared__ __align__(16) uint8_t held[];
+    __shared__ Places places;
+    __shared__ int ids[kMostTokens], rows[kMostTokens];
+    __shared__ float scales[kMostSlice / 4];  // of the rows of a round
+    find_tokens(&places, p.cu, p.seqs, p.tokens, t, count);
+    if (threadIdx.x < kMostTokens) {
+        int64_t id = -1, pos = -1;
+        if (threadIdx.x < count) {
+            const int64_t at = places.at[threadIdx.x], b = places.seq[threadIdx.x];
+            if (at >= 0) {
+                pos = p.start[b] + at;
+                if (pos >= 0 && pos / page < p.width) id = p.block_table[b * p.width + pos / page];
+                if (id >= p.c.pages || id < 0) id = -1;
+            }
+        }
+        ids[threadIdx.x] = static_cast<int>(id);
+        rows[threadIdx.x] = id < 0 ? 0 : static_cast<int>(pos % page);
     }
-    const int per_head = dim / 16, units = static_cast<int>(heads) * per_head;
-    for (int i = threadIdx.x; i < 2 * units; i += kThreads) {
-        const int kind = i >= units, r = kind ? i - units : i;
-        const int64_t h = r / per_head;
-        const int d = r % per_head * 16;
-        T *out = static_cast<T *>(kind ? p.v_out : p.k_out) + (t * heads + h) * dim + d;
-        float scale = __int_as_float(0x7FC00000);  // a position the cache does not hold reads as NaN
-        uint4 w4 = make_uint4(0, 0, 0, 0);
-        if (id >= 0) {
-            scale = (kind ? p.c.v_scale : p.c.k_scale)[id * heads + h];
-            w4 = *reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(kind ? p.c.v : p.c.k) +
-                                                  ((id * heads + h) * page + pos % page) * dim + d);
+    __syncthreads();
+    // piece i: of (keys or values, head, token, place in the row); powers of two but for the heads
+    const int row_log = 31 - __clz(dim / 16), head_log = row_log + 31 - __clz(a.tokens), pieces = 2 * heads << head_log;
+    for (int first = 0; first < pieces; first += a.slice) {
+        const int many = min(a.slice, pieces - first);
+        for (int i = threadIdx.x; i < many; i += kReadThreads) {
+            const int q = first + i, kh = q >> head_log, tok = (q >> row_log) & (a.tokens - 1), h = kh >= heads ? kh - heads : kh;
+            const int64_t at = static_cast<int64_t>(ids[tok]) * heads + h;
+            if (ids[tok] >= 0) {
+                const uint8_t *const src = static_cast<const uint8_t *>(kh >= heads ? p.c.v : p.c.k) + (at * page + rows[tok]) * dim + (q & ((1 << row_log) - 1)) * 16;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(static_cast<uint32_t>(__cvta_generic_to_shared(held)) + i * 16), "l"(src) : "memory");
+            } else {
+                reinterpret_cast<uint4 *>(held)[i] = make_uint4(0, 0, 0, 0);
+            }
+            // a position the cache does not hold reads as NaN
+            if ((q & ((1 << row_log) - 1)) == 0) scales[i >> row_log] = ids[tok] >= 0 ? (kh >= heads ? p.c.v_scale : p.c.k_scale)[at] : __int_as_float(0x7FC00000);
         }
-        const uint32_t *w = &w4.x;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncthreads();
+        constexpr int kCodes = 16 / sizeof(T), kPer = 16 / kCodes;  // values of a store; stores of a piece
+#pragma unroll 4
+        for (int i = threadIdx.x; i < many * kPer; i += kReadThreads) {
+            const int q = first + i / kPer, kh = q >> head_log, tok = (q >> row_log) & (a.tokens - 1), h = kh >= heads ? kh - heads : kh;
+            if (tok >= count) continue;
+            uint32_t w[kCodes / 4];
+            memcpy(w, held + i * kCodes, kCodes);
+            const float scale = scales[(i / kPer) >> row_log];
+            float v[kCodes];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            float v[4];
+            for (int j = 0; j < kCodes / 4; ++j) decode4<KV>(w[j], v + 4 * j);
+            T e[kCodes];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = __fmul_rn(decode<KV>(w[q] >> (8 * e)), scale);
-            store4<T, true>(out + 4 * q, v);
+            for (int j = 0; j < kCodes; ++j) e[j] = from_float<T>(__fmul_rn(v[j], scale));
+            uint4 o;
+            memcpy(&o, e, 16);
+            T *out = static_cast<T *>(kh >= heads ? p.v_out : p.k_out) + ((t + tok) * heads + h) * dim + (q & ((1 << row_log) - 1)) * 16 + i % kPer * kCodes;
+            __stcs(reinterpret_cast<uint4 *>(out), o);
         }
+        __syncthreads();
     }
 }
 
@@ -285,12 +423,20 @@ cudaError_t append_codes(const AppendArgs &a, bool aligned, int64_t blocks, cuda
 }
 
 template <typename T>
-cudaError_t read_codes(const KvReadProblem &p, cudaStream_t s) {
-    if (p.c.dtype == OM_I8)
-        kv_read_kernel<T, OM_I8><<<static_cast<unsigned>(p.tokens), kThreads, 0, s>>>(p);
+cudaError_t read_codes(const ReadArgs &a, cudaStream_t s) {
+    const unsigned grid = static_cast<unsigned>((a.p.tokens + a.tokens - 1) / a.tokens);
+    if (a.p.c.dtype == OM_I8)
+        kv_read_kernel<T, OM_I8><<<grid, kReadThreads, a.slice * 16, s>>>(a);
     else
-        kv_read_kernel<T, OM_E4M3><<<static_cast<unsigned>(p.tokens), kThreads, 0, s>>>(p);
+        kv_read_kernel<T, OM_E4M3><<<grid, kReadThreads, a.slice * 16, s>>>(a);
     return cudaGetLastError();
+}
+
+// Tokens of a block: as many as leave every SM several blocks.
+int tokens_of_block(int64_t tokens, int most) {
+    int n = 1;
+    while (n < most && tokens >= int64_t(n) * 2 * 8 * num_sms()) n *= 2;
+    return n;
 }
 
 // Groups of four elements start on their own size's boundary in every row.
@@ -301,11 +447,11 @@ bool heads_aligned(const Heads &x, int64_t heads, int bytes) {
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendProblem &p, cudaStream_t s) {
-    AppendArgs a{p, 0, 0};
+    AppendArgs a{p, 0, 0, tokens_of_block(p.tokens, 8)};
     const int64_t most = p.max_new < p.tokens ? p.max_new : p.tokens;
     a.slots = (most + p.c.page - 2) / p.c.page + 1;
     a.cache_blocks = p.seqs * a.slots * p.c.heads * 2;
-    const int64_t blocks = a.cache_blocks + (p.q_heads > 0 ? p.tokens : 0);
+    const int64_t blocks = a.cache_blocks + (p.q_heads > 0 ? (p.tokens + a.tokens - 1) / a.tokens : 0);
     const int bytes = p.dtype == OM_F32 ? 4 : 2;
     const bool aligned = heads_aligned(p.k, p.c.heads, bytes) && heads_aligned(p.v, p.c.heads, bytes) &&
                          (p.q_heads == 0 || (heads_aligned(p.q, p.q_heads, bytes) && heads_aligned(p.q_out, p.q_heads, bytes)));
@@ -315,9 +461,12 @@ cudaError_t launch_kv_append(const KvAppendProblem &p, cudaStream_t s) {
 }
 
 cudaError_t launch_kv_read(const KvReadProblem &p, cudaStream_t s) {
-    if (p.dtype == OM_F32) return read_codes<float>(p, s);
-    if (p.dtype == OM_F16) return read_codes<__half>(p, s);
-    return read_codes<__nv_bfloat16>(p, s);
+    ReadArgs a{p, tokens_of_block(p.tokens, kMostTokens), 1};
+    const int64_t row = p.c.dim / 16, pieces = 2 * p.c.heads * row * a.tokens;
+    while (a.slice < kMostSlice && (a.slice < pieces || a.slice < row)) a.slice *= 2;
+    if (p.dtype == OM_F32) return read_codes<float>(a, s);
+    if (p.dtype == OM_F16) return read_codes<__half>(a, s);
+    return read_codes<__nv_bfloat16>(a, s);
 }
 
 cudaError_t launch_rope_table(int64_t rows, int64_t rot, double base, int scaling, double factor,
