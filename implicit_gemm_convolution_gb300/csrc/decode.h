@@ -11,6 +11,23 @@
 
 namespace om {
 
+// Launches a kernel that may be started while the stream's kernel before it still runs: it has to
+// call wait_for_earlier() before its first access to memory.
+template <typename... P, typename... A>
+cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, const A &...args) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // y[i][j] = sum_p x[i][p] * (u[j][p] - z[j][p / group]) * s[j][p / group].
 struct W4Problem {
     int64_t m, n, k, group;

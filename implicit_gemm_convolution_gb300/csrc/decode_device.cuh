@@ -12,6 +12,14 @@
 
 namespace om {
 
+// Waits until the kernels before this one in its stream have finished and their writes are visible, and lets the next
+// kernel's blocks take the room that this one's leave (they wait here too): what it saves is the launch of
+// a kernel between two short ones.
+__device__ __forceinline__ void wait_for_earlier() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 template <typename T>
 __device__ __forceinline__ float to_float(T v) {
     if constexpr (sizeof(T) == 4) {

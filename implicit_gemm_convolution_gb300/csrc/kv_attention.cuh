@@ -245,6 +245,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
     uint2 *const q_shared = reinterpret_cast<uint2 *>(smem + kWarps * C::kRing);  // [part][step][nt][lane]
     float *const join = reinterpret_cast<float *>(C::kEarly ? smem + kWarps * C::kRing + C::kQBytes : smem);
 
+    wait_for_earlier();
     // ---- this block's share of the units of all items (sequence, key head, row block)
     const int seqs = static_cast<int>(p.seqs);
     int total = 0, longest = 0;
@@ -929,8 +930,7 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
     if (grid > Config<T, DIM, NT>::kMaxBlocks) grid = Config<T, DIM, NT>::kMaxBlocks;
     if (units < grid * kMinUnits) grid = static_cast<int64_t>((units + kMinUnits - 1) / kMinUnits);
     if (grid < 1) grid = 1;
-    kv_attention_kernel<T, KV, DIM, NT><<<static_cast<unsigned>(grid), kThreads, kSmem, s>>>(a);
-    return cudaGetLastError();
+    return launch_behind(kv_attention_kernel<T, KV, DIM, NT>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmem, s, a);
 }
 
 template <typename T, int KV, int DIM>

@@ -288,6 +288,7 @@ __device__ void rotate_queries(const AppendArgs &a, int64_t block) {
 
 template <typename T, int KV, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendArgs a) {
+    wait_for_earlier();
     const int64_t block = blockIdx.x;
     if (block < a.cache_blocks)
         append_page<T, KV, ALIGNED>(a, block);
@@ -315,6 +316,7 @@ __global__ void __launch_bounds__(kReadThreads) kv_read_kernel(const __grid_cons
     __shared__ Places places;
     __shared__ int ids[kMostTokens], rows[kMostTokens];
     __shared__ float scales[kMostSlice / 4];  // of the rows of a round
+    wait_for_earlier();
     find_tokens(&places, p.cu, p.seqs, p.tokens, t, count);
     if (threadIdx.x < kMostTokens) {
         int64_t id = -1, pos = -1;
@@ -409,11 +411,7 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename T, int KV>
 cudaError_t append_typed(const AppendArgs &a, bool aligned, int64_t blocks, cudaStream_t s) {
-    if (aligned)
-        kv_append_kernel<T, KV, true><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a);
-    else
-        kv_append_kernel<T, KV, false><<<static_cast<unsigned>(blocks), kThreads, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_behind(aligned ? kv_append_kernel<T, KV, true> : kv_append_kernel<T, KV, false>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s, a);
 }
 
 template <typename T>
@@ -425,11 +423,7 @@ cudaError_t append_codes(const AppendArgs &a, bool aligned, int64_t blocks, cuda
 template <typename T>
 cudaError_t read_codes(const ReadArgs &a, cudaStream_t s) {
     const unsigned grid = static_cast<unsigned>((a.p.tokens + a.tokens - 1) / a.tokens);
-    if (a.p.c.dtype == OM_I8)
-        kv_read_kernel<T, OM_I8><<<grid, kReadThreads, a.slice * 16, s>>>(a);
-    else
-        kv_read_kernel<T, OM_E4M3><<<grid, kReadThreads, a.slice * 16, s>>>(a);
-    return cudaGetLastError();
+    return launch_behind(a.p.c.dtype == OM_I8 ? kv_read_kernel<T, OM_I8> : kv_read_kernel<T, OM_E4M3>, dim3(grid), dim3(kReadThreads), a.slice * 16, s, a);
 }
 
 // Tokens of a block: as many as leave every SM several blocks.

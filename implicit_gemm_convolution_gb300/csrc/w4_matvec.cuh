@@ -218,6 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_matvec_kernel(const __grid_con
         z_row[r] = (z_low + (g + 8 * r) * ldz) & 3;
     }
 
+    wait_for_earlier();
     int turn = 0;
     for (int pass = t_begin; pass < t_end; pass += kMaxTiles) {
         const int pass_tiles = min(kMaxTiles, t_end - pass);
@@ -572,8 +573,7 @@ cudaError_t launch(Args a, cudaStream_t s) {
         }
     }
     const int64_t smem = C::kFixed + cols * 64 + a.slab * per_unit;
-    w4_matvec_kernel<T, NT, GB, ALIGNED><<<grid, kThreads, static_cast<size_t>(smem), s>>>(a);
-    return cudaGetLastError();
+    return launch_behind(w4_matvec_kernel<T, NT, GB, ALIGNED>, grid, dim3(kThreads), static_cast<size_t>(smem), s, a);
 }
 
 template <typename T, int NT, int GB>
