@@ -97,14 +97,13 @@ struct KvAttentionProblem {
 // two partial results (rows x (dim + 2) floats) for each of kKvMaxBlocks blocks.
 constexpr int64_t kKvMaxBlocks = 608;
 constexpr size_t kKvCounterBytes = 4096;
-inline int64_t kv_block_rows(int64_t group, int64_t dim, int64_t max_new) {
+inline int64_t kv_block_rows(int64_t group, int64_t max_new) {
     // more rows than a block holds take further blocks
     const int64_t rows = max_new > (int64_t(1) << 20) || group > (int64_t(1) << 20) ? int64_t(1) << 20 : group * max_new;
-    if (rows <= 8) return 8;
-    return rows <= 16 || dim > 128 ? 16 : 32;
+    return rows <= 8 ? 8 : 16;
 }
 inline size_t kv_workspace_bytes(int64_t group, int64_t dim, int64_t max_new) {
-    return kKvCounterBytes + static_cast<size_t>(2 * kKvMaxBlocks * kv_block_rows(group, dim, max_new) * (dim + 2) * 4);
+    return kKvCounterBytes + static_cast<size_t>(2 * kKvMaxBlocks * kv_block_rows(group, max_new) * (dim + 2) * 4);
 }
 cudaError_t launch_kv_attention_f32(const KvAttentionProblem &p, cudaStream_t s);
 cudaError_t launch_kv_attention_f16(const KvAttentionProblem &p, cudaStream_t s);

@@ -13,7 +13,7 @@
 //
 // Layout. The products are taken transposed, S^T = C Q^T and O^T = E^T P^T: codes
 // are the 16-row operand and the query rows (query tokens times the heads that
-// share a key head) the 8-column one, so a block holds 8, 16 or 32 of them and one
+// share a key head) the 8-column one, so a block holds 8 or 16 of them and one
 // query head wastes no more than 7 columns. Each byte of the cache is
 // used by exactly one lane: the sums run over head dimensions (for S) and positions (for O), whose
 // order is free, so a lane takes 16 consecutive bytes of a row as four
@@ -63,17 +63,6 @@ template <int N>
 __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
-__device__ __forceinline__ uint4 lds16(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-    return v;
-}
-__device__ __forceinline__ uint2 lds8(uint32_t a) {
-    uint2 v;
-    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a) : "memory");
-    return v;
-}
-
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -204,10 +193,10 @@ struct Config {
     // query fragments stay in registers where they fit beside the sums
     static constexpr bool kQShared = NT * kParts * S::kSteps > 16;
     static constexpr int kQBytes = kParts * S::kSteps * NT * 256;
-    static constexpr int kStages = DIM == 64 ? 6 : (DIM == 128 && NT == 4 ? 4 : 3);
+    static constexpr int kStages = DIM == 64 ? 6 : 3;
     static constexpr int kJoin = S::kSteps * NT * 128 + NT * 128;  // floats of one warp's state
     // the next segment's copies start before the join of the warps, which then has memory of its own
-    static constexpr bool kEarly = NT == 1;
+    static constexpr bool kEarly = NT * DIM <= 256;
     static constexpr int kRing = kStages * S::kTileBytes;  // of one warp
     static constexpr int kSmem = kWarps * kRing + kQBytes + (kEarly ? 2 * kJoin * 4 : 0);
     static constexpr int64_t kSlot = 8 * NT * (DIM + 2);
@@ -375,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
     // the next segment's queries: 16 threads a row
     constexpr int kEach = DIM / 16;
     const int q_row = threadIdx.x / 16, q_d = threadIdx.x % 16 * kEach;
-    float qv[C::kEarly ? kEach : 1];
+    float qv[C::kEarly ? NT : 1][kEach];
     auto load_queries = [&](int nt, float *v) {
         const int r = part.row0 + nt * 8 + q_row;
         if (nt * 8 + q_row < part.rows) {
@@ -441,7 +430,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
             pages_end = w0 < w1 ? (hi + page - 1) >> page_log : 0;  // inside the table: hi is
             id0 = load_id(pb + lane);
             id1 = load_id(pb + 32 + lane);
-            if constexpr (C::kEarly) load_queries(0, qv);
+            if constexpr (C::kEarly) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) load_queries(nt, qv[nt]);
+            }
             k_lane = static_cast<const uint8_t *>(p.c.k) + static_cast<int64_t>(part.h) * page * DIM + g * DIM + c * 16;
             f_pos = w0;
             f_new = true;
@@ -559,17 +551,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
         // column n = row of the block, step s of lane c: four elements from 64 (s / 4) + 16 c + 4 (s % 4)
         {
             const int row = q_row;
-#pragma unroll 1
+#pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 const int r = part.row0 + nt * 8 + row;
                 const bool live = nt * 8 + row < part.rows;
-                float v[kEach];
-                if constexpr (C::kEarly) {
-#pragma unroll
-                    for (int e = 0; e < kEach; ++e) v[e] = qv[e];
-                } else {
-                    load_queries(nt, v);
-                }
+                float *const v = qv[C::kEarly ? nt : 0];
+                if constexpr (!C::kEarly) load_queries(nt, v);
                 unsigned top = 0;
 #pragma unroll
                 for (int e = 0; e < kEach; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
@@ -642,7 +629,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
         float kf[NT][2], vr = 0.0f;
         bool next_scaled = false;
         bool page_ok = false, odd_scale = false;
-        uint32_t src = ring_at + lane * 16;
+        const uint8_t *const lane_ring = smem + warp * C::kRing + lane * 16;
+        int src_at = 0;
         bool c_new = true;
 #pragma unroll 1
         for (int pos = w0; pos < w1; pos += kTile) {
@@ -684,6 +672,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
                 vr = odd_scale ? __int_as_float(0x7FC00000) : __fdividef(va, vmax);
             }
 
+            const uint8_t *const src = lane_ring + src_at;
             float s[NT][4], s1[NT][4];  // two chains of products
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -691,8 +680,8 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
                 for (int j = 0; j < 4; ++j) s[nt][j] = s1[nt][j] = 0.0f;
 #pragma unroll
             for (int i = 0; i < S::kKeyChunks; ++i) {
-                const uint4 ra = lds16(src + i * 512);
-                const uint4 rc = lds16(src + (S::kKeyChunks + i) * 512);
+                const uint4 ra = *reinterpret_cast<const uint4 *>(src + i * 512);
+                const uint4 rc = *reinterpret_cast<const uint4 *>(src + (S::kKeyChunks + i) * 512);
                 const uint32_t x[4] = {ra.x, ra.y, ra.z, ra.w}, y[4] = {rc.x, rc.y, rc.z, rc.w};
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
@@ -779,19 +768,19 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
                     }
                 }
             }
-            const uint32_t vsrc = src + kTile * DIM - (S::kValueBytes == 16 ? 0 : lane * 8);
+            const uint8_t *const vsrc = src + kTile * DIM - (S::kValueBytes == 16 ? 0 : lane * 8);
 #pragma unroll
             for (int i = 0; i < S::kValueChunks; ++i) {
                 constexpr int kWords = S::kValueBytes / 4;
                 uint32_t v[4][kWords];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const uint32_t at = vsrc + (r * S::kValueChunks + i) * 32 * S::kValueBytes;
+                    const uint8_t *const at = vsrc + (r * S::kValueChunks + i) * 32 * S::kValueBytes;
                     if constexpr (kWords == 4) {
-                        const uint4 x = lds16(at);
+                        const uint4 x = *reinterpret_cast<const uint4 *>(at);
                         v[r][0] = x.x; v[r][1] = x.y; v[r][2] = x.z; v[r][3] = x.w;
                     } else {
-                        const uint2 x = lds8(at);
+                        const uint2 x = *reinterpret_cast<const uint2 *>(at);
                         v[r][0] = x.x; v[r][1] = x.y;
                     }
                 }
@@ -812,7 +801,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
                     }
                 }
             }
-            src = src == ring_at + lane * 16 + (C::kStages - 1) * S::kTileBytes ? ring_at + lane * 16 : src + S::kTileBytes;
+            src_at = src_at == (C::kStages - 1) * S::kTileBytes ? 0 : src_at + S::kTileBytes;
         }
         cp_wait<0>();
     }
@@ -935,11 +924,8 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
 
 template <typename T, int KV, int DIM>
 cudaError_t by_rows(const Args &a, cudaStream_t s) {
-    const int64_t rows = kv_block_rows(a.p.q_heads / a.p.c.heads, DIM, a.p.max_new);
+    const int64_t rows = kv_block_rows(a.p.q_heads / a.p.c.heads, a.p.max_new);
     if (rows == 8) return launch<T, KV, DIM, 1>(a, s);
-    if constexpr (DIM <= 128) {
-        if (rows == 32) return launch<T, KV, DIM, 4>(a, s);
-    }
     return launch<T, KV, DIM, 2>(a, s);
 }
 
