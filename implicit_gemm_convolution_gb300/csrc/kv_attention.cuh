@@ -14,12 +14,13 @@
 // Layout. The products are taken transposed, S^T = C Q^T and O^T = E^T P^T: codes
 // are the 16-row operand and the query rows (query tokens times the heads that
 // share a key head) the 8-column one, so a block holds 8 or 16 of them and one
-// query head wastes no more than 7 columns. Each byte of the cache is
-// used by exactly one lane: the sums run over head dimensions (for S) and positions (for O), whose
-// order is free, so a lane takes 16 consecutive bytes of a row as four
-// k-steps (keys) or eight row pairs (values). A lane's copies therefore go through a ring in
-// shared memory that only the lane itself reads, with no barrier and no
-// bank conflict; S^T turns into P^T's operand by one 8 x 8 transpose per 8 positions.
+// query head wastes no more than 7 columns. The sums run over head dimensions (for S) and positions (for
+// O), whose order is free, so a lane takes 16 consecutive bytes of a row as four k-steps (keys) or
+// eight row pairs (values): no byte is moved within a register row. A warp copies its own
+// 16 positions of a page, keys and values, each as they lie in memory (whole lines: pieces of
+// half a line read at three quarters of the rate), into a ring that no other warp reads, rows turned by an
+// exclusive-or so that both ways of reading them are free of bank conflicts. S^T turns into P^T's operand by
+// one 8 x 8 transpose per 8 positions.
 #pragma once
 
 #include <cfloat>
@@ -50,13 +51,19 @@ struct Shape {
     static constexpr int kValueChunks = DIM / 8 / kValueBytes;
     static constexpr int kSteps = DIM / 16;                  // k-steps of S, row tiles of O
     static constexpr int kTileBytes = 2 * kTile * DIM;
+    static constexpr int kCopies = kTile * DIM / 512;        // 16-byte copies of a lane, for keys and for values
+    static constexpr int kCopyRows = 512 / DIM;              // rows that one of them covers for a warp
+    // Where piece p (16 bytes) of row r < 8 lies in a tile (rows r + 8: 8 rows further). Rows of 128 bytes and
+    // more: pieces by an exclusive-or whose low bit is the row's and whose third bit parts even rows from
+    // odd ones; rows of 64 bytes: neighbouring pairs of rows and of pieces change places.
+    __device__ static __forceinline__ int place(int r, int p) {
+        if constexpr (DIM == 64) return (r ^ ((r >> 1) & 1)) * 64 + (p ^ ((r >> 1) & 2)) * 16;
+        return r * DIM + (p ^ (r & 7) ^ ((r & 1) << 2)) * 16;
+    }
 };
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp8(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -312,8 +319,9 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
     uint32_t f_dst = 0;
     const int64_t page_bytes = static_cast<int64_t>(heads) * page * DIM;
     const uint8_t *k_lane = nullptr, *f_k = nullptr;
-    const int64_t v_lane = static_cast<const uint8_t *>(p.c.v) - static_cast<const uint8_t *>(p.c.k) + 2 * c * DIM + g * S::kValueBytes -
-                           (g * DIM + c * 16);  // from a lane's place among the keys to its place among the values
+    const int64_t to_values = static_cast<const uint8_t *>(p.c.v) - static_cast<const uint8_t *>(p.c.k);
+    const int copy_row = lane * 16 / DIM;
+    const uint32_t copy_to = S::place(copy_row, lane % (DIM / 16));
     bool f_new = true;
     auto load_id = [&](int j) -> int {
         const int id = j < pages_end ? p.block_table[seq.b * p.width + j] : -1;
@@ -334,29 +342,18 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
             }
             // values behind the last visible position are taken as zero: a weight of zero would
             // not hide a NaN among them
-            const int left = f_id < 0 ? 0 : hi - f_pos, key_bytes = f_id < 0 ? 0 : 16;
-            const uint8_t *const f_v = f_k + v_lane;
-            const uint32_t vdst = f_dst + kTile * DIM - (S::kValueBytes == 16 ? 0 : lane * 8);
+            const int left = f_id < 0 ? 0 : hi - f_pos;
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-#pragma unroll
-                for (int i = 0; i < S::kKeyChunks; ++i) cp16(f_dst + (r * S::kKeyChunks + i) * 512, f_k + r * 8 * DIM + i * 64, key_bytes);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const int t = (r & 1) + (r & 2) * 4;
-                const int bytes = 2 * c + t < left ? S::kValueBytes : 0;
-#pragma unroll
-                for (int i = 0; i < S::kValueChunks; ++i) {
-                    const uint32_t d = vdst + (r * S::kValueChunks + i) * 32 * S::kValueBytes;
-                    if constexpr (S::kValueBytes == 16)
-                        cp16(d, f_v + t * DIM + i * 128, bytes);
-                    else
-                        cp8(d, f_v + t * DIM + i * 128, bytes);
-                }
+            for (int j = 0; j < S::kCopies; ++j) {
+                // row j kCopyRows + copy_row: its place differs by constants
+                const uint32_t to = f_dst + j * 512 + (copy_to ^ (DIM == 64 ? 0 : (j * S::kCopyRows & 7) * 16));
+                const int bytes = copy_row + j * S::kCopyRows < left ? 16 : 0;
+                cp16(to, f_k + j * 512, bytes);
+                cp16(to + kTile * DIM, f_k + to_values + j * 512, bytes);
             }
             f_k += kTile * DIM;
             f_pos += kTile;
-            f_dst = f_dst == ring_at + lane * 16 + (C::kStages - 1) * S::kTileBytes ? ring_at + lane * 16 : f_dst + S::kTileBytes;
+            f_dst = f_dst == ring_at + (C::kStages - 1) * S::kTileBytes ? ring_at : f_dst + S::kTileBytes;
         }
         cp_commit();
     };
@@ -382,6 +379,12 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
             for (int e = 0; e < kEach; ++e) v[e] = 0.0f;
         }
     };
+
+    // a lane's places in a tile: keys by (row g, pieces c, c + 4, ...), values by (rows 2 c and 2 c + 1,
+    // piece g, or half a piece)
+    const int key_at = S::place(g, c);
+    const int value_at[2] = {S::place(2 * c, DIM == 64 ? g / 2 : g) + (DIM == 64 ? g % 2 * 8 : 0),
+                             S::place(2 * c + 1, DIM == 64 ? g / 2 : g) + (DIM == 64 ? g % 2 * 8 : 0)};
 
     float o[S::kSteps][NT][4], m[NT][2], l[NT][2], vmax = FLT_MIN;
     bool have = false;
@@ -434,10 +437,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) load_queries(nt, qv[nt]);
             }
-            k_lane = static_cast<const uint8_t *>(p.c.k) + static_cast<int64_t>(part.h) * page * DIM + g * DIM + c * 16;
+            k_lane = static_cast<const uint8_t *>(p.c.k) + static_cast<int64_t>(part.h) * page * DIM + lane * 16;
             f_pos = w0;
             f_new = true;
-            f_dst = ring_at + lane * 16;
+            f_dst = ring_at;
 #pragma unroll 1
             for (int i = 0; i < C::kStages - 1; ++i) fetch();
             load_scales(id0, &ka0, &va0);
@@ -629,13 +632,14 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
         float kf[NT][2], vr = 0.0f;
         bool next_scaled = false;
         bool page_ok = false, odd_scale = false;
-        const uint8_t *const lane_ring = smem + warp * C::kRing + lane * 16;
+        const uint8_t *const my_ring = smem + warp * C::kRing;
         int src_at = 0;
         bool c_new = true;
 #pragma unroll 1
         for (int pos = w0; pos < w1; pos += kTile) {
+            cp_wait<C::kStages - 2>();
+            __syncwarp();  // the tile is here for every lane, and every lane is done with the last one
             fetch();
-            cp_wait<C::kStages - 1>();
             if (c_new || (pos & (page - 1)) == 0) {  // a page's first tile
                 c_new = false;
                 int off = (pos >> page_log) - pb;
@@ -672,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
                 vr = odd_scale ? __int_as_float(0x7FC00000) : __fdividef(va, vmax);
             }
 
-            const uint8_t *const src = lane_ring + src_at;
+            const uint8_t *const src = my_ring + src_at;
             float s[NT][4], s1[NT][4];  // two chains of products
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -680,8 +684,10 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
                 for (int j = 0; j < 4; ++j) s[nt][j] = s1[nt][j] = 0.0f;
 #pragma unroll
             for (int i = 0; i < S::kKeyChunks; ++i) {
-                const uint4 ra = *reinterpret_cast<const uint4 *>(src + i * 512);
-                const uint4 rc = *reinterpret_cast<const uint4 *>(src + (S::kKeyChunks + i) * 512);
+                // piece 4 i + c of rows g and g + 8
+                const uint8_t *const at = src + (key_at ^ (i & 1) * 64) + i / 2 * 128;
+                const uint4 ra = *reinterpret_cast<const uint4 *>(at);
+                const uint4 rc = *reinterpret_cast<const uint4 *>(at + 8 * DIM);
                 const uint32_t x[4] = {ra.x, ra.y, ra.z, ra.w}, y[4] = {rc.x, rc.y, rc.z, rc.w};
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
@@ -768,14 +774,15 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
                     }
                 }
             }
-            const uint8_t *const vsrc = src + kTile * DIM - (S::kValueBytes == 16 ? 0 : lane * 8);
+            const uint8_t *const vsrc = src + kTile * DIM;
 #pragma unroll
             for (int i = 0; i < S::kValueChunks; ++i) {
                 constexpr int kWords = S::kValueBytes / 4;
                 uint32_t v[4][kWords];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const uint8_t *const at = vsrc + (r * S::kValueChunks + i) * 32 * S::kValueBytes;
+                    // rows 2 c, 2 c + 1 and 8 further
+                    const uint8_t *const at = vsrc + value_at[r & 1] + r / 2 * 8 * DIM + i * 128;
                     if constexpr (kWords == 4) {
                         const uint4 x = *reinterpret_cast<const uint4 *>(at);
                         v[r][0] = x.x; v[r][1] = x.y; v[r][2] = x.z; v[r][3] = x.w;
@@ -804,6 +811,7 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
             src_at = src_at == (C::kStages - 1) * S::kTileBytes ? 0 : src_at + S::kTileBytes;
         }
         cp_wait<0>();
+        __syncwarp();  // every lane is done with the last tile: the ring takes the next segment's
     }
     if (n_parts == 0) return;
 
