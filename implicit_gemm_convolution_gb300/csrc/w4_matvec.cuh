@@ -349,9 +349,14 @@ __global__ void __launch_bounds__(kThreads, 1) w4_matvec_kernel(const __grid_con
                                         raw[j][e + 2] = v.z;
                                         raw[j][e + 3] = v.w;
                                     }
-                                } else if (i < count && k0 + 8 <= k && a.x_bytes >= 4) {
+                                } else if (i < count && a.x_bytes >= 4) {  // words, the last one's second element behind k or not
+                                    constexpr int kOf = 4 / sizeof(T);
 #pragma unroll
-                                    for (int e = 0; e < kRaw; ++e) raw[j][e] = reinterpret_cast<const uint32_t *>(src)[e];
+                                    for (int e = 0; e < kRaw; ++e) {
+                                        raw[j][e] = 0;
+                                        if (k0 + kOf * (e + 1) <= k) raw[j][e] = reinterpret_cast<const uint32_t *>(src)[e];
+                                        else if (kOf == 2 && k0 + 2 * e < k) raw[j][e] = reinterpret_cast<const uint16_t *>(src)[2 * e];
+                                    }
                                 } else if (i >= count || k0 >= k) {
 #pragma unroll
                                     for (int e = 0; e < kRaw; ++e) raw[j][e] = 0;

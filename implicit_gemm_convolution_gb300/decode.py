@@ -238,7 +238,8 @@ def kv_append(cache, q, k, v, table, block_table, ctx_len, cu, max_new: int, pai
 def kv_read(cache, block_table, start, cu, max_tokens: int, tokens: int, dtype=torch.float32, k_out=None, v_out=None,
             stream=None):
     """Reads `tokens` tokens back as values: token i of sequence b is position
-    start[b] + i. Returns keys and values, (tokens, heads, dim) of dtype."""
+    start[b] + i; max_tokens is at least the largest number of a sequence. Returns keys
+    and values, (tokens, heads, dim) of dtype."""
     batch, seqs = _batch(block_table, start, cu, "start")
     if dtype not in DTYPES:
         raise TypeError("dtype must be float32, float16 or bfloat16")
@@ -300,6 +301,8 @@ def kv_attention(cache, q, block_table, ctx_len, cu, max_new: int, scale=None, w
         lp = lse.data_ptr()
     ws, ws_bytes = None, 0
     if workspace is not None:
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor")
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     st = _lib().om_kv_attention(cache._ref, seqs, tokens, max_new, q_heads, q.data_ptr(), ts, hs, DTYPES[dtype], *batch,
                                 dim ** -0.5 if scale is None else scale, window, *oa, lp, ws, ws_bytes, _stream(stream, q))

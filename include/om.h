@@ -357,10 +357,11 @@ typedef enum om_dtype {
  *   group: 32, 64 or a multiple of 128 (OM_ERR_UNSUPPORTED otherwise); the last
  *      group of a row may be short.
  * Made for few rows (a decoding batch): the weights are read once for each
- * eight or so rows of x. The difference u - z and its products with x are exact (an
- * OM_F32 x is taken as three 8-bit parts); sums are 32 bits. Any alignment of
- * w and zeros; 16-byte aligned w with ldw a multiple of 16 is the fast form.
- * m or n zero: OM_OK, nothing launched. k == 0: +0 everywhere.
+ * 16 rows of a 16-bit x, 5 rows of a 32-bit one. The difference u - z and its products with
+ * x are exact (an OM_F32 x is taken as three 8-bit parts); sums are 32 bits. Any
+ * alignment of w and zeros; 16-byte aligned w with ldw a multiple of 16 is the fast form.
+ * m or n zero: OM_OK, nothing launched. k == 0: +0 everywhere. k, ldw and ldz above 2^26, lds above
+ * 2^24, m above 65535: OM_ERR_TOO_LARGE.
  */
 OM_API int om_w4_matvec(int64_t m, int64_t n, int64_t k, int64_t group,
                         const void *x, int64_t ldx, int x_dtype,
@@ -467,6 +468,7 @@ OM_API size_t om_kv_workspace_bytes(int64_t kv_heads, int64_t q_heads, int64_t d
  *   lse: NULL, or [tokens][q_heads]: the natural log of the sum of exponentials.
  * A query that sees no token gives zeros and lse -inf. Memory behind masked tokens
  * (stale codes, pages outside the window) never reaches an output.
+ * OM_ERR_TOO_LARGE where the table could hold 2^31 pieces of 64 positions of all heads and rows.
  * workspace: NULL (each sequence and head by one block), or device memory, 16-byte
  * aligned, of om_kv_workspace_bytes, zeroed once before its first use: long
  * sequences are then split evenly over the GPU. Calls that may run at the same time
