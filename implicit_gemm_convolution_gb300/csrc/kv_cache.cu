@@ -6,6 +6,11 @@
 // code * scale. Every step of the append is one separately rounded binary32
 // operation (the library is built without contraction), so codes, scales and
 // rotated queries have one bit pattern each, whatever the launch.
+//
+// Bound and measured (GB300; 6 680 GB/s is the measured copy bandwidth): HBM. Prompts of 12031 tokens in all, 32 query
+// and 8 key heads of 128, 32-bit: 93 us for 525 MB (5 600 GB/s, 84 %). Reading 76166 tokens of 8 heads of 128 back as
+// bfloat16: 79 us, 5 930 GB/s (89 %); with 16-byte loads whose lanes stored 32 or 64 bytes each it took 108 us. One
+// token for each of 192 sequences: 15 us, the latency of the lookups, the page's old codes and its barrier.
 
 #include <type_traits>
 

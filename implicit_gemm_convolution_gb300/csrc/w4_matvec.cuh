@@ -15,6 +15,14 @@
 // it needs. Groups of 4, 8 or 16 warps of a block split the codes of the same 16 rows; their sums
 // are joined in shared memory, in the warps' order. x stays in shared memory, for as many
 // codes at a time as fit (a slab); sums then wait in shared memory between slabs.
+//
+// Bound and measured (GB300; 6 680 GB/s is the measured copy bandwidth). The bytes of the weights would take half a
+// byte a code; what bounds it is the issue of the instructions that widen them, about 11 for eight codes, and
+// what goes with a unit. 1 x 11008 x 4096, 32-bit x, groups of 128: 13.7 us, 1 750 GB/s (26 %), 4.4 us of it until x is
+// laid out. 16 x 28669 x 8178, bfloat16, groups of 32 with zero points, rows at odd addresses: 90 us, 1 560 GB/s
+// (23 %). 1 x 1024 x 1024, float16: 3.9 us, latency. Tried and no faster: scales and zeros as a table in shared memory
+// instead of between lanes (bank conflicts, 102 against 90 us), units of 128 codes (twice the instructions around them, 148
+// us), x loaded before the first copies (no change).
 #pragma once
 
 #include <type_traits>
@@ -47,7 +55,7 @@ struct Config {
     static constexpr int kStage = kZeroAt + kRowTile * kZeroWords * 4;
     static_assert(kStage % 128 == 0, "places of words in a stage are whole multiples of 128 bytes apart");
     static constexpr int kRing = kStages * kStage;                 // of one warp
-    static constexpr int kJoinWarps = kTokens;                     // that join a tile's sums: two lanes an output
+    static constexpr int kJoinWarps = kParts == 3 ? kTokens : NT;  // that join a tile's sums
     static constexpr int kJoins = NT == 1 ? 2 : 1;                 // buffers of the sums of all warps
     static constexpr int kJoin = kJoins * kWarps * NT * 32 * 16;
     static constexpr int kAcc = kMaxTiles * kRowTile * kTokens * 4;
@@ -242,8 +250,9 @@ __global__ void __launch_bounds__(kThreads, 1) w4_matvec_kernel(const __grid_con
                         const int r = q / C::kRowPieces;
                         return dst + (ALIGNED ? r * 128 + (((q ^ r) & 7) * 16) : q * 16);
                     };
-                    if (rows >= kRowTile && byte0 + C::kRowPieces * 16 <= row_bytes && groups - grp >= kGroups + 8 && (unit > 0 || pass + f_tile > 0)) {
-                        // everything copied lies inside its row
+                    if (rows > kRowTile && grp + kGroups <= groups && (unit > 0 || pass + f_tile > 0)) {
+                        // Every group is there, and there are rows behind the tile's and something before it: what is
+                        // copied beyond a row's ends lies inside the operands. Codes behind k meet zeros of x.
 #pragma unroll
                         for (int i = 0; i < C::kPieces; ++i) {
                             const int q = lane + 32 * i;
@@ -417,6 +426,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_matvec_kernel(const __grid_con
                     __syncwarp();
                     const uint8_t *const held = smem + warp * C::kRing + stage * C::kStage;
                     const int grp = group_of(slab + unit);
+                    // a wide group goes on in the unit's second half, or the next one begins
+                    const int second_half = GB < 4 || a.wide == 1 ? 1 : static_cast<int>(static_cast<unsigned>((slab + unit) * 2 + 1) / static_cast<unsigned>(a.wide)) - grp;
                     // lane c has the scales and zero points of groups c and c + 4 of rows g and g + 8
                     constexpr int kHeld = kGroups == 8 ? 2 : 1;
                     float held_s[kHeld][2];
@@ -444,12 +455,11 @@ __global__ void __launch_bounds__(kThreads, 1) w4_matvec_kernel(const __grid_con
                     for (int b = 0; b < 8; ++b) {
                         if (b % GB == 0) {  // a group begins
                             int j = b / GB;
-                            if (GB == 4 && a.wide > 1 && b == 4)  // a wide group: the same one, or the next
-                                j = static_cast<int>(static_cast<unsigned>((slab + unit) * 2 + 1) / static_cast<unsigned>(a.wide)) - grp;
+                            if (GB == 4 && b == 4) j = second_half;
                             const int from = (lane & ~3) + j % 4;
                             s0 = __shfl_sync(0xffffffffu, held_s[b / GB / 4][0], from);
                             s1 = __shfl_sync(0xffffffffu, held_s[b / GB / 4][1], from);
-                            const uint32_t z = p.z ? __shfl_sync(0xffffffffu, held_z[b / GB / 4], from) : kMagic | 0x00080008u;
+                            const uint32_t z = __shfl_sync(0xffffffffu, held_z[b / GB / 4], from);
                             off0 = __byte_perm(z, 0, 0x1010);
                             off1 = __byte_perm(z, 0, 0x3232);
                         }
@@ -500,22 +510,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_matvec_kernel(const __grid_con
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) sums[(warp * NT + nt) * 32 + lane] = make_float4(total[nt][0], total[nt][1], total[nt][2], total[nt][3]);
                 team_barrier();
-                // two lanes an output, each half of the warps; the joining warps take turns
-                int first = part - turn * C::kJoinWarps;
-                first = (first % a.split + a.split) % a.split;
-                for (int id = first * 32 + lane; id < 2 * kRowTile * tokens; id += a.split * 32) {
-                    const int r = id % kRowTile, half = id / kRowTile % 2, tok = id / (2 * kRowTile);
-                    float sum = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < C::kParts; ++j) {
-                        const int cc = tok * C::kParts + j;
-                        const float *from = reinterpret_cast<const float *>(sums + team * a.split * NT * 32 + (cc / 8) * 32 + (r % 8) * 4 + cc % 8 / 2) + (cc & 1) + (r / 8) * 2;
-#pragma unroll
-                        for (int w = 0; w < 8; ++w)
-                            if (w < a.split / 2) sum += from[(half * (a.split / 2) + w) * NT * 128];
-                    }
-                    sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-                    if (half) continue;
+                auto finish = [&](int tok, int r, float sum) {
                     sum *= 1.0f / kCode;
                     if constexpr (kWhole) {  // 2^(e - 1): e can be -126
                         const int e = exponent(row_top[tok]);
@@ -529,6 +524,47 @@ __global__ void __launch_bounds__(kThreads, 1) w4_matvec_kernel(const __grid_con
                     } else {
                         const int row = (pass + tile) * kRowTile + r;
                         if (row < n) y[tok * p.ldy + row] = from_float<T>(sum);
+                    }
+                };
+                // the joining warps take turns
+                int first = part - turn * C::kJoinWarps;
+                first = (first % a.split + a.split) % a.split;
+                const float4 *const of_team = sums + team * a.split * NT * 32;
+                if constexpr (kWhole) {
+                    // two lanes an output, each half of the warps
+                    for (int id = first * 32 + lane; id < 2 * kRowTile * tokens; id += a.split * 32) {
+                        const int r = id % kRowTile, half = id / kRowTile % 2, tok = id / (2 * kRowTile);
+                        float sum = 0.0f;
+#pragma unroll
+                        for (int j = 0; j < C::kParts; ++j) {
+                            const int cc = tok * C::kParts + j;
+                            const float *from = reinterpret_cast<const float *>(of_team + (cc / 8) * 32 + (r % 8) * 4 + cc % 8 / 2) + (cc & 1) + (r / 8) * 2;
+#pragma unroll
+                            for (int w = 0; w < 8; ++w)
+                                if (w < a.split / 2) sum += from[(half * (a.split / 2) + w) * NT * 128];
+                        }
+                        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+                        if (!half) finish(tok, r, sum);
+                    }
+                } else if (first < NT) {
+                    // a lane's four sums: rows g and g + 8, columns 2 c and 2 c + 1
+                    float4 sum = of_team[first * 32 + lane];
+#pragma unroll 3
+                    for (int w = 1; w < a.split; ++w) {
+                        const float4 v = of_team[(w * NT + first) * 32 + lane];
+                        sum.x += v.x;
+                        sum.y += v.y;
+                        sum.z += v.z;
+                        sum.w += v.w;
+                    }
+                    const int tok = first * 8 + 2 * c;
+                    if (tok < tokens) {
+                        finish(tok, g, sum.x);
+                        finish(tok, g + 8, sum.z);
+                    }
+                    if (tok + 1 < tokens) {
+                        finish(tok + 1, g, sum.y);
+                        finish(tok + 1, g + 8, sum.w);
                     }
                 }
                 tile += teams;
