@@ -16,13 +16,14 @@
 // are joined in shared memory, in the warps' order. x stays in shared memory, for as many
 // codes at a time as fit (a slab); sums then wait in shared memory between slabs.
 //
-// Bound and measured (GB300; 6 680 GB/s is the measured copy bandwidth). The bytes of the weights would take half a
-// byte a code; what bounds it is the issue of the instructions that widen them, about 11 for eight codes, and
-// what goes with a unit. 1 x 11008 x 4096, 32-bit x, groups of 128: 13.7 us, 1 750 GB/s (26 %), 4.4 us of it until x is
-// laid out. 16 x 28669 x 8178, bfloat16, groups of 32 with zero points, rows at odd addresses: 90 us, 1 560 GB/s
-// (23 %). 1 x 1024 x 1024, float16: 3.9 us, latency. Tried and no faster: scales and zeros as a table in shared memory
-// instead of between lanes (bank conflicts, 102 against 90 us), units of 128 codes (twice the instructions around them, 148
-// us), x loaded before the first copies (no change).
+// Bound and measured (GB300; 6 680 GB/s is the measured copy bandwidth). The weights are half a byte a code; what
+// bounds the kernel is the issue of the instructions that widen them, about 11 for eight codes, and of those
+// around a unit. 1 x 11008 x 4096, 32-bit x, groups of 128: 12.6 us, 1 900 GB/s (28 %), 3.6 us of it until x is laid
+// out, then 1.4 us for each of up to five rounds of 16 rows. 16 x 28669 x 8178, bfloat16, groups of 32 with zero
+// points, rows at odd addresses: 77 us, 1 830 GB/s (27 %), 6 us for each of three slabs until x is laid out.
+// 1 x 1024 x 1024, float16: 3.8 us, latency. Tried and no faster: scales and zeros as a table in shared memory instead of
+// between lanes (bank conflicts, 102 against 90 us), units of 128 codes (twice the instructions around them, 148 us),
+// x loaded before the first copies (no change), six pieces of x a thread at a time instead of four (79 us).
 #pragma once
 
 #include <type_traits>
