@@ -22,9 +22,8 @@
 // one 8 x 8 transpose per 8 positions.
 //
 // Split. The work of all (sequence, key head, row block) items, in units of 64 positions, is cut into equal
-// shares of two blocks an SM, found on the device from the lengths; an item that a cut crosses is joined by
-// the block that finishes its last part. More and shorter shares (four times as many) ran no faster, three blocks an
-// SM neither: with the copies as they are the memory is the limit.
+// shares of the blocks that fit at once, found on the device from the lengths; an item that a cut crosses is joined by
+// the block that finishes its last part. More and shorter shares (four times as many) ran no faster.
 //
 // Bound and measured (GB300; 6 680 GB/s is the measured copy bandwidth). HBM, 2 dim bytes a position and key head:
 // 64 sequences of up to 16384 tokens, 8 key heads of 128, 8 query heads each, bfloat16, whole numbers: 252 us,
@@ -211,7 +210,7 @@ struct Config {
     // query fragments stay in registers where they fit beside the sums
     static constexpr bool kQShared = NT * kParts * S::kSteps > 16;
     static constexpr int kQBytes = kParts * S::kSteps * NT * 256;
-    static constexpr int kStages = DIM == 64 ? 6 : 3;
+    static constexpr int kStages = DIM == 64 ? 6 : (DIM == 256 ? 2 : 3);
     static constexpr int kJoin = S::kSteps * NT * 128 + NT * 128;  // floats of one warp's state
     // the next segment's copies start before the join of the warps, which then has memory of its own
     static constexpr bool kEarly = NT * DIM <= 256;
@@ -226,8 +225,12 @@ struct Config {
     static_assert(2 * kThreads * 4 <= kQBytes, "the sums of the parts' join fit where the queries were");
 };
 
-template <typename T, int KV, int DIM, int NT>
-__global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_constant__ Args a) {
+// BLOCKS: of an SM, at least. Three where the registers allow it (heads of up to 128, 8 rows of 16 bits) and there are items for
+// all: 256 sequences of 500 tokens, 8 key heads, 68 -> 59 us, heads of 64 (64 sequences of up to 8000 tokens) 91 -> 80 us. Few
+// items are cut into parts, whose join takes longer the more they are, and 190 registers run the loop
+// faster than 168: one sequence of 131071 tokens 61 us with two, 66 us with the code for three.
+template <typename T, int KV, int DIM, int NT, int BLOCKS>
+__global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __grid_constant__ Args a) {
     using S = Shape<DIM>;
     using C = Config<T, DIM, NT>;
     constexpr int kRows = 8 * NT;
@@ -930,15 +933,15 @@ __global__ void __launch_bounds__(kThreads, 2) kv_attention_kernel(const __grid_
     }
 }
 
-template <typename T, int KV, int DIM, int NT>
+template <typename T, int KV, int DIM, int NT, int BLOCKS>
 cudaError_t launch(const Args &a, cudaStream_t s) {
     constexpr int kSmem = Config<T, DIM, NT>::kSmem;
     static int blocks_per_sm = 0;
     if (blocks_per_sm == 0) {
-        cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<T, KV, DIM, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<T, KV, DIM, NT, BLOCKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         int n = 0;
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kv_attention_kernel<T, KV, DIM, NT>, kThreads, kSmem);
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kv_attention_kernel<T, KV, DIM, NT, BLOCKS>, kThreads, kSmem);
         if (e != cudaSuccess) return e;
         blocks_per_sm = n < 1 ? 1 : n;
     }
@@ -950,14 +953,18 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
     if (grid > Config<T, DIM, NT>::kMaxBlocks) grid = Config<T, DIM, NT>::kMaxBlocks;
     if (units < grid * kMinUnits) grid = static_cast<int64_t>((units + kMinUnits - 1) / kMinUnits);
     if (grid < 1) grid = 1;
-    return launch_behind(kv_attention_kernel<T, KV, DIM, NT>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmem, s, a);
+    return launch_behind(kv_attention_kernel<T, KV, DIM, NT, BLOCKS>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmem, s, a);
 }
 
 template <typename T, int KV, int DIM>
 cudaError_t by_rows(const Args &a, cudaStream_t s) {
     const int64_t rows = kv_block_rows(a.p.q_heads / a.p.c.heads, a.p.max_new);
-    if (rows == 8) return launch<T, KV, DIM, 1>(a, s);
-    return launch<T, KV, DIM, 2>(a, s);
+    if constexpr (DIM <= 128 && sizeof(T) == 2) {
+        const int64_t items = (a.p.tokens * (a.p.q_heads / a.p.c.heads) / 8 + a.p.seqs) * a.p.c.heads;
+        if (rows == 8 && items >= 2 * static_cast<int64_t>(num_sms())) return launch<T, KV, DIM, 1, 3>(a, s);
+    }
+    if (rows == 8) return launch<T, KV, DIM, 1, 2>(a, s);
+    return launch<T, KV, DIM, 2, 2>(a, s);
 }
 
 template <typename T, int KV>
