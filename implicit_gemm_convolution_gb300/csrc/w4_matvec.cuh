@@ -251,9 +251,10 @@ __global__ void __launch_bounds__(kThreads, 1) w4_matvec_kernel(const __grid_con
                         const int r = q / C::kRowPieces;
                         return dst + (ALIGNED ? r * 128 + (((q ^ r) & 7) * 16) : q * 16);
                     };
-                    if (rows > kRowTile && grp + kGroups <= groups && (unit > 0 || pass + f_tile > 0)) {
+                    if (rows >= kRowTile + 3 && grp + kGroups <= groups && (unit > 0 || pass + f_tile > 0)) {
                         // Every group is there, and there are rows behind the tile's and something before it: what is
-                        // copied beyond a row's ends lies inside the operands. Codes behind k meet zeros of x.
+                        // copied beyond a row's ends lies inside the operands (three rows: two zero points a row, eight
+                        // bytes copied). Codes behind k meet zeros of x.
 #pragma unroll
                         for (int i = 0; i < C::kPieces; ++i) {
                             const int q = lane + 32 * i;
