@@ -11,6 +11,7 @@ namespace {
 using om::Heads;
 
 constexpr int64_t kLim31 = (int64_t(1) << 31) - 1;
+constexpr int64_t kMargin = int64_t(1) << 16;  // positions and rows are rounded up in 32 bits
 
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? OM_OK : OM_ERR_CUDA; }
 
@@ -50,7 +51,7 @@ Block rows_of(const void *p, int64_t rows, int64_t cols, int64_t ld, int64_t byt
     b.lo = reinterpret_cast<uintptr_t>(p);
     b.rows = cols > 0 ? rows : 0;
     b.row = cols * bytes;
-    b.stride = ld * bytes;
+    b.stride = rows > 1 ? ld * bytes : b.row;  // the stride of a single row may be anything
     return b;
 }
 
@@ -105,7 +106,7 @@ int check_batch(int64_t seqs, int64_t tokens, const int32_t *block_table, int64_
                 const int32_t *lens, const int32_t *cu) {
     if (!block_table || !lens || !cu) return OM_ERR_NULL_PTR;
     if (width < 1) return OM_ERR_INVALID_ARG;
-    if (seqs > kLim31 || tokens > kLim31 || width > kLim31 / page) return OM_ERR_TOO_LARGE;
+    if (seqs > kLim31 || tokens > kLim31 || width > (kLim31 - kMargin) / page) return OM_ERR_TOO_LARGE;
     return aligned(block_table, 4) && aligned(lens, 4) && aligned(cu, 4) ? OM_OK : OM_ERR_ALIGNMENT;
 }
 
@@ -251,7 +252,7 @@ int om_kv_attention(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int6
     if (max_new < 1) return OM_ERR_INVALID_ARG;
     const int bst = check_batch(seqs, tokens, block_table, width, c.page, ctx_len, cu);
     if (bst != OM_OK) return bst;
-    if (q_heads > 65535 || tokens * q_heads > kLim31) return OM_ERR_TOO_LARGE;
+    if (q_heads > 65535 || tokens * q_heads > kLim31 - kMargin) return OM_ERR_TOO_LARGE;
     // pieces of 64 positions of every key head and eight query rows, at most
     const __int128 units = static_cast<__int128>(width * c.page / 64 + 1) * c.heads * (tokens * (q_heads / c.heads) / 8 + seqs);
     if (units > kLim31 - (1 << 20)) return OM_ERR_TOO_LARGE;

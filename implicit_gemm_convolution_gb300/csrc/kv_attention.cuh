@@ -34,6 +34,7 @@
 #pragma once
 
 #include <cfloat>
+#include <climits>
 #include <type_traits>
 
 #include "decode_device.cuh"
@@ -248,6 +249,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
     __shared__ float row_factor[kRows];
     __shared__ int2 row_seen[kRows];  // a row sees the positions in (x, y]
     __shared__ int scan[kWarps], scan_longest[kWarps], found_before;
+    __shared__ unsigned scan_doubt[kWarps];
     __shared__ Sequence found;
     __shared__ Part pending[2];  // parts of items of this block: its first and its last segment's
     __shared__ int arrived_last[2];
@@ -258,26 +260,36 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
     wait_for_earlier();
     // ---- this block's share of the units of all items (sequence, key head, row block)
     const int seqs = static_cast<int>(p.seqs);
-    int total = 0, longest = 0;
+    int64_t mine = 0;
+    int longest = 0;
+    bool falls = false;
 #pragma unroll 1
     for (int i = threadIdx.x; i < seqs; i += kThreads) {
         const Sequence s = sequence_of<kRows>(p, i, group);
-        total += heads * s.row_blocks * s.units;
+        mine += heads * s.row_blocks * s.units;
         longest = max(longest, s.units);
+        falls |= p.cu[i] > p.cu[i + 1];
     }
-    total = __reduce_add_sync(0xffffffffu, total);
+    int total = __reduce_add_sync(0xffffffffu, static_cast<int>(mine));
     longest = __reduce_max_sync(0xffffffffu, longest);
+    // Offsets that never decrease share the tokens out, and the host has bounded their units. Others can count a
+    // token for many sequences: nothing is done where their units might pass 32 bits.
+    const unsigned doubt = __reduce_or_sync(0xffffffffu, (falls ? 1u : 0u) | (mine > INT_MAX / kThreads ? 2u : 0u));
     if (lane == 0) {
+        scan_doubt[warp] = doubt;
         scan[warp] = total;
         scan_longest[warp] = longest;
     }
     __syncthreads();
     total = longest = 0;
+    unsigned doubts = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         total += scan[w];
         longest = max(longest, scan_longest[w]);
+        doubts |= scan_doubt[w];
     }
+    if (doubts == 3) return;
     const bool split = p.workspace != nullptr && longest > kWholeUnits;
     const int per = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), kMinUnits);
     if (static_cast<int64_t>(blockIdx.x) * per >= total) return;

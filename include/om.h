@@ -403,7 +403,8 @@ OM_API int om_rope_table(int64_t rows, int64_t rot, double base, int scaling, do
  *   page: 16, 32, 64 or 128 tokens; dim: 64, 128 or 256 (OM_ERR_UNSUPPORTED otherwise).
  * A batch of sequences reaches it through block_table [seqs][width] (the page of positions
  * j*page .. j*page + page - 1 of sequence b is block_table[b][j]) and cu [seqs + 1],
- * not decreasing from 0: sequence b has the tokens cu[b] .. cu[b + 1] - 1 of
+ * not decreasing from 0 (a call with other offsets has unspecified outputs, which may stay
+ * unwritten): sequence b has the tokens cu[b] .. cu[b + 1] - 1 of
  * the call's `tokens` tokens. Table entries outside [0, pages), positions outside the
  * table and offsets outside the batch are never followed: such tokens are not
  * stored, not attended to, and read as NaN. A page belongs to one sequence
@@ -468,7 +469,8 @@ OM_API size_t om_kv_workspace_bytes(int64_t kv_heads, int64_t q_heads, int64_t d
  *   lse: NULL, or [tokens][q_heads]: the natural log of the sum of exponentials.
  * A query that sees no token gives zeros and lse -inf. Memory behind masked tokens
  * (stale codes, pages outside the window) never reaches an output.
- * OM_ERR_TOO_LARGE where the table could hold 2^31 pieces of 64 positions of all heads and rows.
+ * OM_ERR_TOO_LARGE where the table could hold 2^31 pieces of 64 positions of all heads and rows; a table
+ * (of any call) reaches fewer than 2^31 - 2^16 positions.
  * workspace: NULL (each sequence and head by one block), or device memory, 16-byte
  * aligned, of om_kv_workspace_bytes, zeroed once before its first use: long
  * sequences are then split evenly over the GPU. Calls that may run at the same time

@@ -20,3 +20,17 @@ def test_w4_zero_points_to_their_last_byte(n, at):
     z = flat[at:].view(n, 2)
     z.copy_(Z)
     check_w4(om.w4_matvec(X, U, S, zeros=z, group=group), X, U, S, Z, k, group, "bf16")
+
+
+def test_attention_offsets_that_decrease_are_bounded():
+    """Every second sequence claims the whole batch: their units together pass 32 bits, so nothing is done."""
+    seqs, tokens, page, width = 4096, 2048, 128, 512
+    bt = Batch([page], [1], 8, 64, page, "int8", 3).device()
+    q = torch.ones(tokens, 32, 64, dtype=torch.bfloat16, device="cuda")
+    out = torch.full_like(q, -7.0)
+    cu = i32([0, tokens] * (seqs // 2) + [0])
+    table = torch.zeros(seqs, width, dtype=torch.int32, device="cuda")
+    ctx = torch.full((seqs,), page * width, dtype=torch.int32, device="cuda")
+    ws = om.new_kv_workspace(bt.cache, 32, tokens)
+    om.kv_attention(bt.cache, q, table, ctx, cu, tokens, out=out, workspace=ws)
+    assert (out == -7).all() and om.device_status() == 0
