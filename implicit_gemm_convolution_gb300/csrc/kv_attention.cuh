@@ -54,6 +54,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // Weights carry a factor of 2^6 and may exceed the running maximum's by 2^8 before it is
 // raised: below 2^14, inside 16-bit range, with the small ones above its subnormals.
 constexpr float kBias = 6.0f, kSlack = 8.0f;
+constexpr float kLeast = 4 * FLT_MIN;  // value scales below count relative to it
 
 template <int DIM>
 struct Shape {
@@ -86,6 +87,9 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+
+// 1 / x, and 0 for a sum of nothing.
+__device__ __forceinline__ float inverse(float x) { return x == 0.0f ? 0.0f : __fdiv_rn(1.0f, x); }
 
 __device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
@@ -412,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
     const int value_at[2] = {S::place(2 * c, DIM == 64 ? g / 2 : g) + (DIM == 64 ? g % 2 * 8 : 0),
                              S::place(2 * c + 1, DIM == 64 ? g / 2 : g) + (DIM == 64 ? g % 2 * 8 : 0)};
 
-    float o[S::kSteps][NT][4], m[NT][2], l[NT][2], vmax = FLT_MIN;
+    float o[S::kSteps][NT][4], m[NT][2], l[NT][2], vmax = kLeast;
     bool have = false;
 #pragma unroll 1
     for (;;) {
@@ -474,17 +478,19 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
         if (C::kEarly && more) begin_segment();
 
         if (have) {
-            // ---- sums over the lanes that share a column; value scales back into the sums
+            // ---- sums over the lanes that share a column. States are joined as weighted means: a mean is no larger than the
+            // values, where a sum with its scale could pass the range.
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1) l[nt][j] = __fadd_rn(l[nt][j], __shfl_xor_sync(0xffffffffu, l[nt][j], x));
+                    const float inv = inverse(l[nt][j]);
 #pragma unroll
                     for (int st = 0; st < S::kSteps; ++st) {
-                        o[st][nt][j] = __fmul_rn(o[st][nt][j], vmax);
-                        o[st][nt][j + 2] = __fmul_rn(o[st][nt][j + 2], vmax);
+                        o[st][nt][j] = __fmul_rn(__fmul_rn(o[st][nt][j], inv), vmax);
+                        o[st][nt][j + 2] = __fmul_rn(__fmul_rn(o[st][nt][j + 2], inv), vmax);
                     }
                 }
             // ---- join the warps: 2, 3 into 0, 1, then 1 into 0, in the fragments' own layout
@@ -512,10 +518,13 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             const float top = fmaxf(m[nt][j], om[j]);
-                            wa[j] = m[nt][j] == -INFINITY ? 0.0f : ex2(m[nt][j] - top);
-                            wb[j] = om[j] == -INFINITY ? 0.0f : ex2(om[j] - top);
+                            wa[j] = m[nt][j] == -INFINITY ? 0.0f : __fmul_rn(l[nt][j], ex2(m[nt][j] - top));
+                            wb[j] = om[j] == -INFINITY ? 0.0f : __fmul_rn(ol[j], ex2(om[j] - top));
                             m[nt][j] = top;
-                            l[nt][j] = __fmaf_rn(l[nt][j], wa[j], __fmul_rn(ol[j], wb[j]));
+                            l[nt][j] = __fadd_rn(wa[j], wb[j]);
+                            const float inv = inverse(l[nt][j]);
+                            wa[j] = __fmul_rn(wa[j], inv);
+                            wb[j] = __fmul_rn(wb[j], inv);
                         }
 #pragma unroll
                         for (int st = 0; st < S::kSteps; ++st) {
@@ -536,13 +545,12 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             const int col = nt * 8 + 2 * c + j;
-                            const float inv = l[nt][j] == 0.0f ? 0.0f : __fdiv_rn(1.0f, l[nt][j]);
                             // d of (step st, lane group g): consecutive in a lane
                             float *dst = join + col * (DIM + 4) + g * (DIM >= 128 ? 16 : 8);
 #pragma unroll
                             for (int st = 0; st < S::kSteps; ++st)
                                 *reinterpret_cast<float2 *>(dst + (DIM >= 128 ? st / 8 * 128 + st % 8 * 2 : st * 2)) =
-                                    make_float2(__fmul_rn(o[st][nt][j], inv), __fmul_rn(o[st][nt][j + 2], inv));
+                                    make_float2(o[st][nt][j], o[st][nt][j + 2]);
                             if (g == 0) write_lse(p, last, group, col, m[nt][j], l[nt][j]);
                         }
                 }
@@ -642,7 +650,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
         // ---- one pass over the warp's positions
         // raise: where the maximum goes up; less: what weights are taken relative to
         float raise[NT][2], less[NT][2];
-        vmax = FLT_MIN;
+        vmax = kLeast;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -690,7 +698,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
                     for (int j = 0; j < 2; ++j) kf[nt][j] = __fmul_rn(ka, factor[nt][j]);
                 odd_scale = !(fabsf(va) <= FLT_MAX);  // an infinite scale counts as NaN
                 if (!odd_scale && fabsf(va) > vmax) {  // sums relative to the largest scale so far
-                    const float r = __fdividef(vmax, fabsf(va));
+                    const float r = __fdividef(vmax * 0.25f, fabsf(va) * 0.25f);  // which divides up to 2^126
                     vmax = fabsf(va);
 #pragma unroll
                     for (int nt = 0; nt < NT; ++nt)
@@ -699,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
 #pragma unroll
                             for (int j = 0; j < 4; ++j) o[st][nt][j] = __fmul_rn(o[st][nt][j], r);
                 }
-                vr = odd_scale ? __int_as_float(0x7FC00000) : __fdividef(va, vmax);
+                vr = odd_scale ? __int_as_float(0x7FC00000) : __fdividef(va * 0.25f, vmax * 0.25f);
             }
 
             const uint8_t *const src = my_ring + src_at;
@@ -895,8 +903,9 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
         float mass = 0.0f;
 #pragma unroll 4
         for (int j = set; j < n; j += kSets) {
-            const float mj = weight[j * kRows + row], w = mj == -INFINITY ? 0.0f : ex2(mj - best);
-            mass = __fmaf_rn(__ldcg(slot_of(j) + kRows * DIM + kRows + row), w, mass);
+            const float mj = weight[j * kRows + row], lj = __ldcg(slot_of(j) + kRows * DIM + kRows + row);
+            const float w = mj == -INFINITY ? 0.0f : __fmul_rn(lj, ex2(mj - best));
+            mass = __fadd_rn(mass, w);
             weight[j * kRows + row] = w;
         }
         part_sum[threadIdx.x] = mass;
@@ -904,10 +913,9 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
         mass = 0.0f;
 #pragma unroll
         for (int s = 0; s < kSets; ++s) mass = __fadd_rn(mass, part_sum[s * kRows + row]);
-        if (set == 0) {
-            part_top[row] = mass;
-            write_lse(p, done, group, row, best, mass);
-        }
+        if (set == 0) write_lse(p, done, group, row, best, mass);
+        const float inv = inverse(mass);
+        for (int j = set; j < n; j += kSets) weight[j * kRows + row] = __fmul_rn(weight[j * kRows + row], inv);
         __syncthreads();
         float *const stage = weight + (n * kRows + 3) / 4 * 4;
         const int pairs = (done.rows + 1) / 2;  // of columns that are rows
@@ -934,11 +942,9 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
                     }
                 }
             }
-            const float sa = part_top[col], sb = part_top[col + 1];
-            const float ia = sa == 0.0f ? 0.0f : __fdiv_rn(1.0f, sa), ib = sb == 0.0f ? 0.0f : __fdiv_rn(1.0f, sb);
             float *dst = stage + col * (DIM + 4) + (DIM >= 128 ? st / 8 * 128 + gg * 16 + st % 8 * 2 : gg * 8 + st * 2);
-            *reinterpret_cast<float2 *>(dst) = make_float2(__fmul_rn(acc.x, ia), __fmul_rn(acc.z, ia));
-            *reinterpret_cast<float2 *>(dst + DIM + 4) = make_float2(__fmul_rn(acc.y, ib), __fmul_rn(acc.w, ib));
+            *reinterpret_cast<float2 *>(dst) = make_float2(acc.x, acc.z);
+            *reinterpret_cast<float2 *>(dst + DIM + 4) = make_float2(acc.y, acc.w);
         }
         __syncthreads();
         write_rows<T, DIM>(a, done, group, stage);

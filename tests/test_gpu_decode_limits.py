@@ -34,3 +34,12 @@ def test_attention_offsets_that_decrease_are_bounded():
     ws = om.new_kv_workspace(bt.cache, 32, tokens)
     om.kv_attention(bt.cache, q, table, ctx, cu, tokens, out=out, workspace=ws)
     assert (out == -7).all() and om.device_status() == 0
+
+
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("x,kind,dim,hq", [("f32", "int8", 128, 4), ("bf16", "e4m3", 128, 8), ("bf16", "int8", 64, 20), ("f32", "e4m3", 256, 2)])
+def test_attention_values_near_the_end_of_the_range(x, kind, dim, hq, workspace):
+    """Means of thousands of values near 1e36: their plain sums have no 32-bit float."""
+    bt = Batch([5000, 700], [1, 1], 2, dim, 64, kind, dim + hq)
+    bt.vs = bt.vs * 1e36
+    attend_and_check(bt, hq, x, workspace=workspace)
