@@ -88,8 +88,13 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// 1 / x, and 0 for a sum of nothing.
-__device__ __forceinline__ float inverse(float x) { return x == 0.0f ? 0.0f : __fdiv_rn(1.0f, x); }
+// 1 / x to a unit in the last place, and 0 for a sum of nothing. Sums lie far inside the range. (Three rounded
+// divisions in a row took 0.4 us of one short sequence's 6.9 us.)
+__device__ __forceinline__ float inverse(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return x == 0.0f ? 0.0f : y;
+}
 
 __device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
