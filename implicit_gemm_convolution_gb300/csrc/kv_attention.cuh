@@ -895,6 +895,14 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
         const int row = threadIdx.x % kRows, set = threadIdx.x / kRows;
         __syncthreads();
         float best = -INFINITY;
+        // the sums of a thread's first parts are loaded beside their maxima
+        constexpr int kFirst = 4;
+        float first_sum[kFirst];
+#pragma unroll
+        for (int i = 0; i < kFirst; ++i) {
+            const int j = set + i * kSets;
+            first_sum[i] = j < n ? __ldcg(slot_of(j) + kRows * DIM + kRows + row) : 0.0f;
+        }
 #pragma unroll 4
         for (int j = set; j < n; j += kSets) {
             const float mj = __ldcg(slot_of(j) + kRows * DIM + row);
@@ -906,13 +914,17 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
 #pragma unroll
         for (int s = 0; s < kSets; ++s) best = fmaxf(best, part_top[s * kRows + row]);
         float mass = 0.0f;
-#pragma unroll 4
-        for (int j = set; j < n; j += kSets) {
-            const float mj = weight[j * kRows + row], lj = __ldcg(slot_of(j) + kRows * DIM + kRows + row);
+        auto weigh = [&](int j, float lj) {
+            const float mj = weight[j * kRows + row];
             const float w = mj == -INFINITY ? 0.0f : __fmul_rn(lj, ex2(mj - best));
             mass = __fadd_rn(mass, w);
             weight[j * kRows + row] = w;
-        }
+        };
+#pragma unroll
+        for (int i = 0; i < kFirst; ++i)
+            if (set + i * kSets < n) weigh(set + i * kSets, first_sum[i]);
+#pragma unroll 1
+        for (int j = set + kFirst * kSets; j < n; j += kSets) weigh(j, __ldcg(slot_of(j) + kRows * DIM + kRows + row));
         part_sum[threadIdx.x] = mass;
         __syncthreads();
         mass = 0.0f;
