@@ -26,9 +26,9 @@
 // the block that finishes its last part. More and shorter shares (four times as many) ran no faster.
 //
 // Bound and measured (GB300; 6 680 GB/s is the measured copy bandwidth). HBM, 2 dim bytes a position and key head:
-// 64 sequences of up to 16384 tokens, 8 key heads of 128, 8 query heads each, bfloat16, whole numbers: 252 us,
-// 6 400 GB/s, 96 %. One sequence of 131071 tokens, float16, 8-bit floats, pages of 16: 60 us, 4 500 GB/s; about
-// 4 us until the first product, 45 us in the loop, 9 us for the joins. One of 331 tokens: 6.6 us, latency. 25
+// 64 sequences of up to 16384 tokens, 8 key heads of 128, 8 query heads each, bfloat16, whole numbers: 250 us,
+// 6 450 GB/s, 97 %. One sequence of 131071 tokens, float16, 8-bit floats, pages of 16: 60 us, 4 500 GB/s; about
+// 4 us until the first product, 45 us in the loop, 9 us for the joins. One of 331 tokens: 6.9 us, latency. 25
 // rows of 32-bit queries over a window of 4096: 69 us, 33 %: the products' issue (two parts of queries and of weights
 // each, rows in two blocks that each widen the codes).
 #pragma once
