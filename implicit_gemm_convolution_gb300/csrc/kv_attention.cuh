@@ -6,8 +6,8 @@
 // one pass over the positions with a running m. Codes are exact in 16-bit floats,
 // so both products run on the tensor cores with 32-bit sums; the query row is
 // scaled by a power of two to fill the 16-bit range and, for 32-bit queries, held in
-// two parts of 11 bits. The weights 2^(x - m) are two parts of 11 bits too, but one for
-// bfloat16, whose outputs have 8 bits. Value scales go into the weights, relative to the largest value scale met so far, so that they
+// two parts of 11 bits. The weights 2^(x - m) are two parts of 11 bits too, for every type: with one part, 16-bit outputs
+// were off by more than their own rounding. Value scales go into the weights, relative to the largest value scale met so far, so that they
 // stay in 16-bit range.
 //
 // Layout. The products are taken transposed, S^T = C Q^T and O^T = E^T P^T: codes
@@ -213,10 +213,9 @@ __device__ __forceinline__ void write_lse(const KvAttentionProblem &p, const Par
 template <typename T, int DIM, int NT>
 struct Config {
     using S = Shape<DIM>;
-    // 11-bit parts of queries and of weights: a float16 query is one part as it is, but its
-    // output is as exact as one rounded weight, so its weights take two
+    // 11-bit parts of queries: a 16-bit query is one part as it is
     static constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
-    static constexpr int kWeightParts = std::is_same_v<T, __nv_bfloat16> ? 1 : 2;
+    static constexpr int kWeightParts = 2;
     // query fragments stay in registers where they fit beside the sums
     static constexpr bool kQShared = NT * kParts * S::kSteps > 16;
     static constexpr int kQBytes = kParts * S::kSteps * NT * 256;
