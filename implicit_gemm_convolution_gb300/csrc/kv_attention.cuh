@@ -96,6 +96,10 @@ __device__ __forceinline__ float inverse(float x) {
     return x == 0.0f ? 0.0f : y;
 }
 
+// A part's sum of weights, taken relative to the maximum of all parts. Without a maximum a part saw nothing (its sum is 0) or
+// scores that are all NaN (its sum is NaN, and stays).
+__device__ __forceinline__ float joined(float sum, float top, float best) { return top == -INFINITY ? sum : __fmul_rn(sum, ex2(top - best)); }
+
 __device__ __forceinline__ void mma(float *d, const uint32_t *a, uint32_t b0, uint32_t b1) {
     asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
@@ -522,8 +526,8 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
 #pragma unroll
                         for (int j = 0; j < 2; ++j) {
                             const float top = fmaxf(m[nt][j], om[j]);
-                            wa[j] = m[nt][j] == -INFINITY ? 0.0f : __fmul_rn(l[nt][j], ex2(m[nt][j] - top));
-                            wb[j] = om[j] == -INFINITY ? 0.0f : __fmul_rn(ol[j], ex2(om[j] - top));
+                            wa[j] = joined(l[nt][j], m[nt][j], top);
+                            wb[j] = joined(ol[j], om[j], top);
                             m[nt][j] = top;
                             l[nt][j] = __fadd_rn(wa[j], wb[j]);
                             const float inv = inverse(l[nt][j]);
@@ -915,7 +919,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
         float mass = 0.0f;
         auto weigh = [&](int j, float lj) {
             const float mj = weight[j * kRows + row];
-            const float w = mj == -INFINITY ? 0.0f : __fmul_rn(lj, ex2(mj - best));
+            const float w = joined(lj, mj, best);
             mass = __fadd_rn(mass, w);
             weight[j * kRows + row] = w;
         };

@@ -467,7 +467,8 @@ OM_API size_t om_kv_workspace_bytes(int64_t kv_heads, int64_t q_heads, int64_t d
  * cache's heads; query head h reads head h / (q_heads / heads).
  *   out[t][h] = sum_i softmax_i(scale * q[t][h] . key_i) value_i, of q's dtype;
  *   lse: NULL, or [tokens][q_heads]: the natural log of the sum of exponentials.
- * A query that sees no token gives zeros and lse -inf. Memory behind masked tokens
+ * A query that sees no token gives zeros and lse -inf; one with a score that is NaN (its own elements, a
+ * page's scale) gives NaN for both. Memory behind masked tokens
  * (stale codes, pages outside the window) never reaches an output.
  * OM_ERR_TOO_LARGE where the table could hold 2^31 pieces of 64 positions of all heads and rows; a table
  * (of any call) reaches fewer than 2^31 - 2^16 positions.

@@ -62,3 +62,43 @@ def test_16_bit_outputs_are_rounded_once(x, dim, kind):
     tol = before_rounding(bt, big, mag)
     off = np.abs(ref.f64(out) - want)
     assert (off <= tol + half_unit(np.abs(want) + tol, x)).all(), int((off > tol + half_unit(np.abs(want) + tol, x)).sum())
+
+
+# ------------------------------------------------------------------ not a number
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("x,kind,dim", [("f32", "int8", 128), ("bf16", "e4m3", 64), ("f16", "int8", 256)])
+def test_lse_of_a_query_that_is_not_a_number(x, kind, dim, workspace):
+    """Its outputs and its log-sum-exp are NaN, whatever the length and the split; the other rows' are not."""
+    bt = Batch([1, 64, 300, 5000], [1, 1, 2, 1], 2, dim, 16, kind, dim)
+    q = torch.randn(5, 4, dim, generator=gen(2), device="cuda").to(ref.TORCH[x])
+    bad = torch.zeros(5, 4, dtype=torch.bool, device="cuda")
+    for t, h in ((0, 1), (1, 3), (2, 0), (4, 2)):
+        q[t, h, dim - 3] = float("nan")
+        bad[t, h] = True
+    out, lse = attend(bt, q, workspace=workspace)
+    assert (torch.isnan(out).all(-1) == bad).all() and (torch.isnan(out).any(-1) == bad).all()
+    assert (torch.isnan(lse) == bad).all() and torch.isfinite(lse[~bad]).all()
+
+
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("page,ctx,at", [(64, 50, 0), (16, 64, 2), (16, 64, 0), (64, 640, 3), (128, 9000, 40), (16, 9000, 562)])
+def test_lse_of_a_key_page_that_is_not_a_number(page, ctx, at, workspace):
+    """The page a warp's whole range, a part of it, or a part of one block's share."""
+    bt = Batch([ctx, ctx], [1, 1], 1, 128, page, "int8", ctx + page)
+    bt.ks[int(bt.table_np[0][at])] = float("nan")
+    q = torch.randn(2, 4, 128, generator=gen(1), device="cuda")
+    out, lse = attend(bt, q, workspace=workspace)
+    assert torch.isnan(out[0]).all() and torch.isnan(lse[0]).all()
+    assert torch.isfinite(out[1]).all() and torch.isfinite(lse[1]).all()
+
+
+def test_lse_of_rows_that_do_not_see_the_page():
+    """Three drafts around the first token of a page whose key scale is NaN: the ones behind it only."""
+    bt = Batch([66, 130], [4, 3], 1, 64, 64, "e4m3", 9)
+    bt.ks[int(bt.table_np[0][1])] = float("nan")
+    bt.ks[int(bt.table_np[1][2])] = float("nan")
+    q = torch.randn(7, 8, 64, generator=gen(1), device="cuda").bfloat16()
+    out, lse = attend(bt, q)
+    seen = torch.tensor([0, 0, 1, 1, 0, 1, 1], dtype=torch.bool, device="cuda")[:, None]  # positions 62 .. 65, 127 .. 129
+    assert (torch.isnan(out).all(-1) == seen).all() and (torch.isnan(out).any(-1) == seen).all()
+    assert (torch.isnan(lse) == seen).all() and torch.isfinite(lse[~seen[:, 0]]).all()
