@@ -6,9 +6,13 @@
 // one pass over the positions with a running m. Codes are exact in 16-bit floats,
 // so both products run on the tensor cores with 32-bit sums; the query row is
 // scaled by a power of two to fill the 16-bit range and, for 32-bit queries, held in
-// two parts of 11 bits. The weights 2^(x - m) are two parts of 11 bits too, for every type: with one part, 16-bit outputs
-// were off by more than their own rounding. Value scales go into the weights, relative to the largest value scale met so far, so that they
-// stay in 16-bit range.
+// two parts of 11 bits. The weights are two parts of 11 bits too, for every type: with one part, 16-bit outputs
+// were off by more than their own rounding.
+//
+// Range. What goes to the tensor cores for a position is w = 2^(x - m) s / u with a unit u of the row's sums, a power of two
+// that is set anew when the largest |w| of a tile (16 positions of a page) leaves [2^-1, 2^15]. So a weight is off by no more than 2^-22 of
+// itself or 2^-24 of its tile's largest, however far the tile's scores and scale are from other tiles' (relative to the
+// largest scale met, pages with smaller ones lost their bits).
 //
 // Layout. The products are taken transposed, S^T = C Q^T and O^T = E^T P^T: codes
 // are the 16-row operand and the query rows (query tokens times the heads that
@@ -51,10 +55,14 @@ constexpr int kUnit = kTile * kWarps;  // positions of a unit of work
 constexpr int kMinUnits = 4;           // a block takes at least so many units
 constexpr int kWholeUnits = 12;        // items of no more units are not split: joining parts takes longer than that many units
 constexpr float kLog2e = 1.4426950408889634f;
-// Weights carry a factor of 2^6 and may exceed the running maximum's by 2^8 before it is
-// raised: below 2^14, inside 16-bit range, with the small ones above its subnormals.
-constexpr float kBias = 6.0f, kSlack = 8.0f;
-constexpr float kLeast = 4 * FLT_MIN;  // value scales below count relative to it
+// A tile's largest weight is 2^8 as its unit is set, and may go to 2^15 and 2^-1 with the same one: inside 16-bit
+// range, its second part above the subnormals. The maximum may lag behind while exponentials are below 2^40.
+constexpr float kBias = 8.0f, kMost = 32768.0f, kLeast = 0.5f, kMostExp = 1099511627776.0f;
+constexpr float kNone = -FLT_MAX;  // the maximum of no scores
+// Units from 2^-100 to 2^126; a smaller one may not raise sums above 2^100.
+constexpr float kLeastUnit = 7.8886090522101181e-31f;
+constexpr unsigned kMostUnit = 253u << 23;
+__device__ __forceinline__ float reciprocal(float power) { return __uint_as_float((254u << 23) - __float_as_uint(power)); }
 
 template <int DIM>
 struct Shape {
@@ -219,7 +227,6 @@ struct Config {
     using S = Shape<DIM>;
     // 11-bit parts of queries: a 16-bit query is one part as it is
     static constexpr int kParts = sizeof(T) == 4 ? 2 : 1;
-    static constexpr int kWeightParts = 2;
     // query fragments stay in registers where they fit beside the sums
     static constexpr bool kQShared = NT * kParts * S::kSteps > 16;
     static constexpr int kQBytes = kParts * S::kSteps * NT * 256;
@@ -421,10 +428,11 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
     // a lane's places in a tile: keys by (row g, pieces c, c + 4, ...), values by (rows 2 c and 2 c + 1,
     // piece g, or half a piece)
     const int key_at = S::place(g, c);
+    const unsigned column_bit = 1u << (2 * c);
     const int value_at[2] = {S::place(2 * c, DIM == 64 ? g / 2 : g) + (DIM == 64 ? g % 2 * 8 : 0),
                              S::place(2 * c + 1, DIM == 64 ? g / 2 : g) + (DIM == 64 ? g % 2 * 8 : 0)};
 
-    float o[S::kSteps][NT][4], m[NT][2], l[NT][2], vmax = kLeast;
+    float o[S::kSteps][NT][4], m[NT][2], l[NT][2], per_unit[NT][2];
     bool have = false;
 #pragma unroll 1
     for (;;) {
@@ -487,18 +495,19 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
 
         if (have) {
             // ---- sums over the lanes that share a column. States are joined as weighted means: a mean is no larger than the
-            // values, where a sum with its scale could pass the range.
+            // values, where a sum with its unit could pass the range.
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
 #pragma unroll
                     for (int x = 4; x < 32; x <<= 1) l[nt][j] = __fadd_rn(l[nt][j], __shfl_xor_sync(0xffffffffu, l[nt][j], x));
-                    const float inv = inverse(l[nt][j]);
+                    const float inv = inverse(l[nt][j]), back = reciprocal(per_unit[nt][j]);
+                    if (m[nt][j] == kNone) m[nt][j] = -INFINITY;
 #pragma unroll
                     for (int st = 0; st < S::kSteps; ++st) {
-                        o[st][nt][j] = __fmul_rn(__fmul_rn(o[st][nt][j], inv), vmax);
-                        o[st][nt][j + 2] = __fmul_rn(__fmul_rn(o[st][nt][j + 2], inv), vmax);
+                        o[st][nt][j] = __fmul_rn(__fmul_rn(o[st][nt][j], inv), back);
+                        o[st][nt][j + 2] = __fmul_rn(__fmul_rn(o[st][nt][j + 2], inv), back);
                     }
                 }
             // ---- join the warps: 2, 3 into 0, 1, then 1 into 0, in the fragments' own layout
@@ -656,9 +665,6 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
         }
 
         // ---- one pass over the warp's positions
-        // raise: where the maximum goes up; less: what weights are taken relative to
-        float raise[NT][2], less[NT][2];
-        vmax = kLeast;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -667,16 +673,17 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
                 for (int j = 0; j < 4; ++j) o[s][nt][j] = 0.0f;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
-                m[nt][j] = raise[nt][j] = -INFINITY;
-                l[nt][j] = less[nt][j] = 0.0f;
+                m[nt][j] = kNone;
+                l[nt][j] = 0.0f;
+                per_unit[nt][j] = 1.0f;
             }
         }
-        float kf[NT][2], vr = 0.0f;
+        float kf[NT][2], vf[NT][2], value = 0.0f;  // vf: the page's value scale by the columns' units
         bool next_scaled = false;
         bool page_ok = false, odd_scale = false;
         const uint8_t *const my_ring = smem + warp * C::kRing;
         int src_at = 0;
-        bool c_new = true;
+        bool c_new = true, empty = true;  // empty: no sums yet
 #pragma unroll 1
         for (int pos = w0; pos < w1; pos += kTile) {
             cp_wait<C::kStages - 2>();
@@ -705,17 +712,11 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
 #pragma unroll
                     for (int j = 0; j < 2; ++j) kf[nt][j] = __fmul_rn(ka, factor[nt][j]);
                 odd_scale = !(fabsf(va) <= FLT_MAX);  // an infinite scale counts as NaN
-                if (!odd_scale && fabsf(va) > vmax) {  // sums relative to the largest scale so far
-                    const float r = __fdividef(vmax * 0.25f, fabsf(va) * 0.25f);  // which divides up to 2^126
-                    vmax = fabsf(va);
+                value = va;
 #pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                        for (int st = 0; st < S::kSteps; ++st)
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) o[st][nt][j] = __fmul_rn(o[st][nt][j], r);
-                }
-                vr = odd_scale ? __int_as_float(0x7FC00000) : __fdividef(va * 0.25f, vmax * 0.25f);
+                    for (int j = 0; j < 2; ++j) vf[nt][j] = __fmul_rn(value, per_unit[nt][j]);
             }
 
             const uint8_t *const src = my_ring + src_at;
@@ -754,6 +755,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) s[nt][j] = __fmul_rn(__fadd_rn(s[nt][j], s1[nt][j]), kf[nt][j & 1]);
+            unsigned sees_none = 0;  // columns
             if (!(page_ok && pos >= lo_last && pos <= all_see)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
@@ -763,15 +765,33 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
                         const int t = pos + g + (j & 2) * 4;
                         if (!page_ok || t <= seen[j & 1].x || t > seen[j & 1].y) s[nt][j] = -INFINITY;
                     }
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        if (!page_ok || pos + kTile - 1 <= seen[j].x || pos > seen[j].y) sees_none |= column_bit << (8 * nt + j);
                 }
             }
-            // the maximum is raised only when a weight would pass the slack
-            bool high = false;
+            float e[NT][4];
+            for (bool again = false;; again = true) {
+                // a bit for each column whose largest weight is above the low end, and one for what is above the top
+                unsigned fit = value == 0.0f || odd_scale ? (1u << kRows) - 1 : sees_none;
+                bool high = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int j = 0; j < 2; ++j) high |= fmaxf(s[nt][j], s[nt][j + 2]) > raise[nt][j];
-            if (__any_sync(0xffffffffu, high)) {
+                    for (int j = 0; j < 2; ++j) {
+                        const float less = m[nt][j] - kBias;
+                        e[nt][j] = ex2(__fsub_rn(s[nt][j], less));
+                        e[nt][j + 2] = ex2(__fsub_rn(s[nt][j + 2], less));
+                        const float top = fmaxf(e[nt][j], e[nt][j + 2]), w = fabsf(__fmul_rn(top, vf[nt][j]));
+                        if (w >= kLeast) fit |= column_bit << (8 * nt + j);
+                        high |= w > kMost || top > kMostExp;
+                    }
+                if (high) fit |= 1u << 31;
+                if (again || __reduce_or_sync(0xffffffffu, fit) == (1u << kRows) - 1) break;
+                // the columns whose largest weight is outside: a new maximum if it is above the old one, and a new unit
+                float by[NT][2];  // what the sums are multiplied by
+                int up[NT][2];    // the unit goes down by so many powers of two
+                bool changed = false, smaller = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -780,41 +800,73 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
                         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-                        const float top = fmaxf(m[nt][j], x);
-                        const float r = m[nt][j] == -INFINITY ? 0.0f : ex2(m[nt][j] - top);
-                        m[nt][j] = top;
-                        raise[nt][j] = top + kSlack;
-                        less[nt][j] = top == -INFINITY ? 0.0f : top - kBias;
-                        l[nt][j] = __fmul_rn(l[nt][j], r);
-#pragma unroll
-                        for (int st = 0; st < S::kSteps; ++st) {
-                            o[st][nt][j] = __fmul_rn(o[st][nt][j], r);
-                            o[st][nt][j + 2] = __fmul_rn(o[st][nt][j + 2], r);
+                        const float top = ex2(x - (m[nt][j] - kBias)), w = fabsf(__fmul_rn(top, vf[nt][j]));
+                        by[nt][j] = 1.0f;
+                        up[nt][j] = 0;
+                        if (x > kNone && !(w >= kLeast && w <= kMost && top <= kMostExp)) {
+                            if (x > m[nt][j]) {
+                                by[nt][j] = ex2(m[nt][j] - x);
+                                m[nt][j] = x;
+                                l[nt][j] = __fmul_rn(l[nt][j], by[nt][j]);
+                            }
+                            if (value != 0.0f && !odd_scale) {
+                                const float to = fmaxf(__fmul_rn(ex2(x - m[nt][j]), fabsf(value)), kLeastUnit);
+                                const unsigned unit = min(__float_as_uint(to) & 0x7f800000u, kMostUnit);
+                                up[nt][j] = (static_cast<int>((254u << 23) - unit) - static_cast<int>(__float_as_uint(per_unit[nt][j]))) >> 23;
+                                smaller |= up[nt][j] > 0;
+                            }
+                            changed = true;
                         }
                     }
+                const bool sums = !empty && __any_sync(0xffffffffu, changed);
+                if (sums && __any_sync(0xffffffffu, smaller)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            unsigned most = 0;  // magnitudes compare as their bits
+#pragma unroll
+                            for (int st = 0; st < S::kSteps; ++st)
+                                most = max(most, max(__float_as_uint(o[st][nt][j]) & 0x7fffffffu, __float_as_uint(o[st][nt][j + 2]) & 0x7fffffffu));
+#pragma unroll
+                            for (int i = 4; i < 32; i <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, i));
+                            up[nt][j] = min(up[nt][j], max(227 - static_cast<int>(most >> 23), 0));
+                        }
+                }
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        per_unit[nt][j] = __uint_as_float(__float_as_uint(per_unit[nt][j]) + (static_cast<unsigned>(up[nt][j]) << 23));
+                        vf[nt][j] = __fmul_rn(value, per_unit[nt][j]);
+                        by[nt][j] = __fmul_rn(by[nt][j], __uint_as_float(static_cast<unsigned>(min(max(up[nt][j], -126), 127) + 127) << 23));
+                    }
+                if (sums) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                        for (int st = 0; st < S::kSteps; ++st)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) o[st][nt][j] = __fmul_rn(o[st][nt][j], by[nt][j & 1]);
+                }
             }
-            uint32_t pf[C::kWeightParts][NT][2];
+            empty = false;
+            uint32_t pf[2][NT][2];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float w[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float e = ex2(__fsub_rn(s[nt][j], less[nt][j & 1]));
-                    l[nt][j & 1] = __fadd_rn(l[nt][j & 1], e);
-                    w[j] = __fmul_rn(e, vr);
-                    if (odd_scale && e == 0.0f) w[j] = 0.0f;  // hidden: its scale does not count
+                    l[nt][j & 1] = __fadd_rn(l[nt][j & 1], e[nt][j]);
+                    w[j] = __fmul_rn(e[nt][j], vf[nt][j & 1]);
+                    if (odd_scale && s[nt][j] == -INFINITY) w[j] = 0.0f;  // hidden: its scale does not count
                 }
-                uint32_t x[2] = {pack_half(w[0], w[1]), pack_half(w[2], w[3])};
-#pragma unroll
-                for (int part_i = 0; part_i < C::kWeightParts; ++part_i) {
-                    pf[part_i][nt][0] = transpose8(x[0]);
-                    pf[part_i][nt][1] = transpose8(x[1]);
-                    if (part_i + 1 < C::kWeightParts) {
-                        const float2 y = unpack_half(x[0]), z = unpack_half(x[1]);
-                        x[0] = pack_half(w[0] - y.x, w[1] - y.y);
-                        x[1] = pack_half(w[2] - z.x, w[3] - z.y);
-                    }
-                }
+                const uint32_t x[2] = {pack_half(w[0], w[1]), pack_half(w[2], w[3])};
+                const float2 y = unpack_half(x[0]), z = unpack_half(x[1]);
+                pf[0][nt][0] = transpose8(x[0]);
+                pf[0][nt][1] = transpose8(x[1]);
+                pf[1][nt][0] = transpose8(pack_half(w[0] - y.x, w[1] - y.y));
+                pf[1][nt][1] = transpose8(pack_half(w[2] - z.x, w[3] - z.y));
             }
             const uint8_t *const vsrc = src + kTile * DIM;
 #pragma unroll
@@ -846,15 +898,15 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             if constexpr (kParts == 1) {
-#pragma unroll
-                                for (int part_i = 0; part_i < C::kWeightParts; ++part_i) mma(o[st][nt], frag, pf[part_i][nt][0], pf[part_i][nt][1]);
+                                mma(o[st][nt], frag, pf[1][nt][0], pf[1][nt][1]);
+                                mma(o[st][nt], frag, pf[0][nt][0], pf[0][nt][1]);
                             } else {
                                 // 32-bit outputs: the tensor cores cut their sums off instead of rounding them, which over
                                 // thousands of positions adds up; a tile's sum is joined by a rounded addition (relative
                                 // error over 60000 positions 2.5e-6 -> below 1e-6)
                                 float tile_sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-                                for (int part_i = C::kWeightParts - 1; part_i >= 0; --part_i) mma(tile_sum, frag, pf[part_i][nt][0], pf[part_i][nt][1]);
+                                mma(tile_sum, frag, pf[1][nt][0], pf[1][nt][1]);
+                                mma(tile_sum, frag, pf[0][nt][0], pf[0][nt][1]);
 #pragma unroll
                                 for (int j = 0; j < 4; ++j) o[st][nt][j] = __fadd_rn(o[st][nt][j], tile_sum[j]);
                             }

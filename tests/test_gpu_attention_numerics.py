@@ -102,3 +102,68 @@ def test_lse_of_rows_that_do_not_see_the_page():
     seen = torch.tensor([0, 0, 1, 1, 0, 1, 1], dtype=torch.bool, device="cuda")[:, None]  # positions 62 .. 65, 127 .. 129
     assert (torch.isnan(out).all(-1) == seen).all() and (torch.isnan(out).any(-1) == seen).all()
     assert (torch.isnan(lse) == seen).all() and torch.isfinite(lse[~seen[:, 0]]).all()
+
+
+# ------------------------------------------------------------------ scales far apart
+def two_sorts(kind, dim, x, ratio, far_score, ctx=128, new=1, seed=0):
+    """Pages in turn of two sorts: even ones with a value scale `ratio` times the odd ones' and scores `far_score` lower."""
+    bt = Batch([ctx, ctx - 5], [new, 1], 2, dim, 16, kind, dim + seed, width_extra=0)
+    near = np.concatenate([row[1::2] for row in bt.table_np])
+    far = np.concatenate([row[0::2] for row in bt.table_np])
+    low = -100.0 if kind == "int8" else -112.0
+    raw = torch.randint(-3, 4, bt.k.shape, generator=gen(seed + 1), device="cuda").float()
+    raw[torch.from_numpy(far).cuda()] = low
+    bt.k = raw.to(bt.k.dtype)
+    bt.ks = torch.full_like(bt.ks, 0.02)
+    bt.ks[torch.from_numpy(far).cuda()] = far_score / (0.25 * -low * dim ** 0.5)
+    bt.vs[torch.from_numpy(far).cuda()] = bt.vs[torch.from_numpy(far).cuda()] * ratio
+    q = torch.full((new + 1, 6, dim), 0.25, device="cuda").to(ref.TORCH[x])
+    return bt, q, near, far
+
+
+def check_two_sorts(bt, q, x, big, what, window=0):
+    out, lse = attend(bt, q, window=window)
+    want, wl, mag, _ = exact(bt, q, window)
+    tol = before_rounding(bt, np.full(mag.shape[:2], big), mag)
+    off = np.abs(ref.f64(out) - want)
+    limit = tol + half_unit(np.abs(want) + tol, x)
+    assert (off <= limit).all(), f"{what}: {float((off / limit).max())} of the tolerance"
+    assert (np.abs(ref.f64(lse) - wl) <= 2e-5 + 2.0 ** -20 * np.abs(wl)).all()
+
+
+@pytest.mark.parametrize("x,kind,dim", [("f32", "int8", 128), ("f32", "e4m3", 64), ("f32", "int8", 256), ("bf16", "int8", 128), ("f16", "e4m3", 128)])
+@pytest.mark.parametrize("ratio", [1e3, 1e5, 1e7, 1e10, 1e20, 1e-10])
+def test_pages_that_do_not_count_take_no_bits(ratio, x, kind, dim):
+    """All attention is on pages whose value scale is far from the others'."""
+    bt, q, _, _ = two_sorts(kind, dim, x, ratio, 150.0)
+    check_two_sorts(bt, q, x, 0.3, f"ratio {ratio}")  # big: 0.25 . 3 . 0.02 . dim^0.5 of the attended ones
+
+
+@pytest.mark.parametrize("kind,dim", [("int8", 128), ("e4m3", 64), ("int8", 256)])
+@pytest.mark.parametrize("ratio", [1e3, 1e6, 1e10, 1e16])
+def test_pages_that_count_alike(ratio, kind, dim):
+    """Weights smaller by as much as the value scales are larger: both sorts are half of the output."""
+    bt, q, _, _ = two_sorts(kind, dim, "f32", ratio, float(np.log(ratio)))
+    check_two_sorts(bt, q, "f32", float(np.log(ratio)) + 0.3, f"ratio {ratio}")
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+def test_pages_that_another_row_sees_take_no_bits(x):
+    """Four drafts and a window that ends inside the huge page for the first of them: the others do not see it."""
+    bt, q, _, _ = two_sorts("int8", 128, x, 1.0, 0.5, ctx=260, new=4)
+    huge = int(bt.table_np[0][2])  # positions 32 .. 47
+    bt.vs[huge] = bt.vs[huge] * 1e9
+    window = 257 - 48 + 1  # of the queries at 256 .. 259: the first sees 47 and on, the others 48 and on
+    check_two_sorts(bt, q, x, 0.8, "window", window=window)
+
+
+def test_values_of_which_the_heaviest_is_zero():
+    """The first token takes nearly all of the weight and its value is 0: what is left is the sum of the small weights."""
+    bt, q, _, _ = two_sorts("int8", 128, "f32", 1.0, 0.1, ctx=512)
+    for b in range(2):
+        first = int(bt.table_np[b][0])
+        bt.v[first, :, 0] = 0
+        bt.k[first, :, 0] = 100
+        bt.k[first, :, 1:] = 0
+        bt.ks[first] = 12.0 / (0.25 * 100 * 128 ** 0.5)  # 12 above the others
+    check_two_sorts(bt, q, "f32", 12.3, "a heavy token of value 0")
