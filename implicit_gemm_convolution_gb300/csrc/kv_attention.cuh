@@ -432,6 +432,56 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
     const int value_at[2] = {S::place(2 * c, DIM == 64 ? g / 2 : g) + (DIM == 64 ? g % 2 * 8 : 0),
                              S::place(2 * c + 1, DIM == 64 ? g / 2 : g) + (DIM == 64 ? g % 2 * 8 : 0)};
 
+    // Value codes that are NaN, in a tile that not every row sees as a whole: a weight of 0 would not hide them. Rows that see one
+    // become NaN in its dimension, and the code becomes 0. o, and the tile's values at vsrc.
+    auto hide_nan_codes = [&](float (&o)[S::kSteps][NT][4], uint8_t *vsrc, int pos) {
+        auto is_nan = [](uint32_t x) { return ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; };
+        uint32_t any = 0;
+#pragma unroll
+        for (int j = 0; j < S::kCopies; ++j) {
+            const uint4 x = *reinterpret_cast<const uint4 *>(vsrc + lane * 16 + j * 512);
+            any |= is_nan(x.x) | is_nan(x.y) | is_nan(x.z) | is_nan(x.w);
+        }
+        if (!__any_sync(0xffffffffu, any != 0)) return;
+#pragma unroll 1
+        for (int r = 0; r < kTile; ++r) {
+            bool sees[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const int2 seen = row_seen[nt * 8 + 2 * c + j];
+                    sees[nt][j] = pos + r > seen.x && pos + r <= seen.y;
+                }
+#pragma unroll
+            for (int i = 0; i < S::kValueChunks; ++i) {
+                // a lane's dimensions: the piece g, or half a piece, as in the product
+                constexpr int kWords = S::kValueBytes / 4;
+                uint32_t *const at = reinterpret_cast<uint32_t *>(vsrc + S::place(r & 7, DIM == 64 ? g / 2 : g) + (DIM == 64 ? g % 2 * 8 : 0) + r / 8 * 8 * DIM + i * 128);
+                uint32_t x[kWords];
+#pragma unroll
+                for (int w = 0; w < kWords; ++w) {
+                    x[w] = at[w];
+                    const uint32_t bad = is_nan(x[w]);
+                    x[w] &= ~((bad >> 7) * 0xffu);
+#pragma unroll
+                    for (int byte = 0; byte < 4; ++byte)
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+                                if (sees[nt][j] && (bad >> (8 * byte) & 0x80u)) o[i * 2 * kWords + 2 * w + byte / 2][nt][j + byte % 2 * 2] = __int_as_float(0x7FC00000);
+                }
+                __syncwarp();  // the four lanes of the piece have read it
+                if (c == 0) {
+#pragma unroll
+                    for (int w = 0; w < kWords; ++w) at[w] = x[w];
+                }
+            }
+        }
+        __syncwarp();
+    };
+
     float o[S::kSteps][NT][4], m[NT][2], l[NT][2], per_unit[NT][2];
     bool have = false;
 #pragma unroll 1
@@ -769,6 +819,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
                     for (int j = 0; j < 2; ++j)
                         if (!page_ok || pos + kTile - 1 <= seen[j].x || pos > seen[j].y) sees_none |= column_bit << (8 * nt + j);
                 }
+                if constexpr (KV == OM_E4M3) hide_nan_codes(o, smem + warp * C::kRing + src_at + kTile * DIM, pos);
             }
             float e[NT][4];
             for (bool again = false;; again = true) {

@@ -167,3 +167,48 @@ def test_values_of_which_the_heaviest_is_zero():
         bt.k[first, :, 1:] = 0
         bt.ks[first] = 12.0 / (0.25 * 100 * 128 ** 0.5)  # 12 above the others
     check_two_sorts(bt, q, "f32", 12.3, "a heavy token of value 0")
+
+
+# ------------------------------------------------------------------ masked codes that are not numbers
+def check_with_nan(bt, q, x, window):
+    out, lse = attend(bt, q, window=window)
+    want, wl, mag, big = exact(bt, q, window)
+    got = ref.f64(out)
+    assert (np.isnan(got) == np.isnan(want)).all(), f"{int((np.isnan(got) != np.isnan(want)).sum())} outputs"
+    ok = ~np.isnan(want)
+    tol = before_rounding(bt, big, np.where(ok, mag, 0.0))
+    assert (np.abs(got - want)[ok] <= (tol + half_unit(np.abs(want) + tol, x))[ok]).all()
+    assert (np.abs(ref.f64(lse) - wl) <= 1e-4).all()
+    return np.isnan(want)
+
+
+@pytest.mark.parametrize("x", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("hkv,hq", [(2, 2), (1, 6)])
+def test_value_codes_before_the_window_in_its_first_tile(hkv, hq, dim, x):
+    bt = Batch([70, 91], [1, 1], hkv, dim, 32, "e4m3", dim)
+    for b, c in enumerate(bt.ctx):
+        lo = c - 20
+        for t in range(lo // 16 * 16, lo):
+            bt.v.view(torch.int8)[int(bt.table_np[b][t // 32]), :, t % 32] = 0x7F
+    q = torch.randn(2, hq, dim, generator=gen(1), device="cuda").to(ref.TORCH[x])
+    assert not check_with_nan(bt, q, x, 20).any()
+
+
+@pytest.mark.parametrize("x", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("hkv,hq", [(2, 2), (1, 6)])
+@pytest.mark.parametrize("window", [0, 20])
+def test_value_codes_that_some_rows_see(window, hkv, hq, dim, x):
+    """Drafts of which the later ones see the code, and a window that has left it behind for them: the rows that see it
+    are NaN in its dimension, and nothing else is."""
+    bt = Batch([45, 300], [3, 5], hkv, dim, 32, "e4m3", dim)
+    raw = bt.v.view(torch.int8)
+    at = lambda b, t: (int(bt.table_np[b][t // 32]), slice(None), t % 32)
+    for t, d, code in ((44, 3, 0x7F), (44, dim - 1, -1), (24, 17, 0x7F)):  # 24: in the window of the first two queries
+        raw[at(0, t)][..., d] = code
+    for t, d, code in ((297, 0, -1), (299, 33, 0x7F), (277, 8, 0x7F), (290, 5, 0x7F)):  # 290: every row's
+        raw[at(1, t)][..., d] = code
+    q = torch.randn(8, hq, dim, generator=gen(1), device="cuda").to(ref.TORCH[x])
+    nan = check_with_nan(bt, q, x, window)
+    assert nan[2, :, 3].all() and not nan[:2, :, 3].any() and nan[3:, :, 5].all()
