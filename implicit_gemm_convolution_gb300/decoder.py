@@ -93,12 +93,18 @@ class AttentionLayer:
 
     def capture(self, x):
         """A CUDA graph of one step on the buffer x (seqs, model), and the tensor that holds its
-        result. One step runs before the capture, and its tokens are taken back."""
+        result. One step runs before the capture, so that all kernels are loaded; no page is reached in it, whatever x holds:
+        the cache and the lengths stay as they are."""
         side = torch.cuda.Stream()
         side.wait_stream(torch.cuda.current_stream())
+        pages = self.block_table
         with torch.cuda.stream(side):
-            self.run(x)
-            self.ctx_len -= 1
+            self.block_table = torch.full_like(pages, -1)
+            try:
+                self.run(x)
+                self.ctx_len -= 1
+            finally:
+                self.block_table = pages
         torch.cuda.current_stream().wait_stream(side)
         graph = torch.cuda.CUDAGraph()
         with torch.cuda.graph(graph):
