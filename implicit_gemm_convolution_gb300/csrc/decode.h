@@ -4,6 +4,7 @@
 // installed; not part of the public ABI.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 #include <cuda_runtime.h>
 
@@ -27,6 +28,19 @@ cudaError_t launch_behind(void (*kernel)(P...), dim3 grid, dim3 block, size_t sm
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
+
+// What a launcher has found out or set up, for each device: a kernel's attributes and occupancy belong to one. Host threads that
+// meet here write the same value.
+class PerDevice {
+    std::atomic<int> kept_[64] = {};
+
+public:
+    // The current device's place, 0 at first; NULL for a device behind the last place.
+    std::atomic<int> *here() {
+        int dev = 0;
+        return cudaGetDevice(&dev) == cudaSuccess && dev >= 0 && dev < 64 ? &kept_[dev] : nullptr;
+    }
+};
 
 // y[i][j] = sum_p x[i][p] * (u[j][p] - z[j][p / group]) * s[j][p / group].
 struct W4Problem {

@@ -1077,7 +1077,9 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
 template <typename T, int KV, int DIM, int NT, int BLOCKS>
 cudaError_t launch(const Args &a, cudaStream_t s) {
     constexpr int kSmem = Config<T, DIM, NT>::kSmem;
-    static int blocks_per_sm = 0;
+    static PerDevice blocks;
+    std::atomic<int> *const kept = blocks.here();
+    int blocks_per_sm = kept ? kept->load(std::memory_order_relaxed) : 0;
     if (blocks_per_sm == 0) {
         cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<T, KV, DIM, NT, BLOCKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
@@ -1085,6 +1087,7 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
         e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kv_attention_kernel<T, KV, DIM, NT, BLOCKS>, kThreads, kSmem);
         if (e != cudaSuccess) return e;
         blocks_per_sm = n < 1 ? 1 : n;
+        if (kept) kept->store(blocks_per_sm, std::memory_order_relaxed);
     }
     const KvAttentionProblem &p = a.p;
     // no more blocks than the table's units could ask for

@@ -589,11 +589,12 @@ __global__ void fill_zero_kernel(T *y, int64_t m, int64_t n, int64_t ldy) {
 template <typename T, int NT, int GB, bool ALIGNED>
 cudaError_t launch(Args a, cudaStream_t s) {
     using C = Config<T, NT, GB, ALIGNED>;
-    static bool ready = false;
-    if (!ready) {
+    static PerDevice ready;
+    std::atomic<int> *const is_ready = ready.here();
+    if (!is_ready || !is_ready->load(std::memory_order_relaxed)) {
         const cudaError_t e = cudaFuncSetAttribute(w4_matvec_kernel<T, NT, GB, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxSmem);
         if (e != cudaSuccess) return e;
-        ready = true;
+        if (is_ready) is_ready->store(1, std::memory_order_relaxed);
     }
     // x in shared memory: all of it, or as many units at a time as fit, in slabs of equal size
     const int64_t tokens = a.p.m < C::kTokens ? a.p.m : C::kTokens, cols = tokens * C::kParts, per_unit = cols * kUnit * 2;
