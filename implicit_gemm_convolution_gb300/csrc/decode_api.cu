@@ -256,8 +256,9 @@ int om_kv_attention(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int6
     // pieces of 64 positions of every key head and eight query rows, at most
     const __int128 units = static_cast<__int128>(width * c.page / 64 + 1) * c.heads * (tokens * (q_heads / c.heads) / 8 + seqs);
     if (units > kLim31 - (1 << 20)) return OM_ERR_TOO_LARGE;
+    // a window of all positions there can be is none: the kernel takes positions less the window in 64 bits
     om::KvAttentionProblem p{c, seqs, tokens, max_new, q_heads, {q, q_ts, q_hs}, {out, o_ts, o_hs}, dtype, lse,
-                             block_table, width, ctx_len, cu, scale, window, workspace};
+                             block_table, width, ctx_len, cu, scale, window < kLim31 ? window : 0, workspace};
     int st = check_heads(p.q, tokens, q_heads, c.dim, dtype, false);
     if (st == OM_OK) st = check_heads(p.out, tokens, q_heads, c.dim, dtype, true);
     if (st != OM_OK) return st;
