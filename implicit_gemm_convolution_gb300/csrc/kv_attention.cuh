@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
     longest = __reduce_max_sync(0xffffffffu, longest);
     // Offsets that never decrease share the tokens out, and the host has bounded their units. Others can count a
     // token for many sequences: nothing is done where their units might pass 32 bits.
-    const unsigned doubt = __reduce_or_sync(0xffffffffu, (falls ? 1u : 0u) | (mine > INT_MAX / kThreads ? 2u : 0u));
+    const unsigned doubt = __reduce_or_sync(0xffffffffu, (falls ? 1u : 0u) | (mine > (INT_MAX - kKvMaxBlocks) / kThreads ? 2u : 0u));
     if (lane == 0) {
         scan_doubt[warp] = doubt;
         scan[warp] = total;
