@@ -5,7 +5,8 @@ position rotation applied on the way), attention and read back.
 Argument marshalling over include/om.h, like the rest of the binding: every
 step of the computation is a kernel of the library. Tensors are CUDA tensors
 with unit stride in the last dimension; activations are float32, float16 or
-bfloat16; calls run on the current stream unless one is given, and never
+bfloat16; calls run on the current stream unless one is given (outputs that they
+allocate then belong to that stream's memory, as under torch.cuda.stream), and never
 synchronise. Sequences of a batch are given by ``cu`` (int32 [seqs + 1], sequence b has
 tokens cu[b] .. cu[b + 1] - 1 of the call), ``ctx_len`` (int32 [seqs], its
 length with those tokens) and ``block_table`` (int32 [seqs, width], the page of
@@ -68,6 +69,14 @@ def _stream(stream, t):
     return int(stream.cuda_stream) or None
 
 
+def _empty(shape, dtype, device, stream):
+    """A new output, of the memory that belongs to the stream that the call runs on: another stream's may still be read there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _cuda(t, name, dim, dtypes):
     """Raises unless t is a CUDA tensor of `dim` dimensions, one of the types and
     unit stride in the last dimension."""
@@ -110,7 +119,7 @@ def w4_matvec(x, weight, scales, zeros=None, group: int = 128, out=None, stream=
         zp, ldz = zeros.data_ptr(), zeros.stride(0) if n > 1 else groups
     dtype = x.dtype
     if out is None:
-        out = torch.empty((m, n), dtype=dtype, device=x.device)
+        out = _empty((m, n), dtype, x.device, stream)
         ldy = n
     else:
         _cuda(out, "out", 2, (dtype,))
@@ -134,7 +143,7 @@ def rope_table(rows: int, rot: int, base: float = 10000.0, scaling=None, factor:
     bits. scaling: None, "linear", "ntk" or "yarn" (see om_rope_table)."""
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"unknown scaling {scaling!r}")
-    out = torch.empty((rows, rot // 2, 2), dtype=torch.float32, device=device)
+    out = _empty((rows, rot // 2, 2), torch.float32, device, stream)
     _check(lib().om_rope_table(rows, rot, base, ROPE_SCALINGS[scaling], factor, original, beta_fast, beta_slow,
                                out.data_ptr(), _stream(stream, out)), "om_rope_table")
     return out
@@ -217,7 +226,7 @@ def kv_append(cache, q, k, v, table, block_table, ctx_len, cu, max_new: int, pai
         shape = (tokens, q_heads, dim)
         qa = _heads(q, "q", shape, dtype)
         if q_out is None:
-            q_out = torch.empty(shape, dtype=dtype, device=q.device)
+            q_out = _empty(shape, dtype, q.device, stream)
             oa = q_out.data_ptr(), q_heads * dim, dim
         else:
             oa = _heads(q_out, "q_out", shape, dtype)
@@ -247,11 +256,11 @@ def kv_read(cache, block_table, start, cu, max_tokens: int, tokens: int, dtype=t
         raise ValueError("tokens and max_tokens must not be negative")
     shape = (tokens, cache.heads, cache.dim)
     if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=block_table.device)
+        k_out = _empty(shape, dtype, block_table.device, stream)
     else:
         _heads(k_out, "k_out", shape, dtype)
     if v_out is None:
-        v_out = torch.empty(shape, dtype=dtype, device=block_table.device)
+        v_out = _empty(shape, dtype, block_table.device, stream)
     else:
         _heads(v_out, "v_out", shape, dtype)
     if not (k_out.is_contiguous() and v_out.is_contiguous()):
@@ -289,7 +298,7 @@ def kv_attention(cache, q, block_table, ctx_len, cu, max_new: int, scale=None, w
     ts, hs, _ = q.stride()
     batch, seqs = _batch(block_table, ctx_len, cu, "ctx_len")
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=q.device)
+        out = _empty(shape, dtype, q.device, stream)
         oa = out.data_ptr(), q_heads * dim, dim
     else:
         oa = _heads(out, "out", shape, dtype)
