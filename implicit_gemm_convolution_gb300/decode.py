@@ -18,7 +18,7 @@ import ctypes
 
 import torch
 
-from . import OmError, _check, lib
+from . import OmError, lib
 
 OM_F32, OM_F16, OM_BF16, OM_I8, OM_E4M3 = range(5)
 DTYPES = {torch.float32: OM_F32, torch.float16: OM_F16, torch.bfloat16: OM_BF16}
@@ -63,10 +63,23 @@ def _lib():
     return _functions
 
 
-def _stream(stream, t):
+def _call(name, device, stream, *args):
+    """Calls the library's function with the arguments and the stream (None: the device's current one) on a device,
+    that of its tensors whichever is current, and raises on a status."""
     if stream is None:
-        return torch._C._cuda_getCurrentRawStream(t.get_device()) or None
-    return int(stream.cuda_stream) or None
+        handle = torch._C._cuda_getCurrentRawStream(device) or None
+    else:
+        if stream.device_index != device:
+            raise ValueError("stream and tensors are on different devices")
+        handle = int(stream.cuda_stream) or None
+    function = getattr(_lib(), name)
+    if torch._C._cuda_getDevice() == device:
+        st = function(*args, handle)
+    else:
+        with torch.cuda.device(device):
+            st = function(*args, handle)
+    if st:
+        raise OmError(st, name)
 
 
 def _empty(shape, dtype, device, stream):
@@ -77,9 +90,9 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
-def _cuda(t, name, dim, dtypes):
+def _cuda(t, name, dim, dtypes, device=None):
     """Raises unless t is a CUDA tensor of `dim` dimensions, one of the types and
-    unit stride in the last dimension."""
+    unit stride in the last dimension, on the device (by number) if one is given. Returns its device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda or t.dtype not in dtypes:
@@ -88,6 +101,10 @@ def _cuda(t, name, dim, dtypes):
         raise ValueError(f"{name} must have {dim} dimensions")
     if t.stride(-1) != 1 and t.shape[-1] > 1:
         raise ValueError(f"{name} needs unit stride in its last dimension")
+    on = t.get_device()
+    if device is not None and on != device:
+        raise ValueError(f"{name} is on another device")
+    return on
 
 
 _I32 = (torch.int32,)
@@ -101,9 +118,9 @@ def w4_matvec(x, weight, scales, zeros=None, group: int = 128, out=None, stream=
     group)) float32, float16 or bfloat16; zeros uint8 of that shape (None: 8
     everywhere); group 32, 64 or a multiple of 128. Returns (m, n) of x's type.
     """
-    _cuda(x, "x", 2, DTYPES)
-    _cuda(weight, "weight", 2, (torch.uint8,))
-    _cuda(scales, "scales", 2, DTYPES)
+    device = _cuda(x, "x", 2, DTYPES)
+    _cuda(weight, "weight", 2, (torch.uint8,), device)
+    _cuda(scales, "scales", 2, DTYPES, device)
     m, k = x.shape
     n, wb = weight.shape
     if group < 1:
@@ -113,7 +130,7 @@ def w4_matvec(x, weight, scales, zeros=None, group: int = 128, out=None, stream=
         raise ValueError("weight, scales and x have different sizes")
     zp, ldz = None, 0
     if zeros is not None:
-        _cuda(zeros, "zeros", 2, (torch.uint8,))
+        _cuda(zeros, "zeros", 2, (torch.uint8,), device)
         if zeros.shape != (n, groups):
             raise ValueError("zeros and scales have different shapes")
         zp, ldz = zeros.data_ptr(), zeros.stride(0) if n > 1 else groups
@@ -122,17 +139,14 @@ def w4_matvec(x, weight, scales, zeros=None, group: int = 128, out=None, stream=
         out = _empty((m, n), dtype, x.device, stream)
         ldy = n
     else:
-        _cuda(out, "out", 2, (dtype,))
+        _cuda(out, "out", 2, (dtype,), device)
         if out.shape != (m, n):
             raise ValueError("out has the wrong shape")
         ldy = out.stride(0) if m > 1 else n
     if n > 1:
         wb, groups = weight.stride(0), scales.stride(0)
-    st = _lib().om_w4_matvec(m, n, k, group, x.data_ptr(), x.stride(0) if m > 1 else k, DTYPES[dtype], weight.data_ptr(), wb,
-                             scales.data_ptr(), groups, DTYPES[scales.dtype], zp, ldz, out.data_ptr(), ldy,
-                             _stream(stream, x))
-    if st:
-        raise OmError(st, "om_w4_matvec")
+    _call("om_w4_matvec", device, stream, m, n, k, group, x.data_ptr(), x.stride(0) if m > 1 else k, DTYPES[dtype], weight.data_ptr(), wb,
+          scales.data_ptr(), groups, DTYPES[scales.dtype], zp, ldz, out.data_ptr(), ldy)
     return out
 
 
@@ -144,8 +158,8 @@ def rope_table(rows: int, rot: int, base: float = 10000.0, scaling=None, factor:
     if scaling not in ROPE_SCALINGS:
         raise ValueError(f"unknown scaling {scaling!r}")
     out = _empty((rows, rot // 2, 2), torch.float32, device, stream)
-    _check(lib().om_rope_table(rows, rot, base, ROPE_SCALINGS[scaling], factor, original, beta_fast, beta_slow,
-                               out.data_ptr(), _stream(stream, out)), "om_rope_table")
+    _call("om_rope_table", _cuda(out, "device's memory", 3, (torch.float32,)), stream, rows, rot, base, ROPE_SCALINGS[scaling], factor, original,
+          beta_fast, beta_slow, out.data_ptr())
     return out
 
 
@@ -157,7 +171,7 @@ class PagedKVCache:
     def __init__(self, k, v, k_scale, v_scale):
         for t, name, dim, dtypes in ((k, "k", 4, CODES), (v, "v", 4, CODES), (k_scale, "k_scale", 2, (torch.float32,)),
                                      (v_scale, "v_scale", 2, (torch.float32,))):
-            _cuda(t, name, dim, dtypes)
+            self.device = _cuda(t, name, dim, dtypes, k.get_device())
             if not t.is_contiguous():
                 raise ValueError(f"{name} must be contiguous")
         if k.shape != v.shape or k.dtype != v.dtype or k_scale.shape != k.shape[:2] or v_scale.shape != k.shape[:2]:
@@ -176,14 +190,14 @@ class PagedKVCache:
         return cls(k, v, ks, vs)
 
 
-def _batch(block_table, lens, cu, lens_name):
+def _batch(block_table, lens, cu, lens_name, device):
     """Pointers and sizes of a batch's lookups: (block_table, width, lens, cu), sequences."""
-    if not (block_table.is_cuda and lens.is_cuda and cu.is_cuda and block_table.dtype is lens.dtype is cu.dtype is _int32
+    if not (block_table.get_device() == lens.get_device() == cu.get_device() == device and block_table.dtype is lens.dtype is cu.dtype is _int32
             and block_table.dim() == 2 and lens.dim() == 1 and cu.dim() == 1 and block_table.is_contiguous() and lens.is_contiguous()
             and cu.is_contiguous()):
-        _cuda(block_table, "block_table", 2, _I32)
-        _cuda(lens, lens_name, 1, _I32)
-        _cuda(cu, "cu", 1, _I32)
+        _cuda(block_table, "block_table", 2, _I32, device)
+        _cuda(lens, lens_name, 1, _I32, device)
+        _cuda(cu, "cu", 1, _I32, device)
         raise ValueError("block_table must be contiguous")
     seqs, width = block_table.shape
     if lens.numel() != seqs or cu.numel() != seqs + 1:
@@ -191,10 +205,10 @@ def _batch(block_table, lens, cu, lens_name):
     return (block_table.data_ptr(), width, lens.data_ptr(), cu.data_ptr()), seqs
 
 
-def _heads(t, name, shape, dtype):
+def _heads(t, name, shape, dtype, device):
     """Pointer, token stride and head stride of a (tokens, heads, dim) operand."""
-    if not t.is_cuda or t.dtype is not dtype or t.shape != shape:
-        _cuda(t, name, 3, (dtype,))
+    if t.get_device() != device or t.dtype is not dtype or t.shape != shape:
+        _cuda(t, name, 3, (dtype,), device)
         raise ValueError(f"{name} must have the shape {tuple(shape)}")
     ts, hs, one = t.stride()
     if one != 1:
@@ -211,11 +225,12 @@ def kv_append(cache, q, k, v, table, block_table, ctx_len, cu, max_new: int, pai
     from rope_table (None: no rotation); max_new at least the largest number of new
     tokens of a sequence. q_out may be q.
     """
-    _cuda(k, "k", 3, DTYPES)
+    device = cache.device
+    _cuda(k, "k", 3, DTYPES, device)
     dtype, tokens, dim = k.dtype, k.shape[0], cache.dim
     shape = (tokens, cache.heads, dim)
-    ka, va = _heads(k, "k", shape, dtype), _heads(v, "v", shape, dtype)
-    batch, seqs = _batch(block_table, ctx_len, cu, "ctx_len")
+    ka, va = _heads(k, "k", shape, dtype, device), _heads(v, "v", shape, dtype, device)
+    batch, seqs = _batch(block_table, ctx_len, cu, "ctx_len", device)
     if pairs not in ROPE_PAIRS:
         raise ValueError(f"unknown pairs {pairs!r}")
     qa, oa, q_heads = (None, 0, 0), (None, 0, 0), 0
@@ -224,23 +239,21 @@ def kv_append(cache, q, k, v, table, block_table, ctx_len, cu, max_new: int, pai
             raise ValueError("q must have 3 dimensions")
         q_heads = q.shape[1]
         shape = (tokens, q_heads, dim)
-        qa = _heads(q, "q", shape, dtype)
+        qa = _heads(q, "q", shape, dtype, device)
         if q_out is None:
             q_out = _empty(shape, dtype, q.device, stream)
             oa = q_out.data_ptr(), q_heads * dim, dim
         else:
-            oa = _heads(q_out, "q_out", shape, dtype)
+            oa = _heads(q_out, "q_out", shape, dtype, device)
     tp, rows, rot = None, 0, 0
     if table is not None:
-        _cuda(table, "table", 3, (torch.float32,))
+        _cuda(table, "table", 3, (torch.float32,), device)
         rows, rot, two = table.shape
         if two != 2 or not table.is_contiguous():
             raise ValueError("table must be a contiguous (rows, rot // 2, 2) tensor")
         tp, rot = table.data_ptr(), 2 * rot
-    st = _lib().om_kv_append(cache._ref, seqs, tokens, max_new, q_heads, *qa, *ka, *va, DTYPES[dtype], tp, rows, rot, ROPE_PAIRS[pairs],
-                             *batch, *oa, _stream(stream, k))
-    if st:
-        raise OmError(st, "om_kv_append")
+    _call("om_kv_append", device, stream, cache._ref, seqs, tokens, max_new, q_heads, *qa, *ka, *va, DTYPES[dtype], tp, rows, rot,
+          ROPE_PAIRS[pairs], *batch, *oa)
     return q_out
 
 
@@ -249,7 +262,8 @@ def kv_read(cache, block_table, start, cu, max_tokens: int, tokens: int, dtype=t
     """Reads `tokens` tokens back as values: token i of sequence b is position
     start[b] + i; max_tokens is at least the largest number of a sequence. Returns keys
     and values, (tokens, heads, dim) of dtype."""
-    batch, seqs = _batch(block_table, start, cu, "start")
+    device = cache.device
+    batch, seqs = _batch(block_table, start, cu, "start", device)
     if dtype not in DTYPES:
         raise TypeError("dtype must be float32, float16 or bfloat16")
     if tokens < 0 or max_tokens < 0:
@@ -258,17 +272,14 @@ def kv_read(cache, block_table, start, cu, max_tokens: int, tokens: int, dtype=t
     if k_out is None:
         k_out = _empty(shape, dtype, block_table.device, stream)
     else:
-        _heads(k_out, "k_out", shape, dtype)
+        _heads(k_out, "k_out", shape, dtype, device)
     if v_out is None:
         v_out = _empty(shape, dtype, block_table.device, stream)
     else:
-        _heads(v_out, "v_out", shape, dtype)
+        _heads(v_out, "v_out", shape, dtype, device)
     if not (k_out.is_contiguous() and v_out.is_contiguous()):
         raise ValueError("k_out and v_out must be contiguous")
-    st = _lib().om_kv_read(cache._ref, seqs, tokens, *batch, k_out.data_ptr(), v_out.data_ptr(), DTYPES[dtype],
-                           _stream(stream, block_table))
-    if st:
-        raise OmError(st, "om_kv_read")
+    _call("om_kv_read", device, stream, cache._ref, seqs, tokens, *batch, k_out.data_ptr(), v_out.data_ptr(), DTYPES[dtype])
     return k_out, v_out
 
 
@@ -290,31 +301,30 @@ def kv_attention(cache, q, block_table, ctx_len, cu, max_new: int, scale=None, w
     of exponentials. workspace: from new_kv_workspace; without one each sequence
     and head is one block's work. Returns (tokens, q heads, dim) of q's type.
     """
-    _cuda(q, "q", 3, DTYPES)
+    device = cache.device
+    _cuda(q, "q", 3, DTYPES, device)
     dtype, shape = q.dtype, q.shape
     tokens, q_heads, dim = shape
     if dim != cache.dim:
         raise ValueError("q and the cache have different head dimensions")
     ts, hs, _ = q.stride()
-    batch, seqs = _batch(block_table, ctx_len, cu, "ctx_len")
+    batch, seqs = _batch(block_table, ctx_len, cu, "ctx_len", device)
     if out is None:
         out = _empty(shape, dtype, q.device, stream)
         oa = out.data_ptr(), q_heads * dim, dim
     else:
-        oa = _heads(out, "out", shape, dtype)
+        oa = _heads(out, "out", shape, dtype, device)
     lp = None
     if lse is not None:
-        _cuda(lse, "lse", 2, (torch.float32,))
+        _cuda(lse, "lse", 2, (torch.float32,), device)
         if lse.shape != (tokens, q_heads) or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous (tokens, q heads) tensor")
         lp = lse.data_ptr()
     ws, ws_bytes = None, 0
     if workspace is not None:
-        if not workspace.is_cuda or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor")
+        if workspace.get_device() != device or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous tensor on the cache's device")
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    st = _lib().om_kv_attention(cache._ref, seqs, tokens, max_new, q_heads, q.data_ptr(), ts, hs, DTYPES[dtype], *batch,
-                                dim ** -0.5 if scale is None else scale, window, *oa, lp, ws, ws_bytes, _stream(stream, q))
-    if st:
-        raise OmError(st, "om_kv_attention")
+    _call("om_kv_attention", device, stream, cache._ref, seqs, tokens, max_new, q_heads, q.data_ptr(), ts, hs, DTYPES[dtype], *batch,
+          dim ** -0.5 if scale is None else scale, window, *oa, lp, ws, ws_bytes)
     return out
