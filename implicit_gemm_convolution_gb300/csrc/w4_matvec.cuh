@@ -251,8 +251,8 @@ __global__ void __launch_bounds__(kThreads, 1) w4_matvec_kernel(const __grid_con
                         const int r = q / C::kRowPieces;
                         return dst + (ALIGNED ? r * 128 + (((q ^ r) & 7) * 16) : q * 16);
                     };
-                    if (rows >= kRowTile + 3 && grp + kGroups <= groups && (unit > 0 || pass + f_tile > 0)) {
-                        // Every group is there, and there are rows behind the tile's and something before it: what is
+                    if (rows >= kRowTile + 3 && grp + kGroups <= groups && (grp > 0 || pass + f_tile > 0)) {
+                        // Every group is there, and there are rows behind the tile's and groups before it: what is
                         // copied beyond a row's ends lies inside the operands (three rows: two zero points a row, eight
                         // bytes copied). Codes behind k meet zeros of x.
 #pragma unroll
@@ -273,7 +273,7 @@ __global__ void __launch_bounds__(kThreads, 1) w4_matvec_kernel(const __grid_con
                             }
                         }
                     } else {
-                        const bool head = unit == 0 && pass + f_tile == 0;
+                        const bool head = grp == 0 && pass + f_tile == 0;  // wide groups: the first one goes on in later units
                         auto clipped = [&](uint32_t to, const uint8_t *tile, int at, const uint8_t *base, const uint8_t *aligned, int left, auto size) {
                             constexpr int kSize = decltype(size)::value;
                             left = min(max(left, 0), kSize);
