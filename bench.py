@@ -4,9 +4,10 @@ Headline (``value``): the exact-mode fp32 product C = A*B at m = n = k = 4096
 (A, B ~ N(0, 1), row-major, contiguous), one om_gemm_f32_ws call per step
 (the balanced schedule; om_gemm_f32 without scratch is reported beside it),
 inputs resident in HBM, L2 flushed (a 512 MiB write) before every timed
-call. Also reported per step set: fast mode on the same product, the
+call. The line on standard output holds the headline. Also measured, and written to
+standard error as one JSON line: fast mode on the same product, the
 ResNet-50 stage-1 3x3 and 1x1 convolutions (exact and fast), the prefill
-product and the grouped/strided/dilated convolution.
+product, the grouped/strided/dilated convolution and the host's rate on each.
 
 Roofline: the kernels are bound by the FP32 pipes (bound "alu"). The peak is
 derived from unit counts and the maximum SM clock: SMs x 128 FP32 lanes x 2
@@ -885,6 +886,25 @@ def run_profile(args):
     print(json.dumps({"profile": args.profile, "launches": args.warmup + args.steps}))
 
 
+# of the metric's workloads, beside the headline
+IN_LINE = ("gemm_4096^3_fast_ws", "conv3x3_n32_c64_56_exact_ws", "conv3x3_n32_c64_56_fast_ws")
+
+
+def split_line(line: dict):
+    """The line that is printed (the headline and the metric's other workloads, short enough to be kept whole by
+    whoever keeps the end of the output) and the figures of every workload, or None."""
+    line = dict(line)
+    details = {"modes": line.pop("modes", {})}
+    short = {n: {k: details["modes"][n][k] for k in ("ms", "GFLOP/s", "roofline_frac")} for n in IN_LINE if n in details["modes"]}
+    if short:
+        line["modes"] = short
+    cpu = dict(line.get("cpu_baseline") or {})
+    if "per_workload" in cpu:
+        details["cpu_per_workload"] = cpu.pop("per_workload")
+        line["cpu_baseline"] = cpu
+    return line, details if any(details.values()) else None
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -922,6 +942,9 @@ def main():
             import torch.distributed as dist
             dist.destroy_process_group()
     if line is not None:
+        line, details = split_line(line)
+        if details:
+            print(json.dumps(details), file=sys.stderr, flush=True)
         print(json.dumps(line), flush=True)
 
 
