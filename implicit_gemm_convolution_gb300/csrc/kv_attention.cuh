@@ -29,12 +29,16 @@
 // shares of the blocks that fit at once, found on the device from the lengths; an item that a cut crosses is joined by
 // the block that finishes its last part. More and shorter shares (four times as many) ran no faster.
 //
-// Bound and measured (GB300; 6 680 GB/s is the measured copy bandwidth). HBM, 2 dim bytes a position and key head:
-// 64 sequences of up to 16384 tokens, 8 key heads of 128, 8 query heads each, bfloat16, whole numbers: 250 us,
-// 6 450 GB/s, 97 %. One sequence of 131071 tokens, float16, 8-bit floats, pages of 16: 60 us, 4 500 GB/s; about
-// 4 us until the first product, 45 us in the loop, 9 us for the joins. One of 331 tokens: 6.9 us, latency. 25
-// rows of 32-bit queries over a window of 4096: 69 us, 33 %: the products' issue (two parts of queries and of weights
-// each, rows in two blocks that each widen the codes).
+// Roundings beside those parts: exponentials and reciprocals are the approximate instructions (2^-22), and 16-bit calls leave
+// their sums of values to the tensor cores, which cut them off (2^-23 of the sum, twice a tile). Relative error of 131071 values of one
+// sign: 1e-5 split over the GPU, 2e-4 by one block (half a unit of float16: 4.9e-4).
+//
+// Bound and measured (GB300; 6 790 GB/s is the measured copy bandwidth). HBM, 2 dim bytes a position and key head:
+// 64 sequences of up to 16384 tokens, 8 key heads of 128, 8 query heads each, bfloat16, whole numbers: 249 us,
+// 6 470 GB/s, 95 %. One sequence of 131071 tokens, float16, 8-bit floats, pages of 16: 60 us, 4 500 GB/s; about
+// 4 us until the first product, 45 us in the loop, 9 us for the joins. One of 331 tokens: 7.6 us, latency. 25
+// rows of 32-bit queries over a window of 4096: 72 us, 31 %: latency, at two warps a scheduler (255 registers), with
+// the tensor pipe 34 % and the ALU 34 % busy; rows are in two blocks that each copy and widen the codes.
 #pragma once
 
 #include <cfloat>
@@ -247,7 +251,7 @@ struct Config {
 
 // BLOCKS: of an SM, at least. Three where the registers allow it (heads of up to 128, 8 rows of 16 bits) and there are items for
 // all: 256 sequences of 500 tokens, 8 key heads, 68 -> 59 us, heads of 64 (64 sequences of up to 8000 tokens) 91 -> 80 us. Few
-// items are cut into parts, whose join takes longer the more they are, and 190 registers run the loop
+// items are cut into parts, whose join takes longer the more they are, and 205 registers run the loop
 // faster than 168: one sequence of 131071 tokens 61 us with two, 66 us with the code for three.
 template <typename T, int KV, int DIM, int NT, int BLOCKS>
 __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __grid_constant__ Args a) {

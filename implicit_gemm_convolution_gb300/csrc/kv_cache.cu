@@ -7,9 +7,9 @@
 // operation (the library is built without contraction), so codes, scales and
 // rotated queries have one bit pattern each, whatever the launch.
 //
-// Bound and measured (GB300; 6 680 GB/s is the measured copy bandwidth): HBM. Prompts of 12031 tokens in all, 32 query
-// and 8 key heads of 128, 32-bit: 93 us for 525 MB (5 600 GB/s, 84 %). Reading 76166 tokens of 8 heads of 128 back as
-// bfloat16: 79 us, 5 930 GB/s (89 %); with 16-byte loads whose lanes stored 32 or 64 bytes each it took 108 us. One
+// Bound and measured (GB300; 6 790 GB/s is the measured copy bandwidth): HBM. Prompts of 12031 tokens in all, 32 query
+// and 8 key heads of 128, 32-bit: 93 us for 525 MB (5 600 GB/s, 83 %). Reading 76166 tokens of 8 heads of 128 back as
+// bfloat16: 79 us, 5 930 GB/s (87 %); with 16-byte loads whose lanes stored 32 or 64 bytes each it took 108 us. One
 // token for each of 192 sequences: 15 us, the latency of the lookups, the page's old codes and its barrier.
 
 #include <type_traits>
@@ -70,12 +70,6 @@ struct AppendArgs {
     int64_t cache_blocks;  // blocks that write the cache; the others rotate queries
     int tokens;            // that such a block takes
 };
-
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ void load_unit(const T *row, int first, int second, float *v) {
-    load4<T, ALIGNED>(row + first, v);
-    load4<T, ALIGNED>(row + second, v + 4);
-}
 
 // One block per (page the new tokens touch, head, keys or values): the page's
 // largest new magnitude first, then its scale, its old codes under the new scale and

@@ -260,8 +260,8 @@ def kv_append(cache, q, k, v, table, block_table, ctx_len, cu, max_new: int, pai
 def kv_read(cache, block_table, start, cu, max_tokens: int, tokens: int, dtype=torch.float32, k_out=None, v_out=None,
             stream=None):
     """Reads `tokens` tokens back as values: token i of sequence b is position
-    start[b] + i; max_tokens is at least the largest number of a sequence. Returns keys
-    and values, (tokens, heads, dim) of dtype."""
+    start[b] + i. The lengths come from cu; max_tokens, at least the largest of them, is not
+    needed for them. Returns keys and values, (tokens, heads, dim) of dtype."""
     device = cache.device
     batch, seqs = _batch(block_table, start, cu, "start", device)
     if dtype not in DTYPES:

@@ -467,6 +467,8 @@ OM_API size_t om_kv_workspace_bytes(int64_t kv_heads, int64_t q_heads, int64_t d
  * cache's heads; query head h reads head h / (q_heads / heads).
  *   out[t][h] = sum_i softmax_i(scale * q[t][h] . key_i) value_i, of q's dtype;
  *   lse: NULL, or [tokens][q_heads]: the natural log of the sum of exponentials.
+ * Sums, maxima and lse are 32 bits. Elements of 32-bit queries are held to 2^-22 of their row's largest, softmax weights to 2^-22 of
+ * themselves or 2^-24 of the largest among 16 neighbouring positions; a page's scales take no bits from another page's.
  * A query that sees no token gives zeros and lse -inf; one with a score that is NaN (its own elements, a
  * page's scale) gives NaN for both. Memory behind masked tokens
  * (stale codes, pages outside the window) never reaches an output.
