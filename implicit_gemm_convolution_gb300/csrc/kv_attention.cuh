@@ -249,10 +249,9 @@ struct Config {
     static_assert(2 * kThreads * 4 <= kQBytes, "the sums of the parts' join fit where the queries were");
 };
 
-// BLOCKS: of an SM, at least. Three where the registers allow it (heads of up to 128, 8 rows of 16 bits) and there are items for
-// all: 256 sequences of 500 tokens, 8 key heads, 68 -> 59 us, heads of 64 (64 sequences of up to 8000 tokens) 91 -> 80 us. Few
-// items are cut into parts, whose join takes longer the more they are, and 205 registers run the loop
-// faster than 168: one sequence of 131071 tokens 61 us with two, 66 us with the code for three.
+// BLOCKS: of an SM, at least. Three where the registers allow it (heads of up to 128, 8 rows of 16 bits), two elsewhere. With two, 256
+// sequences of 500 tokens, 8 key heads, take 66 us instead of 57, 64 of up to 8000 tokens with heads of 64 101 instead of 88; one of
+// 131071 tokens, whose parts are more with three, the same (float16 59.5 and 59.9 us, bfloat16 59.4 and 57.9).
 template <typename T, int KV, int DIM, int NT, int BLOCKS>
 __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __grid_constant__ Args a) {
     using S = Shape<DIM>;
@@ -1107,11 +1106,7 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
 template <typename T, int KV, int DIM>
 cudaError_t by_rows(const Args &a, cudaStream_t s) {
     const int64_t rows = kv_block_rows(a.p.q_heads / a.p.c.heads, a.p.max_new);
-    if constexpr (DIM <= 128 && sizeof(T) == 2) {
-        const int64_t items = (a.p.tokens * (a.p.q_heads / a.p.c.heads) / 8 + a.p.seqs) * a.p.c.heads;
-        if (rows == 8 && items >= 2 * static_cast<int64_t>(num_sms())) return launch<T, KV, DIM, 1, 3>(a, s);
-    }
-    if (rows == 8) return launch<T, KV, DIM, 1, 2>(a, s);
+    if (rows == 8) return launch<T, KV, DIM, 1, DIM <= 128 && sizeof(T) == 2 ? 3 : 2>(a, s);
     return launch<T, KV, DIM, 2, 2>(a, s);
 }
 
