@@ -34,9 +34,9 @@
 // sign: 1e-5 split over the GPU, 2e-4 by one block (half a unit of float16: 4.9e-4).
 //
 // Bound and measured (GB300; 6 790 GB/s is the measured copy bandwidth). HBM, 2 dim bytes a position and key head:
-// 64 sequences of up to 16384 tokens, 8 key heads of 128, 8 query heads each, bfloat16, whole numbers: 249 us,
-// 6 470 GB/s, 95 %. One sequence of 131071 tokens, float16, 8-bit floats, pages of 16: 60 us, 4 500 GB/s; about
-// 4 us until the first product, 45 us in the loop, 9 us for the joins. One of 331 tokens: 7.6 us, latency. 25
+// 64 sequences of up to 16384 tokens, 8 key heads of 128, 8 query heads each, bfloat16, whole numbers: 248 us,
+// 6 510 GB/s, 96 %. One sequence of 131071 tokens, float16, 8-bit floats, pages of 16: 60 us, 4 500 GB/s; with two
+// blocks an SM about 4 us until the first product, 45 us in the loop, 9 us for the joins. One of 331 tokens: 7.6 us, latency. 25
 // rows of 32-bit queries over a window of 4096: 72 us, 31 %: latency, at two warps a scheduler (255 registers), with
 // the tensor pipe 34 % and the ALU 34 % busy; rows are in two blocks that each copy and widen the codes.
 #pragma once
