@@ -63,9 +63,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 // range, its second part above the subnormals. The maximum may lag behind while exponentials are below 2^40.
 constexpr float kBias = 8.0f, kMost = 32768.0f, kLeast = 0.5f, kMostExp = 1099511627776.0f;
 constexpr float kNone = -FLT_MAX;  // the maximum of no scores
-// Units from 2^-100 to 2^126; a smaller one may not raise sums above 2^100.
-constexpr float kLeastUnit = 7.8886090522101181e-31f;
+// Units from 2^-126 to 2^126, and no smaller than a value scale by 2^100; a smaller one may not raise sums above 2^100.
+constexpr float kLeastUnit = FLT_MIN, kLeastOfScale = 7.8886090522101181e-31f;
 constexpr unsigned kMostUnit = 253u << 23;
+// A value scale in units, finite: a weight of 0 stays 0.
+__device__ __forceinline__ float in_units(float value, float per_unit) { return fminf(fmaxf(__fmul_rn(value, per_unit), -FLT_MAX), FLT_MAX); }
+__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<unsigned>(e + 127) << 23); }
 __device__ __forceinline__ float reciprocal(float power) { return __uint_as_float((254u << 23) - __float_as_uint(power)); }
 
 template <int DIM>
@@ -769,7 +772,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < 2; ++j) vf[nt][j] = __fmul_rn(value, per_unit[nt][j]);
+                    for (int j = 0; j < 2; ++j) vf[nt][j] = in_units(value, per_unit[nt][j]);
             }
 
             const uint8_t *const src = my_ring + src_at;
@@ -864,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
                                 l[nt][j] = __fmul_rn(l[nt][j], by[nt][j]);
                             }
                             if (value != 0.0f && !odd_scale) {
-                                const float to = fmaxf(__fmul_rn(ex2(x - m[nt][j]), fabsf(value)), kLeastUnit);
+                                const float to = fmaxf(__fmul_rn(fmaxf(ex2(x - m[nt][j]), kLeastOfScale), fabsf(value)), kLeastUnit);
                                 const unsigned unit = min(__float_as_uint(to) & 0x7f800000u, kMostUnit);
                                 up[nt][j] = (static_cast<int>((254u << 23) - unit) - static_cast<int>(__float_as_uint(per_unit[nt][j]))) >> 23;
                                 smaller |= up[nt][j] > 0;
@@ -884,6 +887,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
                                 most = max(most, max(__float_as_uint(o[st][nt][j]) & 0x7fffffffu, __float_as_uint(o[st][nt][j + 2]) & 0x7fffffffu));
 #pragma unroll
                             for (int i = 4; i < 32; i <<= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, i));
+                            most = __float_as_uint(__fmul_rn(__uint_as_float(most), by[nt][j]));
                             up[nt][j] = min(up[nt][j], max(227 - static_cast<int>(most >> 23), 0));
                         }
                 }
@@ -892,8 +896,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
 #pragma unroll
                     for (int j = 0; j < 2; ++j) {
                         per_unit[nt][j] = __uint_as_float(__float_as_uint(per_unit[nt][j]) + (static_cast<unsigned>(up[nt][j]) << 23));
-                        vf[nt][j] = __fmul_rn(value, per_unit[nt][j]);
-                        by[nt][j] = __fmul_rn(by[nt][j], __uint_as_float(static_cast<unsigned>(min(max(up[nt][j], -126), 127) + 127) << 23));
+                        vf[nt][j] = in_units(value, per_unit[nt][j]);
                     }
                 if (sums) {
 #pragma unroll
@@ -901,7 +904,11 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
 #pragma unroll
                         for (int st = 0; st < S::kSteps; ++st)
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) o[st][nt][j] = __fmul_rn(o[st][nt][j], by[nt][j & 1]);
+                            for (int j = 0; j < 4; ++j) {
+                                // up to 2^252 either way: in two steps
+                                const int k = up[nt][j & 1] / 2;
+                                o[st][nt][j] = __fmul_rn(__fmul_rn(o[st][nt][j], __fmul_rn(by[nt][j & 1], power_of_two(k))), power_of_two(up[nt][j & 1] - k));
+                            }
                 }
             }
             empty = false;
@@ -913,7 +920,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
                 for (int j = 0; j < 4; ++j) {
                     l[nt][j & 1] = __fadd_rn(l[nt][j & 1], e[nt][j]);
                     w[j] = __fmul_rn(e[nt][j], vf[nt][j & 1]);
-                    if (odd_scale && s[nt][j] == -INFINITY) w[j] = 0.0f;  // hidden: its scale does not count
+                    if (odd_scale) w[j] = s[nt][j] == -INFINITY ? 0.0f : __int_as_float(0x7FC00000);  // hidden: its scale does not count
                 }
                 const uint32_t x[2] = {pack_half(w[0], w[1]), pack_half(w[2], w[3])};
                 const float2 y = unpack_half(x[0]), z = unpack_half(x[1]);

@@ -212,3 +212,75 @@ def test_value_codes_that_some_rows_see(window, hkv, hq, dim, x):
     q = torch.randn(8, hq, dim, generator=gen(1), device="cuda").to(ref.TORCH[x])
     nan = check_with_nan(bt, q, x, window)
     assert nan[2, :, 3].all() and not nan[:2, :, 3].any() and nan[3:, :, 5].all()
+
+
+# ------------------------------------------------------------------ scores and scales at once
+def spread(pages, hkv, lo, hi, seed):
+    return 10.0 ** (lo + (hi - lo) * torch.rand(pages, hkv, generator=gen(seed), device="cuda"))
+
+
+def beside_heavier(bt, q, window):
+    """Sum over the positions of |value| by the largest weight among the 16 neighbours: of which a weight is 2^-24 off at most."""
+    qq, out = ref.f64(q), np.zeros((*q.shape[:2], bt.dim))
+    k = ref.code_values(bt.k) * ref.f64(bt.ks)[:, :, None, None]
+    v = np.abs(ref.code_values(bt.v) * ref.f64(bt.vs)[:, :, None, None])
+    group = q.shape[1] // bt.hkv
+    for b, (c, n) in enumerate(zip(bt.ctx, bt.new)):
+        for i in range(n):
+            t, p = int(bt.cu_np[b]) + i, c - n + i
+            pos = np.arange(max(0, p - window + 1) if window else 0, p + 1)
+            ids, rows = bt.table_np[b][pos // bt.page], pos % bt.page
+            for h in range(q.shape[1]):
+                s = k[ids, h // group, rows] @ qq[t, h] * bt.dim ** -0.5
+                w = np.exp(s - s.max())
+                top = np.zeros(p // 16 + 1)
+                np.maximum.at(top, pos // 16, w / w.sum())
+                out[t, h] = top[pos // 16] @ v[ids, h // group, rows]
+    return out
+
+
+def check_spread(bt, hq, x, window=0, q_size=1.5, workspace=True, heavier=False):
+    q = (q_size * torch.randn(int(bt.cu_np[-1]), hq, bt.dim, generator=gen(7), device="cuda")).to(ref.TORCH[x])
+    out, lse = attend(bt, q, window=window, workspace=workspace)
+    want, wl, mag, big = exact(bt, q, window)
+    tol = before_rounding(bt, big, mag) + (2.0 ** -24 * beside_heavier(bt, q, window) if heavier else 0.0)
+    got = ref.f64(out)
+    assert np.isfinite(got).all()
+    assert (np.abs(got - want) <= tol + 2 * half_unit(np.abs(want) + tol, x)).all()
+    assert np.isfinite(ref.f64(lse)).all()
+
+
+@pytest.mark.parametrize("workspace", [True, False])
+@pytest.mark.parametrize("x,kind,dim,page", [("f32", "int8", 64, 16), ("f32", "e4m3", 64, 32), ("bf16", "e4m3", 256, 16), ("bf16", "int8", 128, 64)])
+def test_key_and_value_scales_far_apart(x, kind, dim, page, workspace):
+    """Scores that leave most weights below 2^-126, on pages whose value scales range over 10^24: a weight of 0 stays 0."""
+    bt = Batch([1785, 1039, 300], [1, 3, 2], 2, dim, page, kind, dim + page)
+    bt.ks = bt.ks * spread(bt.pages, 2, -4.0, 1.3, 1)
+    bt.vs = bt.vs * spread(bt.pages, 2, -12.0, 12.0, 2)
+    check_spread(bt, 4, x, workspace=workspace, heavier=True)
+    check_spread(bt, 4, x, window=700, workspace=workspace, q_size=15.0, heavier=True)
+
+
+@pytest.mark.parametrize("lo,hi", [(-37.0, -37.0), (-36.0, -30.0), (-36.0, 0.0), (-36.0, 33.0)])
+@pytest.mark.parametrize("x,kind,dim", [("f32", "int8", 64), ("f32", "e4m3", 128), ("bf16", "int8", 256)])
+def test_value_scales_at_the_ends_of_the_range(x, kind, dim, lo, hi):
+    bt = Batch([700, 40, 5], [2, 1, 5], 1, dim, 16, kind, dim)
+    bt.vs = bt.vs * spread(bt.pages, 1, lo, hi, 3)
+    check_spread(bt, 3, x)
+    check_spread(bt, 3, x, window=50, q_size=0.1)
+
+
+def test_value_scales_that_step_through_the_range():
+    """Each page's value scale 10^36 above or below the page before, and scores that make up for it."""
+    bt = Batch([128, 128], [1, 1], 1, 128, 16, "int8", 3, width_extra=0)
+    bt.k = torch.full_like(bt.k, 1)
+    for b in range(2):
+        for j, p in enumerate(bt.table_np[b]):
+            high = (j + b) % 2 == 0
+            bt.vs[int(p)] = 1e-36 if high else 1.0
+            bt.ks[int(p)] = 80.0 / 128 ** 0.5 if high else 0.0  # 80 above, of 83 that make up for 1e36
+    q = torch.ones(2, 1, 128, device="cuda")
+    out, lse = attend(bt, q)
+    want, wl, mag, _ = exact(bt, q)
+    tol = before_rounding(bt, np.full(mag.shape[:2], 80.0), mag)
+    assert (np.abs(ref.f64(out) - want) <= tol + half_unit(np.abs(want) + tol, "f32")).all()
