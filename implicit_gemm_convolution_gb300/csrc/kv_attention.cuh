@@ -36,8 +36,8 @@
 // Bound and measured (GB300; 6 790 GB/s is the measured copy bandwidth). HBM, 2 dim bytes a position and key head:
 // 64 sequences of up to 16384 tokens, 8 key heads of 128, 8 query heads each, bfloat16, whole numbers: 248 us,
 // 6 510 GB/s, 96 %. One sequence of 131071 tokens, float16, 8-bit floats, pages of 16: 60 us, 4 500 GB/s; with two
-// blocks an SM about 4 us until the first product, 45 us in the loop, 9 us for the joins. One of 331 tokens: 7.6 us, latency. 25
-// rows of 32-bit queries over a window of 4096: 72 us, 31 %: latency, at two warps a scheduler (255 registers), with
+// blocks an SM about 4 us until the first product, 45 us in the loop, 9 us for the joins. One of 331 tokens: 7.8 us, latency. 25
+// rows of 32-bit queries over a window of 4096: 73 us, 31 %: latency, at two warps a scheduler (255 registers), with
 // the tensor pipe 34 % and the ALU 34 % busy; rows are in two blocks that each copy and widen the codes.
 #pragma once
 
@@ -253,7 +253,7 @@ struct Config {
 };
 
 // BLOCKS: of an SM, at least. Three where the registers allow it (heads of up to 128, 8 rows of 16 bits), two elsewhere. With two, 256
-// sequences of 500 tokens, 8 key heads, take 66 us instead of 57, 64 of up to 8000 tokens with heads of 64 101 instead of 88; one of
+// sequences of 500 tokens, 8 key heads, take 66 us instead of 57, 64 of up to 8000 tokens with heads of 64 101 instead of 89; one of
 // 131071 tokens, whose parts are more with three, the same (float16 59.5 and 59.9 us, bfloat16 59.4 and 57.9).
 template <typename T, int KV, int DIM, int NT, int BLOCKS>
 __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __grid_constant__ Args a) {
