@@ -20,8 +20,8 @@
 // ALU 37 to 40 %, tensor pipe 9 to 17 %. About 11 instructions widen eight codes, in chains that four warps a scheduler
 // (registers and shared memory allow no more) do not hide, and no product runs while x is laid out.
 // 1 x 11008 x 4096, 32-bit x, groups of 128: 12.7 us, 1 890 GB/s (28 %), 3.6 us of it until x is laid
-// out, then 1.4 us for each of up to five rounds of 16 rows; groups of 256 and more 14.9 us (their last group's
-// units are copied with clipping), one group a row 16.0 us. 16 x 28669 x 8178, bfloat16, groups of 32 with zero
+// out, then 1.4 us for each of up to five rounds of 16 rows; with zero points 13.1 us, and groups of 256 and more 14.9 us (their
+// last group's units are copied with clipping), one group a row 16.0 us. 16 x 28669 x 8178, bfloat16, groups of 32 with zero
 // points, rows at odd addresses: 77 us, 1 830 GB/s (27 %), 6 us for each of three slabs until x is laid out.
 // More rows take the weights again for every 16 (5 of 32 bits): 2048 x 6144 x 4096, bfloat16, 1.40 ms.
 // 1 x 1024 x 1024, float16: 3.8 us, latency. Tried and no faster: scales and zeros as a table in shared memory instead of

@@ -299,7 +299,8 @@ def kv_attention(cache, q, block_table, ctx_len, cu, max_new: int, scale=None, w
 
     scale: default dim ** -0.5. lse: float32 (tokens, q heads), receives the natural log of the sums
     of exponentials. workspace: from new_kv_workspace; without one each sequence
-    and head is one block's work. Returns (tokens, q heads, dim) of q's type.
+    and head is one block's work. Rows of tokens behind cu's last offset are not written. Returns (tokens, q heads,
+    dim) of q's type.
     """
     device = cache.device
     _cuda(q, "q", 3, DTYPES, device)

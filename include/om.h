@@ -470,7 +470,7 @@ OM_API size_t om_kv_workspace_bytes(int64_t kv_heads, int64_t q_heads, int64_t d
  * Sums, maxima and lse are 32 bits. Elements of 32-bit queries are held to 2^-22 of their row's largest, softmax weights to 2^-22 of
  * themselves or 2^-24 of the largest among 16 neighbouring positions; a page's scales take no bits from another page's.
  * A query that sees no token gives zeros and lse -inf; one with a score that is NaN (its own elements, a
- * page's scale) gives NaN for both. Memory behind masked tokens
+ * page's scale) gives NaN for both. Rows of tokens that no sequence owns (behind cu[seqs]) stay as they are. Memory behind masked tokens
  * (stale codes, pages outside the window) never reaches an output.
  * OM_ERR_TOO_LARGE where the table could hold 2^31 pieces of 64 positions of all heads and rows; a table
  * (of any call) reaches fewer than 2^31 - 2^16 positions.
