@@ -62,6 +62,31 @@ cudaError_t launch_w4_matvec_f32(const W4Problem &p, cudaStream_t s);
 cudaError_t launch_w4_matvec_f16(const W4Problem &p, cudaStream_t s);
 cudaError_t launch_w4_matvec_bf16(const W4Problem &p, cudaStream_t s);
 
+// x = residual + scale act(gate) N_post(y), h = N(x), row by row; leading dimensions in elements.
+struct NormProblem {
+    int64_t tokens, width;
+    const void *y;
+    int64_t ldy;
+    int dtype;  // of y, gate and out
+    const void *residual;
+    int64_t ldr;
+    int stream_dtype;  // of residual and sum: dtype or OM_F32
+    const void *gate;
+    int64_t ldg;
+    int activation;
+    float scale;
+    int layer, post;
+    float eps;
+    const void *post_weight, *post_bias, *weight, *bias;
+    int weight_dtype;  // dtype or OM_F32
+    void *sum;
+    int64_t lds;
+    void *out;
+    int64_t ldo;
+};
+constexpr int64_t kNormMostWidth = 32768;  // 1024 threads of 32 elements
+cudaError_t launch_block_norm(const NormProblem &p, cudaStream_t s);
+
 // A token-major, head-strided operand: element (t, h, d) at t*ts + h*hs + d.
 struct Heads {
     const void *p;

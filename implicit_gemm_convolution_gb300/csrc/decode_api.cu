@@ -1,5 +1,7 @@
 // decode_api.cu -- the C ABI of the decoding operators: argument validation and launch
 // on the caller's stream. Nothing is launched by a call that fails validation.
+#include <cfloat>
+#include <cmath>
 #include <cstdint>
 
 #include "decode.h"
@@ -152,6 +154,48 @@ int om_w4_matvec(int64_t m, int64_t n, int64_t k, int64_t group, const void *x, 
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (x_dtype == OM_F32) return from_cuda(om::launch_w4_matvec_f32(p, st));
     return from_cuda(x_dtype == OM_F16 ? om::launch_w4_matvec_f16(p, st) : om::launch_w4_matvec_bf16(p, st));
+}
+
+int om_block_norm(int64_t tokens, int64_t width, const void *y, int64_t ldy, int dtype, const void *residual, int64_t ldr, int stream_dtype,
+                  const void *gate, int64_t ldg, int activation, float scale, int norm, int post, float eps, const void *post_weight,
+                  const void *post_bias, const void *weight, const void *bias, int weight_dtype, void *sum, int64_t lds, void *out, int64_t ldo,
+                  void *stream) {
+    if (tokens < 0 || width < 0) return OM_ERR_INVALID_ARG;
+    if (!float_type(dtype) || !float_type(stream_dtype) || !float_type(weight_dtype)) return OM_ERR_UNSUPPORTED;
+    if ((stream_dtype != dtype && stream_dtype != OM_F32) || (weight_dtype != dtype && weight_dtype != OM_F32)) return OM_ERR_UNSUPPORTED;
+    if (norm != OM_NORM_RMS && norm != OM_NORM_LAYER) return OM_ERR_UNSUPPORTED;
+    if (activation < OM_GATE_NONE || activation > OM_GATE_SILU) return OM_ERR_UNSUPPORTED;
+    if (!(eps >= 0.0f && eps <= FLT_MAX) || !(fabsf(scale) <= FLT_MAX)) return OM_ERR_INVALID_ARG;
+    if (!post && (post_weight || post_bias)) return OM_ERR_INVALID_ARG;
+    if (tokens == 0 || width == 0) return OM_OK;
+    if (!sum && !out) return OM_ERR_INVALID_ARG;
+    if (width > om::kNormMostWidth || tokens > kLim31) return OM_ERR_TOO_LARGE;
+    if (!y) return OM_ERR_NULL_PTR;
+    // rows of an input may lie in one place (stride 0); an output's may not overlap
+    if (ldy < 0 || (residual && ldr < 0) || (gate && ldg < 0)) return OM_ERR_INVALID_ARG;
+    if (tokens > 1 && ((sum && lds < width) || (out && ldo < width))) return OM_ERR_INVALID_ARG;
+    const int64_t big = int64_t(1) << 40;
+    if (ldy > big || (residual && ldr > big) || (gate && ldg > big) || (sum && lds > big) || (out && ldo > big)) return OM_ERR_TOO_LARGE;
+    const int64_t tb = type_bytes(dtype), rb = type_bytes(stream_dtype), wb = type_bytes(weight_dtype);
+    if (!aligned(y, tb) || !aligned(residual, rb) || !aligned(gate, tb) || !aligned(sum, rb) || !aligned(out, tb) || !aligned(post_weight, wb) ||
+        !aligned(post_bias, wb) || !aligned(weight, wb) || !aligned(bias, wb))
+        return OM_ERR_ALIGNMENT;
+    auto rows = [&](const void *p, int64_t ld, int64_t bytes) { return rows_of(p, tokens, p ? width : 0, ld, bytes); };
+    const Block in[7] = {rows(y, ldy, tb), rows(residual, ldr, rb), rows(gate, ldg, tb), rows_of(post_weight, 1, post_weight ? width : 0, 0, wb),
+                         rows_of(post_bias, 1, post_bias ? width : 0, 0, wb), rows_of(weight, 1, weight ? width : 0, 0, wb),
+                         rows_of(bias, 1, bias ? width : 0, 0, wb)};
+    const Block rs = rows(sum, lds, rb), ro = rows(out, ldo, tb);
+    if (overlaps(rs, ro)) return OM_ERR_ALIAS;
+    // a thread reads its elements of a row before it writes them: an output may take the very place of y or of the residual
+    auto one = [&](const void *a, int64_t la, int64_t ba, const void *b, int64_t lb, int64_t bb) { return a == b && ba == bb && (tokens == 1 || la == lb); };
+    for (int i = 0; i < 7; ++i) {
+        const bool s_here = (i == 0 && one(sum, lds, rb, y, ldy, tb)) || (i == 1 && one(sum, lds, rb, residual, ldr, rb));
+        const bool o_here = (i == 0 && one(out, ldo, tb, y, ldy, tb)) || (i == 1 && one(out, ldo, tb, residual, ldr, rb));
+        if ((!s_here && overlaps(rs, in[i])) || (!o_here && overlaps(ro, in[i]))) return OM_ERR_ALIAS;
+    }
+    const om::NormProblem p{tokens, width, y, ldy, dtype, residual, ldr, stream_dtype, gate, ldg, activation, scale, norm == OM_NORM_LAYER, post != 0, eps,
+                            post_weight, post_bias, weight, bias, weight_dtype, sum, lds, out, ldo};
+    return from_cuda(om::launch_block_norm(p, static_cast<cudaStream_t>(stream)));
 }
 
 int om_rope_table(int64_t rows, int64_t rot, double base, int scaling, double factor, double original,

@@ -24,6 +24,8 @@ OM_F32, OM_F16, OM_BF16, OM_I8, OM_E4M3 = range(5)
 DTYPES = {torch.float32: OM_F32, torch.float16: OM_F16, torch.bfloat16: OM_BF16}
 CODES = {torch.int8: OM_I8, torch.float8_e4m3fn: OM_E4M3}
 ROPE_SCALINGS = {None: 0, "plain": 0, "linear": 1, "ntk": 2, "yarn": 3}
+NORMS = {"rms": 0, "layer": 1}
+GATES = {None: 0, "none": 0, "sigmoid": 1, "silu": 2}
 ROPE_PAIRS = {"half": 0, "interleaved": 1}
 
 
@@ -38,6 +40,8 @@ def _declare(L: ctypes.CDLL) -> None:
                              ctypes.c_double)
     L.om_w4_matvec.restype = ci
     L.om_w4_matvec.argtypes = [i64] * 4 + [vp, i64, ci, vp, i64, vp, i64, ci, vp, i64, vp, i64, vp]
+    L.om_block_norm.restype = ci
+    L.om_block_norm.argtypes = [i64, i64, vp, i64, ci, vp, i64, ci, vp, i64, ci, f32, ci, ci, f32, vp, vp, vp, vp, ci, vp, i64, vp, i64, vp]
     L.om_rope_table.restype = ci
     L.om_rope_table.argtypes = [i64, i64, f64, ci, f64, f64, f64, f64, vp, vp]
     L.om_kv_append.restype = ci
@@ -148,6 +152,87 @@ def w4_matvec(x, weight, scales, zeros=None, group: int = 128, out=None, stream=
     _call("om_w4_matvec", device, stream, m, n, k, group, x.data_ptr(), x.stride(0) if m > 1 else k, DTYPES[dtype], weight.data_ptr(), wb,
           scales.data_ptr(), groups, DTYPES[scales.dtype], zp, ldz, out.data_ptr(), ldy)
     return out
+
+
+def _row_vector(t, name, width, dtypes, device):
+    """Pointer of a (width,) operand, None without one."""
+    if t is None:
+        return None
+    _cuda(t, name, 1, dtypes, device)
+    if t.shape[0] != width:
+        raise ValueError(f"{name} must have the shape ({width},)")
+    return t.data_ptr()
+
+
+def _row_major(t, name, shape, dtype, device):
+    """Pointer and row stride of a (tokens, width) operand."""
+    _cuda(t, name, 2, (dtype,), device)
+    if t.shape != shape:
+        raise ValueError(f"{name} must have the shape {tuple(shape)}")
+    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+
+
+def block_norm(y, residual=None, weight=None, bias=None, *, post_weight=None, post_bias=None, gate=None, activation=None, scale: float = 1.0,
+               norm: str = "rms", post=None, normed: bool = True, eps: float = 1e-6, sum_out=None, out=None, stream=None):
+    """The norms before and after a block with its gate and residual scale: x = residual + scale *
+    act(gate) * N_post(y) and h = N(x), in one pass. Returns (x, h).
+
+    y (tokens, width), the block's output; residual of y's type or float32 (None: 0, and x is None unless sum_out is
+    given: the norm before a first block is block_norm(x, weight=w)[1]); gate (tokens, width) or (width,) of y's type, activation
+    None, "sigmoid" or "silu" of it; norm "rms" or "layer"; weights and biases (width,), all of y's type or all
+    float32. post: whether y is normed (None: if it has a weight or bias); normed False: no second norm, h is None. sum_out (of the residual's type, y's
+    without one) may be residual, out may be y. Widths of up to 32768.
+    """
+    device = _cuda(y, "y", 2, DTYPES)
+    shape, dtype = y.shape, y.dtype
+    tokens, width = shape
+    if norm not in NORMS:
+        raise ValueError(f"unknown norm {norm!r}")
+    if activation not in GATES:
+        raise ValueError(f"unknown activation {activation!r}")
+    if post is None:
+        post = post_weight is not None or post_bias is not None
+    rp, ldr, stream_dtype = None, 0, dtype
+    if residual is not None:
+        _cuda(residual, "residual", 2, (dtype, torch.float32), device)
+        stream_dtype = residual.dtype
+        rp, ldr = _row_major(residual, "residual", shape, stream_dtype, device)
+    elif sum_out is not None:
+        _cuda(sum_out, "sum_out", 2, (dtype, torch.float32), device)
+        stream_dtype = sum_out.dtype
+    if gate is None:
+        gp, ldg = None, 0
+        if activation not in (None, "none"):
+            raise ValueError("an activation needs a gate")
+    elif gate.dim() == 1:
+        gp, ldg = _row_vector(gate, "gate", width, (dtype,), device), 0
+    else:
+        gp, ldg = _row_major(gate, "gate", shape, dtype, device)
+    kinds = {w.dtype for w in (weight, bias, post_weight, post_bias) if w is not None}
+    if len(kinds) > 1:
+        raise TypeError("weights and biases must be of one type")
+    weight_dtype = kinds.pop() if kinds else dtype
+    vectors = [_row_vector(w, name, width, (dtype, torch.float32), device)
+               for w, name in ((post_weight, "post_weight"), (post_bias, "post_bias"), (weight, "weight"), (bias, "bias"))]
+    if not normed and (weight is not None or bias is not None or out is not None):
+        raise ValueError("weight, bias and out belong to the second norm")
+    if residual is None and sum_out is None:
+        if not normed:
+            raise ValueError("nothing to compute: no residual, no sum_out and no second norm")
+        sp, lds = None, 0
+    else:
+        if sum_out is None:
+            sum_out = _empty(shape, stream_dtype, y.device, stream)
+        sp, lds = _row_major(sum_out, "sum_out", shape, stream_dtype, device)
+    if not normed:
+        op, ldo = None, 0
+    else:
+        if out is None:
+            out = _empty(shape, dtype, y.device, stream)
+        op, ldo = _row_major(out, "out", shape, dtype, device)
+    _call("om_block_norm", device, stream, tokens, width, y.data_ptr(), y.stride(0) if tokens > 1 else width, DTYPES[dtype], rp, ldr,
+          DTYPES[stream_dtype], gp, ldg, GATES[activation], scale, NORMS[norm], int(bool(post)), eps, *vectors, DTYPES[weight_dtype], sp, lds, op, ldo)
+    return sum_out, out
 
 
 def rope_table(rows: int, rot: int, base: float = 10000.0, scaling=None, factor: float = 1.0,

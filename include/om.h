@@ -370,6 +370,41 @@ OM_API int om_w4_matvec(int64_t m, int64_t n, int64_t k, int64_t group,
                         const uint8_t *zeros, int64_t ldz,
                         void *y, int64_t ldy, void *stream);
 
+/* Norms of a row v of om_block_norm. */
+typedef enum om_norm {
+    OM_NORM_RMS = 0,  /* v / sqrt(mean(v^2) + eps) * weight + bias */
+    OM_NORM_LAYER = 1 /* d / sqrt(mean(d^2) + eps) * weight + bias, d = v - mean(v) */
+} om_norm;
+
+/* What om_block_norm makes of a gate's elements. */
+typedef enum om_gate {
+    OM_GATE_NONE = 0,
+    OM_GATE_SIGMOID = 1, /* 1 / (1 + e^-g) */
+    OM_GATE_SILU = 2     /* g / (1 + e^-g) */
+} om_gate;
+
+/*
+ * The norms before and after a block, with the block's gate and residual scale between
+ * them, row by row of `tokens` rows of `width` elements (up to 32768; more is OM_ERR_TOO_LARGE):
+ *   sum = residual + scale * act(gate) * N_post(y),   out = N(sum).
+ * y, gate and out are of dtype, residual and sum (the residual stream) of stream_dtype,
+ * weights and biases [width] of weight_dtype; both of these are dtype or OM_F32. Leading dimensions in
+ * elements; y, residual and gate may have 0 (one row for all tokens).
+ *   residual NULL: 0. gate NULL: 1. post 0: N_post(y) = y. A weight that is NULL is 1, a bias 0.
+ *   sum NULL: not stored. out NULL: no second norm. One of them must be given.
+ * sum and out may each be y or the residual itself (same address, type and stride); other overlaps with inputs are
+ * OM_ERR_ALIAS. Everything is computed in 32 bits; out is taken from the sum before that
+ * is rounded to its type, and each output is rounded once. Squares above the range of 32 bits
+ * (elements of 2^64 and more) make their row's norm 0 or NaN. Results do not depend on timing.
+ */
+OM_API int om_block_norm(int64_t tokens, int64_t width, const void *y, int64_t ldy, int dtype,
+                         const void *residual, int64_t ldr, int stream_dtype,
+                         const void *gate, int64_t ldg, int activation, float scale,
+                         int norm, int post, float eps,
+                         const void *post_weight, const void *post_bias,
+                         const void *weight, const void *bias, int weight_dtype,
+                         void *sum, int64_t lds, void *out, int64_t ldo, void *stream);
+
 /* Frequencies of om_rope_table: base^(-2i/rot), i < rot / 2, and their scaling for
  * contexts `factor` times longer than the `original` one. */
 typedef enum om_rope_scaling {
