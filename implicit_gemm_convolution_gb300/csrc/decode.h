@@ -104,6 +104,10 @@ struct KvAppendProblem {
     const int32_t *block_table;
     int64_t width;
     const int32_t *ctx, *cu;
+    // NULL, or [axes][tokens] rotary positions and the axis of each pair (NULL: 0)
+    const int32_t *positions;
+    int64_t axes, axis_stride;
+    const int32_t *pair_axis;
 };
 cudaError_t launch_kv_append(const KvAppendProblem &p, cudaStream_t s);
 

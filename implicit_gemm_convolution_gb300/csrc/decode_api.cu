@@ -211,11 +211,12 @@ int om_rope_table(int64_t rows, int64_t rot, double base, int scaling, double fa
                                            static_cast<cudaStream_t>(stream)));
 }
 
-int om_kv_append(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int64_t max_new, int64_t q_heads,
+int om_kv_append_axes(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int64_t max_new, int64_t q_heads,
                  const void *q, int64_t q_ts, int64_t q_hs, const void *k, int64_t k_ts, int64_t k_hs, const void *v,
                  int64_t v_ts, int64_t v_hs, int dtype, const float *table, int64_t rows, int64_t rot, int pairs,
                  const int32_t *block_table, int64_t width, const int32_t *ctx_len, const int32_t *cu, void *q_out,
-                 int64_t qo_ts, int64_t qo_hs, void *stream) {
+                 int64_t qo_ts, int64_t qo_hs, const int32_t *positions, int64_t axes, int64_t axis_stride,
+                      const int32_t *pair_axis, void *stream) {
     const int cst = check_cache(cache);
     if (cst != OM_OK) return cst;
     const om_kv_cache &c = *cache;
@@ -230,8 +231,15 @@ int om_kv_append(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int64_t
     if (rot > 0 && rows > 0 && !table) return OM_ERR_NULL_PTR;
     if (rows > (int64_t(1) << 40)) return OM_ERR_TOO_LARGE;
     if (!aligned(table, 16)) return OM_ERR_ALIGNMENT;
+    if (positions) {
+        if (axes < 1 || (axes > 1 && axis_stride < tokens)) return OM_ERR_INVALID_ARG;
+        if (axes > 65535 || axis_stride > (int64_t(1) << 40)) return OM_ERR_TOO_LARGE;
+    } else if (axes != 0 || pair_axis) {
+        return OM_ERR_INVALID_ARG;
+    }
+    if (!aligned(positions, 4) || !aligned(pair_axis, 4)) return OM_ERR_ALIGNMENT;
     om::KvAppendProblem p{c, seqs, tokens, max_new, q_heads, {q, q_ts, q_hs}, {k, k_ts, k_hs}, {v, v_ts, v_hs},
-                          {q_out, qo_ts, qo_hs}, dtype, table, rows, rot, pairs, block_table, width, ctx_len, cu};
+                          {q_out, qo_ts, qo_hs}, dtype, table, rows, rot, pairs, block_table, width, ctx_len, cu, positions, axes, axis_stride, pair_axis};
     int st = check_heads(p.k, tokens, c.heads, c.dim, dtype, false);
     if (st == OM_OK) st = check_heads(p.v, tokens, c.heads, c.dim, dtype, false);
     if (st == OM_OK && q_heads > 0) st = check_heads(p.q, tokens, q_heads, c.dim, dtype, false);
@@ -244,16 +252,26 @@ int om_kv_append(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int64_t
     const BatchBlocks bb(seqs, block_table, width, ctx_len, cu);
     const Block rk = heads_block(p.k, tokens, c.heads, c.dim, dtype), rv = heads_block(p.v, tokens, c.heads, c.dim, dtype);
     const Block rt = flat(table, static_cast<__int128>(rows) * rot * 4);
-    if (cb.overlap_themselves() || cb.overlap(rk) || cb.overlap(rv) || cb.overlap(rt)) return OM_ERR_ALIAS;
+    const Block rp = rows_of(positions, positions ? axes : 0, tokens, axis_stride, 4), ra = flat(pair_axis, pair_axis ? rot / 2 * 4 : 0);
+    if (cb.overlap_themselves() || cb.overlap(rk) || cb.overlap(rv) || cb.overlap(rt) || cb.overlap(rp) || cb.overlap(ra)) return OM_ERR_ALIAS;
     for (const Block &x : bb.b)
         if (cb.overlap(x)) return OM_ERR_ALIAS;
     if (q_heads > 0) {
         const Block rq = heads_block(p.q, tokens, q_heads, c.dim, dtype), ro = heads_block(p.q_out, tokens, q_heads, c.dim, dtype);
-        if (cb.overlap(rq) || cb.overlap(ro) || overlaps(ro, rk) || overlaps(ro, rv) || overlaps(ro, rt) || bb.overlap(ro) ||
+        if (cb.overlap(rq) || cb.overlap(ro) || overlaps(ro, rk) || overlaps(ro, rv) || overlaps(ro, rt) || overlaps(ro, rp) || overlaps(ro, ra) || bb.overlap(ro) ||
             (!same(p.q, p.q_out) && overlaps(ro, rq)))
             return OM_ERR_ALIAS;
     }
     return from_cuda(om::launch_kv_append(p, static_cast<cudaStream_t>(stream)));
+}
+
+int om_kv_append(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int64_t max_new, int64_t q_heads,
+                 const void *q, int64_t q_ts, int64_t q_hs, const void *k, int64_t k_ts, int64_t k_hs, const void *v,
+                 int64_t v_ts, int64_t v_hs, int dtype, const float *table, int64_t rows, int64_t rot, int pairs,
+                 const int32_t *block_table, int64_t width, const int32_t *ctx_len, const int32_t *cu, void *q_out,
+                 int64_t qo_ts, int64_t qo_hs, void *stream) {
+    return om_kv_append_axes(cache, seqs, tokens, max_new, q_heads, q, q_ts, q_hs, k, k_ts, k_hs, v, v_ts, v_hs, dtype, table, rows, rot, pairs,
+                             block_table, width, ctx_len, cu, q_out, qo_ts, qo_hs, nullptr, 0, 0, nullptr, stream);
 }
 
 int om_kv_read(const om_kv_cache *cache, int64_t seqs, int64_t tokens, const int32_t *block_table, int64_t width,

@@ -34,6 +34,21 @@ __device__ __forceinline__ int unit_offset(int u, int rot, bool interleaved, int
     return 8 * u;
 }
 
+// Cos and sin of unit u's four pairs where each pair has the position of its own axis (token t's); NaN for axes there
+// are not and positions the table does not hold. The pairs' rows differ: 8 bytes each.
+__device__ __forceinline__ void load_turn_of_axes(float *cs, const KvAppendProblem &p, int64_t t, int u) {
+    const int rot = static_cast<int>(p.rot);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t axis = p.pair_axis ? p.pair_axis[4 * u + i] : 0;
+        const int64_t pos = axis >= 0 && axis < p.axes ? p.positions[axis * p.axis_stride + t] : -1;
+        const float2 x = pos >= 0 && pos < p.rows ? __ldg(reinterpret_cast<const float2 *>(p.table + pos * rot + 8 * u + 2 * i))
+                                                  : make_float2(__int_as_float(0x7FC00000), __int_as_float(0x7FC00000));
+        cs[2 * i] = x.x;
+        cs[2 * i + 1] = x.y;
+    }
+}
+
 // The table's cos and sin of unit u's four pairs at position pos; NaN for positions the table does not hold.
 __device__ __forceinline__ void load_turn(float *cs, const float *table, int64_t rows, int rot, int64_t pos, int u) {
     if (pos >= 0 && pos < rows) {
@@ -75,7 +90,7 @@ struct AppendArgs {
 // largest new magnitude first, then its scale, its old codes under the new scale and
 // its new codes. No two blocks write the same page and head, so there is
 // nothing to order between them. A thread keeps its first four units in registers in between.
-template <typename T, int KV, bool ALIGNED>
+template <typename T, int KV, bool ALIGNED, bool AXES>
 __device__ void append_page(const AppendArgs &a, int64_t block) {
     constexpr int kKept = 4;
     const KvAppendProblem &p = a.p;
@@ -107,7 +122,10 @@ __device__ void append_page(const AppendArgs &a, int64_t block) {
         load4<T, ALIGNED>(rows + t * src.ts + second, v + 4);
         if (8 * u < rot) {
             float cs[8];
-            load_turn(cs, p.table, p.rows, rot, lo + t, u);
+            if constexpr (AXES)
+                load_turn_of_axes(cs, p, t0 + lo - start + t, u);
+            else
+                load_turn(cs, p.table, p.rows, rot, lo + t, u);
             turn(v, cs, inter);
         }
     };
@@ -229,30 +247,33 @@ __device__ __forceinline__ void find_tokens(Places *places, const int32_t *cu, i
 }
 
 // Some tokens' queries; four units of a thread in flight.
-template <typename T, bool ALIGNED>
+template <typename T, bool ALIGNED, bool AXES>
 __device__ void rotate_queries(const AppendArgs &a, int64_t block) {
     const KvAppendProblem &p = a.p;
     const int dim = static_cast<int>(p.c.dim), rot = static_cast<int>(p.rot), per_row = dim / 8;
     const int64_t t = block * a.tokens;
     const int count = static_cast<int>(min(static_cast<int64_t>(a.tokens), p.tokens - t));
-    __shared__ Places places;
-    find_tokens(&places, p.cu, p.seqs, p.tokens, t, count);
     const bool inter = p.interleaved != 0;
-    // a token that no sequence owns has no position: its queries become NaN
-    if (threadIdx.x < count) {
-        const int64_t at = places.at[threadIdx.x], b = places.seq[threadIdx.x];
-        int64_t lo, hi;
-        token_range(p.cu, b, p.tokens, &lo, &hi);
-        places.at[threadIdx.x] = at < 0 ? -1 : static_cast<int64_t>(p.ctx[b]) - (hi - lo) + at;
+    // with axes a token's positions are its own, whichever sequence it belongs to
+    __shared__ Places places;
+    if constexpr (!AXES) {
+        find_tokens(&places, p.cu, p.seqs, p.tokens, t, count);
+        // a token that no sequence owns has no position: its queries become NaN
+        if (threadIdx.x < count) {
+            const int64_t at = places.at[threadIdx.x], b = places.seq[threadIdx.x];
+            int64_t lo, hi;
+            token_range(p.cu, b, p.tokens, &lo, &hi);
+            places.at[threadIdx.x] = at < 0 ? -1 : static_cast<int64_t>(p.ctx[b]) - (hi - lo) + at;
+        }
+        __syncthreads();
     }
-    __syncthreads();
     const int units = static_cast<int>(p.q_heads) * per_row, row_log = 31 - __clz(per_row);
     constexpr int kAhead = 4;
 #pragma unroll 1
     for (int tok = 0; tok < count; ++tok) {
         const T *const src = static_cast<const T *>(p.q.p) + (t + tok) * p.q.ts;
         T *const dst = static_cast<T *>(const_cast<void *>(p.q_out.p)) + (t + tok) * p.q_out.ts;
-        const int64_t pos = places.at[tok];
+        const int64_t pos = AXES ? 0 : places.at[tok];
 #pragma unroll 1
         for (int base = threadIdx.x; base < units; base += kAhead * kThreads) {
             float v[kAhead][8];
@@ -274,7 +295,10 @@ __device__ void rotate_queries(const AppendArgs &a, int64_t block) {
                 const int first = unit_offset(u, rot, inter, &second);
                 if (8 * u < rot) {
                     float cs[8];
-                    load_turn(cs, p.table, p.rows, rot, pos, u);
+                    if constexpr (AXES)
+                        load_turn_of_axes(cs, p, t + tok, u);
+                    else
+                        load_turn(cs, p.table, p.rows, rot, pos, u);
                     turn(v[k], cs, inter);
                 }
                 T *const row = dst + (i >> row_log) * p.q_out.hs;
@@ -285,14 +309,14 @@ __device__ void rotate_queries(const AppendArgs &a, int64_t block) {
     }
 }
 
-template <typename T, int KV, bool ALIGNED>
+template <typename T, int KV, bool ALIGNED, bool AXES>
 __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendArgs a) {
     wait_for_earlier();
     const int64_t block = blockIdx.x;
     if (block < a.cache_blocks)
-        append_page<T, KV, ALIGNED>(a, block);
+        append_page<T, KV, ALIGNED, AXES>(a, block);
     else
-        rotate_queries<T, ALIGNED>(a, block - a.cache_blocks);
+        rotate_queries<T, ALIGNED, AXES>(a, block - a.cache_blocks);
 }
 
 struct ReadArgs {
@@ -410,7 +434,9 @@ __global__ void __launch_bounds__(kThreads)
 
 template <typename T, int KV>
 cudaError_t append_typed(const AppendArgs &a, bool aligned, int64_t blocks, cudaStream_t s) {
-    return launch_behind(aligned ? kv_append_kernel<T, KV, true> : kv_append_kernel<T, KV, false>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, s, a);
+    const dim3 grid(static_cast<unsigned>(blocks)), block(kThreads);
+    if (a.p.positions) return launch_behind(aligned ? kv_append_kernel<T, KV, true, true> : kv_append_kernel<T, KV, false, true>, grid, block, 0, s, a);
+    return launch_behind(aligned ? kv_append_kernel<T, KV, true, false> : kv_append_kernel<T, KV, false, false>, grid, block, 0, s, a);
 }
 
 template <typename T>

@@ -45,8 +45,10 @@ def _declare(L: ctypes.CDLL) -> None:
     L.om_rope_table.restype = ci
     L.om_rope_table.argtypes = [i64, i64, f64, ci, f64, f64, f64, f64, vp, vp]
     L.om_kv_append.restype = ci
-    L.om_kv_append.argtypes = [vp] + [i64] * 4 + [vp, i64, i64] * 3 + [ci, vp, i64, i64, ci, vp, i64, vp, vp,
-                                                                      vp, i64, i64, vp]
+    append = [vp] + [i64] * 4 + [vp, i64, i64] * 3 + [ci, vp, i64, i64, ci, vp, i64, vp, vp, vp, i64, i64]
+    L.om_kv_append.argtypes = append + [vp]
+    L.om_kv_append_axes.restype = ci
+    L.om_kv_append_axes.argtypes = append + [vp, i64, i64, vp, vp]
     L.om_kv_read.restype = ci
     L.om_kv_read.argtypes = [vp, i64, i64, vp, i64, vp, vp, vp, vp, ci, vp]
     L.om_kv_workspace_bytes.restype = ctypes.c_size_t
@@ -301,14 +303,33 @@ def _heads(t, name, shape, dtype, device):
     return t.data_ptr(), ts, hs
 
 
+def rope_axes(sections, order: str = "blocks", device="cuda"):
+    """The axis that turns each rotated pair, int32 (sum of sections,), for kv_append: sections[a] pairs of axis
+    a, one axis after the other ("blocks"), or in turns as long as each has pairs left ("turns")."""
+    sections = [int(n) for n in sections]
+    if order not in ("blocks", "turns"):
+        raise ValueError(f"unknown order {order!r}")
+    if not sections or min(sections) < 0:
+        raise ValueError("sections must be numbers of pairs")
+    if order == "blocks":
+        axis = [a for a, n in enumerate(sections) for _ in range(n)]
+    else:
+        axis = [a for i in range(max(sections)) for a, n in enumerate(sections) if i < n]
+    return torch.tensor(axis, dtype=torch.int32, device=device)
+
+
 def kv_append(cache, q, k, v, table, block_table, ctx_len, cu, max_new: int, pairs: str = "half", q_out=None,
-              stream=None):
+              stream=None, positions=None, pair_axis=None):
     """Stores the new tokens' keys (rotated) and values in the cache and returns the
     rotated queries.
 
     q (tokens, q heads, dim) or None, k and v (tokens, heads, dim) may be parts of one buffer; table
     from rope_table (None: no rotation); max_new at least the largest number of new
     tokens of a sequence. q_out may be q.
+
+    positions, int32 (axes, tokens): the tokens' rotary positions on each axis, where these are not their places in the
+    cache (patches of images and videos; None: the places). pair_axis, int32 (rot // 2,): the axis
+    that turns each pair, as rope_axes lays them out (None: axis 0).
     """
     device = cache.device
     _cuda(k, "k", 3, DTYPES, device)
@@ -337,8 +358,23 @@ def kv_append(cache, q, k, v, table, block_table, ctx_len, cu, max_new: int, pai
         if two != 2 or not table.is_contiguous():
             raise ValueError("table must be a contiguous (rows, rot // 2, 2) tensor")
         tp, rot = table.data_ptr(), 2 * rot
-    _call("om_kv_append", device, stream, cache._ref, seqs, tokens, max_new, q_heads, *qa, *ka, *va, DTYPES[dtype], tp, rows, rot,
-          ROPE_PAIRS[pairs], *batch, *oa)
+    args = cache._ref, seqs, tokens, max_new, q_heads, *qa, *ka, *va, DTYPES[dtype], tp, rows, rot, ROPE_PAIRS[pairs], *batch, *oa
+    if positions is None:
+        if pair_axis is not None:
+            raise ValueError("pair_axis needs positions")
+        _call("om_kv_append", device, stream, *args)
+        return q_out
+    _cuda(positions, "positions", 2, _I32, device)
+    axes = positions.shape[0]
+    if positions.shape[1] != tokens or axes < 1:
+        raise ValueError("positions must have the shape (axes, tokens)")
+    ap = None
+    if pair_axis is not None:
+        _cuda(pair_axis, "pair_axis", 1, _I32, device)
+        if pair_axis.shape[0] * 2 != rot:
+            raise ValueError("pair_axis must have an axis for each pair of the table")
+        ap = pair_axis.data_ptr()
+    _call("om_kv_append_axes", device, stream, *args, positions.data_ptr(), axes, positions.stride(0) if axes > 1 else tokens, ap)
     return q_out
 
 

@@ -480,6 +480,26 @@ OM_API int om_kv_append(const om_kv_cache *cache, int64_t seqs, int64_t tokens, 
                         void *q_out, int64_t qo_ts, int64_t qo_hs, void *stream);
 
 /*
+ * om_kv_append where a token's rotary positions are not its place in the cache: positions
+ * [axes][tokens] (rows axis_stride elements apart) holds one for each axis (time, height and width of a
+ * patch of an image or video; text repeats one), pair_axis [rot / 2] the axis of each pair (NULL:
+ * axis 0 for all). Pair i of token t is turned by entry i of row positions[pair_axis[i]][t] of the table;
+ * axes outside [0, axes) and positions outside the table turn to NaN. The queries of all tokens of the call are turned, those
+ * that no sequence owns too; where a token is stored does not change. positions NULL, axes 0 and pair_axis NULL: om_kv_append.
+ */
+OM_API int om_kv_append_axes(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int64_t max_new,
+                             int64_t q_heads,
+                             const void *q, int64_t q_ts, int64_t q_hs,
+                             const void *k, int64_t k_ts, int64_t k_hs,
+                             const void *v, int64_t v_ts, int64_t v_hs, int dtype,
+                             const float *table, int64_t rows, int64_t rot, int pairs,
+                             const int32_t *block_table, int64_t width,
+                             const int32_t *ctx_len, const int32_t *cu,
+                             void *q_out, int64_t qo_ts, int64_t qo_hs,
+                             const int32_t *positions, int64_t axes, int64_t axis_stride,
+                             const int32_t *pair_axis, void *stream);
+
+/*
  * Reads tokens back as values: token i of sequence b is position start[b] + i.
  * k_out, v_out: [tokens][heads][dim] contiguous, 16-byte aligned, dtype OM_F32, OM_F16
  * or OM_BF16; fl(code * scale), rounded once more to a 16-bit type.
