@@ -134,6 +134,7 @@ struct KvAttentionProblem {
     float scale;
     int64_t window;  // 0: none
     void *workspace;
+    int sinks;  // first positions that are seen besides the window
 };
 // Query rows that a block holds at once (query tokens times heads of a group,
 // in eights), and the workspace of a call: a page of arrival counters, then
@@ -151,6 +152,10 @@ inline size_t kv_workspace_bytes(int64_t group, int64_t dim, int64_t max_new) {
 cudaError_t launch_kv_attention_f32(const KvAttentionProblem &p, cudaStream_t s);
 cudaError_t launch_kv_attention_f16(const KvAttentionProblem &p, cudaStream_t s);
 cudaError_t launch_kv_attention_bf16(const KvAttentionProblem &p, cudaStream_t s);
+// with first tokens that stay visible
+cudaError_t launch_kv_attention_sinks_f32(const KvAttentionProblem &p, cudaStream_t s);
+cudaError_t launch_kv_attention_sinks_f16(const KvAttentionProblem &p, cudaStream_t s);
+cudaError_t launch_kv_attention_sinks_bf16(const KvAttentionProblem &p, cudaStream_t s);
 
 cudaError_t launch_rope_table(int64_t rows, int64_t rot, double base, int scaling, double factor,
                               double original, double beta_fast, double beta_slow, float *table,

@@ -300,14 +300,14 @@ size_t om_kv_workspace_bytes(int64_t kv_heads, int64_t q_heads, int64_t dim, int
     return om::kv_workspace_bytes(q_heads / kv_heads, dim, max_new);
 }
 
-int om_kv_attention(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int64_t max_new, int64_t q_heads,
-                    const void *q, int64_t q_ts, int64_t q_hs, int dtype, const int32_t *block_table, int64_t width,
-                    const int32_t *ctx_len, const int32_t *cu, float scale, int64_t window, void *out, int64_t o_ts,
-                    int64_t o_hs, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+int om_kv_attention_sinks(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int64_t max_new, int64_t q_heads,
+                          const void *q, int64_t q_ts, int64_t q_hs, int dtype, const int32_t *block_table, int64_t width,
+                          const int32_t *ctx_len, const int32_t *cu, float scale, int64_t window, int64_t sinks, void *out,
+                          int64_t o_ts, int64_t o_hs, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
     const int cst = check_cache(cache);
     if (cst != OM_OK) return cst;
     const om_kv_cache &c = *cache;
-    if (seqs < 0 || tokens < 0 || max_new < 0 || q_heads < 1 || window < 0) return OM_ERR_INVALID_ARG;
+    if (seqs < 0 || tokens < 0 || max_new < 0 || q_heads < 1 || window < 0 || sinks < 0) return OM_ERR_INVALID_ARG;
     if (q_heads % c.heads != 0) return OM_ERR_INVALID_ARG;
     if (!float_type(dtype)) return OM_ERR_UNSUPPORTED;
     if (seqs == 0 || tokens == 0) return OM_OK;
@@ -318,9 +318,11 @@ int om_kv_attention(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int6
     // pieces of 64 positions of every key head and eight query rows, at most
     const __int128 units = static_cast<__int128>(width * c.page / 64 + 1) * c.heads * (tokens * (q_heads / c.heads) / 8 + seqs);
     if (units > kLim31 - (1 << 20)) return OM_ERR_TOO_LARGE;
-    // a window of all positions there can be is none: the kernel takes positions less the window in 64 bits
+    // a window of all positions there can be is none (the kernel takes positions less the window in 64 bits), and so is one beside first
+    // positions that are all the table has
+    const bool bound = window > 0 && window < kLim31 && sinks < width * c.page;
     om::KvAttentionProblem p{c, seqs, tokens, max_new, q_heads, {q, q_ts, q_hs}, {out, o_ts, o_hs}, dtype, lse,
-                             block_table, width, ctx_len, cu, scale, window < kLim31 ? window : 0, workspace};
+                             block_table, width, ctx_len, cu, scale, bound ? window : 0, workspace, bound ? static_cast<int>(sinks) : 0};
     int st = check_heads(p.q, tokens, q_heads, c.dim, dtype, false);
     if (st == OM_OK) st = check_heads(p.out, tokens, q_heads, c.dim, dtype, true);
     if (st != OM_OK) return st;
@@ -341,8 +343,17 @@ int om_kv_attention(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int6
             if (overlaps(w[i], w[j])) return OM_ERR_ALIAS;
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (dtype == OM_F32) return from_cuda(om::launch_kv_attention_f32(p, s));
-    return from_cuda(dtype == OM_F16 ? om::launch_kv_attention_f16(p, s) : om::launch_kv_attention_bf16(p, s));
+    if (dtype == OM_F32) return from_cuda(p.sinks > 0 ? om::launch_kv_attention_sinks_f32(p, s) : om::launch_kv_attention_f32(p, s));
+    if (dtype == OM_F16) return from_cuda(p.sinks > 0 ? om::launch_kv_attention_sinks_f16(p, s) : om::launch_kv_attention_f16(p, s));
+    return from_cuda(p.sinks > 0 ? om::launch_kv_attention_sinks_bf16(p, s) : om::launch_kv_attention_bf16(p, s));
+}
+
+int om_kv_attention(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int64_t max_new, int64_t q_heads,
+                    const void *q, int64_t q_ts, int64_t q_hs, int dtype, const int32_t *block_table, int64_t width,
+                    const int32_t *ctx_len, const int32_t *cu, float scale, int64_t window, void *out, int64_t o_ts,
+                    int64_t o_hs, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+    return om_kv_attention_sinks(cache, seqs, tokens, max_new, q_heads, q, q_ts, q_hs, dtype, block_table, width, ctx_len, cu, scale, window, 0, out,
+                                 o_ts, o_hs, lse, workspace, workspace_bytes, stream);
 }
 
 }  // extern "C"

@@ -171,7 +171,9 @@ struct Args {
     bool out_fours, q_fours;  // outputs and queries are aligned for stores and loads of four
 };
 
-// What a block does for one sequence. Units and positions are below 2^31.
+// What a block does for one sequence. Units and positions are below 2^31. With first tokens that stay visible, positions here
+// are places in a sequence that leaves out the gap between them and the window of the first query, a multiple of
+// units and pages: only the page table is asked for the true ones.
 struct Sequence {
     int b, t0;  // t0: its first token in the batch
     int queries, row_blocks;
@@ -180,7 +182,14 @@ struct Sequence {
     int limit;      // positions before it are in the cache
 };
 
-template <int ROWS>
+// The positions before the gap between the first ones and the window of a query at `start`, and the gap's length (0: none).
+__device__ __forceinline__ int2 gap_of(const KvAttentionProblem &p, int64_t start) {
+    const int step = max(kUnit, static_cast<int>(p.c.page)), head = (p.sinks + step - 1) / step * step;
+    const int lo = static_cast<int>(max(start - p.window + 1, static_cast<int64_t>(0)));
+    return make_int2(head, max(lo / step * step - head, 0));
+}
+
+template <int ROWS, bool SINKS>
 __device__ __forceinline__ Sequence sequence_of(const KvAttentionProblem &p, int64_t b, int group) {
     Sequence s;
     int64_t t0, t1;
@@ -194,6 +203,12 @@ __device__ __forceinline__ Sequence sequence_of(const KvAttentionProblem &p, int
     s.limit = static_cast<int>(max(min(ctx, reach), static_cast<int64_t>(0)));
     const int lo = p.window > 0 ? static_cast<int>(max(s.start - p.window + 1, static_cast<int64_t>(0))) : 0;
     s.first_unit = lo / kUnit;
+    if constexpr (SINKS) {
+        const int2 gap = gap_of(p, s.start);
+        s.first_unit = 0;
+        s.start -= gap.y;
+        if (gap.y > 0) s.limit = s.limit >= gap.x + gap.y ? s.limit - gap.y : min(s.limit, gap.x);
+    }
     s.units = max((s.limit + kUnit - 1) / kUnit - s.first_unit, 1);  // rows that see nothing are written too
     return s;
 }
@@ -255,7 +270,7 @@ struct Config {
 // BLOCKS: of an SM, at least. Three where the registers allow it (heads of up to 128, 8 rows of 16 bits), two elsewhere. With two, 256
 // sequences of 500 tokens, 8 key heads, take 66 us instead of 57, 64 of up to 8000 tokens with heads of 64 101 instead of 89; one of
 // 131071 tokens, whose parts are more with three, the same (float16 59.5 and 59.9 us, bfloat16 59.4 and 57.9).
-template <typename T, int KV, int DIM, int NT, int BLOCKS>
+template <typename T, int KV, int DIM, int NT, int BLOCKS, bool SINKS>
 __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __grid_constant__ Args a) {
     using S = Shape<DIM>;
     using C = Config<T, DIM, NT>;
@@ -264,6 +279,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
     constexpr bool kQShared = C::kQShared;
     constexpr int kFrag = S::kSteps * NT;  // float4 of O per lane
     const KvAttentionProblem &p = a.p;
+    const int sinks = SINKS ? p.sinks : 0;
     unsigned *const counters = static_cast<unsigned *>(p.workspace);
     float *const slots = reinterpret_cast<float *>(static_cast<uint8_t *>(p.workspace) + kKvCounterBytes);
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31, g = lane / 4, c = lane % 4;
@@ -272,7 +288,8 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
 
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ float row_factor[kRows];
-    __shared__ int2 row_seen[kRows];  // a row sees the positions in (x, y]
+    __shared__ int2 row_seen[kRows];  // a row sees the positions in (x, y] and, up to y, the first p.sinks
+    __shared__ int2 gap_pages[kWarps];  // of the warp's segment: pages before the gap, pages left out
     __shared__ int scan[kWarps], scan_longest[kWarps], found_before;
     __shared__ unsigned scan_doubt[kWarps];
     __shared__ Sequence found;
@@ -290,7 +307,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
     bool falls = false;
 #pragma unroll 1
     for (int i = threadIdx.x; i < seqs; i += kThreads) {
-        const Sequence s = sequence_of<kRows>(p, i, group);
+        const Sequence s = sequence_of<kRows, SINKS>(p, i, group);
         mine += heads * s.row_blocks * s.units;
         longest = max(longest, s.units);
         falls |= p.cu[i] > p.cu[i + 1];
@@ -327,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
         Sequence s;
         int n = 0;
         if (base + static_cast<int>(threadIdx.x) < seqs) {
-            s = sequence_of<kRows>(p, base + threadIdx.x, group);
+            s = sequence_of<kRows, SINKS>(p, base + threadIdx.x, group);
             n = heads * s.row_blocks * s.units;
         }
         int up = n;
@@ -374,8 +391,12 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
     const int copy_row = lane * 16 / DIM;
     const uint32_t copy_to = S::place(copy_row, lane % (DIM / 16));
     bool f_new = true;
+    auto true_page = [&](int j) -> int {
+        if constexpr (SINKS) return j + (j >= gap_pages[warp].x ? gap_pages[warp].y : 0);
+        return j;
+    };
     auto load_id = [&](int j) -> int {
-        const int id = j < pages_end ? p.block_table[seq.b * p.width + j] : -1;
+        const int id = j < pages_end ? p.block_table[seq.b * p.width + true_page(j)] : -1;
         return id < p.c.pages ? id : -1;
     };
     auto load_scales = [&](int id, float *ka, float *va) {
@@ -438,6 +459,16 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
     const int value_at[2] = {S::place(2 * c, DIM == 64 ? g / 2 : g) + (DIM == 64 ? g % 2 * 8 : 0),
                              S::place(2 * c + 1, DIM == 64 ? g / 2 : g) + (DIM == 64 ? g % 2 * 8 : 0)};
 
+    // Whether a row that sees `seen` does not see position t, and nothing of the tile at pos.
+    auto hidden = [&](int t, const int2 &seen) {
+        if constexpr (SINKS) return (t <= seen.x && t >= sinks) || t > seen.y;
+        return t <= seen.x || t > seen.y;
+    };
+    auto hidden_until = [&](int pos, const int2 &seen) {
+        if constexpr (SINKS) return (pos + kTile - 1 <= seen.x && pos >= sinks) || pos > seen.y;
+        return pos + kTile - 1 <= seen.x || pos > seen.y;
+    };
+
     // Value codes that are NaN, in a tile that not every row sees as a whole: a weight of 0 would not hide them. Rows that see one
     // become NaN in its dimension, and the code becomes 0. o, and the tile's values at vsrc.
     auto hide_nan_codes = [&](float (&o)[S::kSteps][NT][4], uint8_t *vsrc, int pos) {
@@ -457,7 +488,10 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
                     const int2 seen = row_seen[nt * 8 + 2 * c + j];
-                    sees[nt][j] = pos + r > seen.x && pos + r <= seen.y;
+                    if constexpr (SINKS)
+                        sees[nt][j] = !hidden(pos + r, seen);
+                    else
+                        sees[nt][j] = pos + r > seen.x && pos + r <= seen.y;
                 }
 #pragma unroll
             for (int i = 0; i < S::kValueChunks; ++i) {
@@ -501,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
             int n;
             while (u >= before + (n = heads * seq.row_blocks * seq.units)) {
                 before += n;
-                seq = sequence_of<kRows>(p, seq.b + 1, group);
+                seq = sequence_of<kRows, SINKS>(p, seq.b + 1, group);
             }
             const int item = (u - before) / seq.units;
             part.begin = before + item * seq.units;
@@ -530,9 +564,19 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
             const int pos0 = (seq.first_unit + (u - part.begin)) * kUnit, each = (stop - u) * kTile;
             w0 = pos0 + warp * each;
             w1 = min(w0 + each, hi);
-            if (w0 < lo) w0 = lo / kTile * kTile;
+            if constexpr (SINKS) {
+                if (w0 >= sinks && w0 < lo) w0 = lo / kTile * kTile;
+            } else {
+                if (w0 < lo) w0 = lo / kTile * kTile;
+            }
             pb = w0 >> page_log;
             pages_end = w0 < w1 ? (hi + page - 1) >> page_log : 0;  // inside the table: hi is
+            if constexpr (SINKS) {
+                const int2 gap = gap_of(p, static_cast<int64_t>(p.ctx[seq.b]) - seq.queries);
+                __syncwarp();
+                if (lane == 0) gap_pages[warp] = make_int2(gap.x >> page_log, gap.y >> page_log);
+                __syncwarp();
+            }
             id0 = load_id(pb + lane);
             id1 = load_id(pb + 32 + lane);
             if constexpr (C::kEarly) {
@@ -819,11 +863,11 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const int t = pos + g + (j & 2) * 4;
-                        if (!page_ok || t <= seen[j & 1].x || t > seen[j & 1].y) s[nt][j] = -INFINITY;
+                        if (!page_ok || hidden(t, seen[j & 1])) s[nt][j] = -INFINITY;
                     }
 #pragma unroll
                     for (int j = 0; j < 2; ++j)
-                        if (!page_ok || pos + kTile - 1 <= seen[j].x || pos > seen[j].y) sees_none |= column_bit << (8 * nt + j);
+                        if (!page_ok || hidden_until(pos, seen[j])) sees_none |= column_bit << (8 * nt + j);
                 }
                 if constexpr (KV == OM_E4M3) hide_nan_codes(o, smem + warp * C::kRing + src_at + kTile * DIM, pos);
             }
@@ -1084,17 +1128,17 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
     }
 }
 
-template <typename T, int KV, int DIM, int NT, int BLOCKS>
+template <typename T, int KV, int DIM, int NT, int BLOCKS, bool SINKS>
 cudaError_t launch(const Args &a, cudaStream_t s) {
     constexpr int kSmem = Config<T, DIM, NT>::kSmem;
     static PerDevice blocks;
     std::atomic<int> *const kept = blocks.here();
     int blocks_per_sm = kept ? kept->load(std::memory_order_relaxed) : 0;
     if (blocks_per_sm == 0) {
-        cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<T, KV, DIM, NT, BLOCKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<T, KV, DIM, NT, BLOCKS, SINKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         int n = 0;
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kv_attention_kernel<T, KV, DIM, NT, BLOCKS>, kThreads, kSmem);
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kv_attention_kernel<T, KV, DIM, NT, BLOCKS, SINKS>, kThreads, kSmem);
         if (e != cudaSuccess) return e;
         blocks_per_sm = n < 1 ? 1 : n;
         if (kept) kept->store(blocks_per_sm, std::memory_order_relaxed);
@@ -1107,32 +1151,32 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
     if (grid > Config<T, DIM, NT>::kMaxBlocks) grid = Config<T, DIM, NT>::kMaxBlocks;
     if (units < grid * kMinUnits) grid = static_cast<int64_t>((units + kMinUnits - 1) / kMinUnits);
     if (grid < 1) grid = 1;
-    return launch_behind(kv_attention_kernel<T, KV, DIM, NT, BLOCKS>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmem, s, a);
+    return launch_behind(kv_attention_kernel<T, KV, DIM, NT, BLOCKS, SINKS>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmem, s, a);
 }
 
-template <typename T, int KV, int DIM>
+template <typename T, bool SINKS, int KV, int DIM>
 cudaError_t by_rows(const Args &a, cudaStream_t s) {
     const int64_t rows = kv_block_rows(a.p.q_heads / a.p.c.heads, a.p.max_new);
-    if (rows == 8) return launch<T, KV, DIM, 1, DIM <= 128 && sizeof(T) == 2 ? 3 : 2>(a, s);
-    return launch<T, KV, DIM, 2, 2>(a, s);
+    if (rows == 8) return launch<T, KV, DIM, 1, DIM <= 128 && sizeof(T) == 2 ? 3 : 2, SINKS>(a, s);
+    return launch<T, KV, DIM, 2, 2, SINKS>(a, s);
 }
 
-template <typename T, int KV>
+template <typename T, bool SINKS, int KV>
 cudaError_t by_dim(const Args &a, cudaStream_t s) {
-    if (a.p.c.dim == 64) return by_rows<T, KV, 64>(a, s);
-    if (a.p.c.dim == 128) return by_rows<T, KV, 128>(a, s);
-    return by_rows<T, KV, 256>(a, s);
+    if (a.p.c.dim == 64) return by_rows<T, SINKS, KV, 64>(a, s);
+    if (a.p.c.dim == 128) return by_rows<T, SINKS, KV, 128>(a, s);
+    return by_rows<T, SINKS, KV, 256>(a, s);
 }
 
-template <typename T>
+template <typename T, bool SINKS>
 cudaError_t by_codes(const Args &a, cudaStream_t s) {
-    return a.p.c.dtype == OM_I8 ? by_dim<T, OM_I8>(a, s) : by_dim<T, OM_E4M3>(a, s);
+    return a.p.c.dtype == OM_I8 ? by_dim<T, SINKS, OM_I8>(a, s) : by_dim<T, SINKS, OM_E4M3>(a, s);
 }
 
-template <typename T>
+template <typename T, bool SINKS>
 cudaError_t run_kv_attention(const KvAttentionProblem &p, cudaStream_t s) {
     auto fours = [](const Heads &x) { return reinterpret_cast<uintptr_t>(x.p) % (4 * sizeof(T)) == 0 && x.ts % 4 == 0 && x.hs % 4 == 0; };
-    return by_codes<T>(Args{p, fours(p.out), fours(p.q)}, s);
+    return by_codes<T, SINKS>(Args{p, fours(p.out), fours(p.q)}, s);
 }
 
 }  // namespace

@@ -54,8 +54,10 @@ def _declare(L: ctypes.CDLL) -> None:
     L.om_kv_workspace_bytes.restype = ctypes.c_size_t
     L.om_kv_workspace_bytes.argtypes = [i64] * 4
     L.om_kv_attention.restype = ci
-    L.om_kv_attention.argtypes = [vp] + [i64] * 4 + [vp, i64, i64, ci, vp, i64, vp, vp, f32, i64, vp, i64, i64, vp,
-                                                    vp, ctypes.c_size_t, vp]
+    batch, rest = [vp] + [i64] * 4 + [vp, i64, i64, ci, vp, i64, vp, vp, f32, i64], [vp, i64, i64, vp, vp, ctypes.c_size_t, vp]
+    L.om_kv_attention.argtypes = batch + rest
+    L.om_kv_attention_sinks.restype = ci
+    L.om_kv_attention_sinks.argtypes = batch + [i64] + rest
 
 
 _functions = None
@@ -414,9 +416,9 @@ def new_kv_workspace(cache, q_heads: int, max_new: int):
 
 
 def kv_attention(cache, q, block_table, ctx_len, cu, max_new: int, scale=None, window: int = 0, out=None, lse=None,
-                 workspace=None, stream=None):
+                 workspace=None, stream=None, sinks: int = 0):
     """Attention of each sequence's last tokens' queries, q (tokens, q heads, dim),
-    to its cached tokens, causal, within `window` positions (0: all).
+    to its cached tokens, causal, within `window` positions (0: all) and the sequence's first `sinks` ones.
 
     scale: default dim ** -0.5. lse: float32 (tokens, q heads), receives the natural log of the sums
     of exponentials. workspace: from new_kv_workspace; without one each sequence
@@ -447,6 +449,6 @@ def kv_attention(cache, q, block_table, ctx_len, cu, max_new: int, scale=None, w
         if workspace.get_device() != device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the cache's device")
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _call("om_kv_attention", device, stream, cache._ref, seqs, tokens, max_new, q_heads, q.data_ptr(), ts, hs, DTYPES[dtype], *batch,
-          dim ** -0.5 if scale is None else scale, window, *oa, lp, ws, ws_bytes)
+    _call("om_kv_attention_sinks", device, stream, cache._ref, seqs, tokens, max_new, q_heads, q.data_ptr(), ts, hs, DTYPES[dtype], *batch,
+          dim ** -0.5 if scale is None else scale, window, sinks, *oa, lp, ws, ws_bytes)
     return out

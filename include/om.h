@@ -544,6 +544,20 @@ OM_API int om_kv_attention(const om_kv_cache *cache, int64_t seqs, int64_t token
                            void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * om_kv_attention whose window leaves a sequence's first `sinks` tokens visible: the query at position p sees
+ * the positions t <= p with t > p - window or t < sinks. With window 0, or sinks 0, it is om_kv_attention.
+ * What lies between is neither read nor counted as work.
+ */
+OM_API int om_kv_attention_sinks(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int64_t max_new,
+                                 int64_t q_heads,
+                                 const void *q, int64_t q_ts, int64_t q_hs, int dtype,
+                                 const int32_t *block_table, int64_t width,
+                                 const int32_t *ctx_len, const int32_t *cu, float scale, int64_t window,
+                                 int64_t sinks,
+                                 void *out, int64_t o_ts, int64_t o_hs, float *lse,
+                                 void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Synchronises stream, then reads and clears the library's device-wide status
  * words for the current device. Every device-side wait in the library's
  * kernels (mbarrier waits of the TMA and tensor-core pipelines) is bounded;
