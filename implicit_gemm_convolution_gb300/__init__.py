@@ -337,7 +337,8 @@ def conv2d_ex(x, w, stride: int = 1, padding: int = 0, dilation: int = 1, groups
 
 
 # the decoding operators need torch when they are first named, not at import
-_DECODE = ("PagedKVCache", "block_norm", "kv_append", "kv_attention", "kv_read", "new_kv_workspace", "rope_axes", "rope_table", "w4_matvec")
+_DECODE = ("PagedKVCache", "block_norm", "kv_append", "kv_attention", "kv_read", "kv_shared_attention", "new_kv_workspace",
+           "new_shared_workspace", "rope_axes", "rope_table", "w4_matvec")
 
 
 def __getattr__(name):

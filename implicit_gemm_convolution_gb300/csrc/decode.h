@@ -156,6 +156,42 @@ cudaError_t launch_kv_attention_bf16(const KvAttentionProblem &p, cudaStream_t s
 cudaError_t launch_kv_attention_sinks_f32(const KvAttentionProblem &p, cudaStream_t s);
 cudaError_t launch_kv_attention_sinks_f16(const KvAttentionProblem &p, cudaStream_t s);
 cudaError_t launch_kv_attention_sinks_bf16(const KvAttentionProblem &p, cudaStream_t s);
+// as a part of a larger softmax: out is 32 bits, lse holds (maximum, sum) of each row, as kv_shared.cuh joins them
+cudaError_t launch_kv_attention_part_f32(const KvAttentionProblem &p, cudaStream_t s);
+cudaError_t launch_kv_attention_part_f16(const KvAttentionProblem &p, cudaStream_t s);
+cudaError_t launch_kv_attention_part_bf16(const KvAttentionProblem &p, cudaStream_t s);
+
+// Attention to prefixes that groups of sequences share: sequences group_at[j] .. group_at[j + 1] - 1 have prefix_len[j] tokens
+// in the pages prefix_table[j]. Blocks leave (maximum, sum, weighted mean) of each row: those that have an item alone in its rows'
+// places, the others in two slots a block.
+constexpr int kSharedRows = 128;       // rows of an item: token times query head of a key head
+constexpr int kSharedMinUnits = 1;     // tiles that a block takes at least
+constexpr int kSharedMostBlocks = 304; // two an SM
+// Positions of a tile: what leaves two blocks of an SM their shared and tensor memory (heads of 256: one block).
+constexpr int shared_tile(int64_t dim, int parts) { return dim == 256 || (dim == 128 && parts == 2) ? 64 : 128; }
+struct SharedProblem {
+    om_kv_cache c;
+    int64_t seqs, tokens, q_heads, groups;
+    Heads q;
+    int dtype, group;  // group: query heads of a key head
+    bool q_fours;
+    const int32_t *prefix_table;
+    int64_t prefix_width;
+    const int32_t *prefix_len, *group_at, *cu;
+    float scale;
+    int tile_log;
+    int64_t blocks, slot_rows;
+    float2 *whole_state, *slot_state;  // [tokens][q_heads], [2 blocks][slot_rows]
+    float *whole, *slots;              // and their values, [dim] each
+    const float2 *own_state;           // of the sequences' own tokens, [tokens][q_heads]
+    const float *own;
+    Heads out;
+    float *lse;
+    unsigned *status;
+};
+cudaError_t launch_kv_shared_i8(const SharedProblem &p, cudaStream_t s);
+cudaError_t launch_kv_shared_e4m3(const SharedProblem &p, cudaStream_t s);
+cudaError_t launch_kv_shared_join(const SharedProblem &p, cudaStream_t s);
 
 cudaError_t launch_rope_table(int64_t rows, int64_t rot, double base, int scaling, double factor,
                               double original, double beta_fast, double beta_slow, float *table,

@@ -122,6 +122,35 @@ struct BatchBlocks {
     bool overlap(const Block &x) const { return overlaps(x, b[0]) || overlaps(x, b[1]) || overlaps(x, b[2]); }
 };
 
+// Where a call on shared prefixes keeps what its kernels hand on, behind the scratch of the attention to own tokens.
+struct SharedPlaces {
+    float2 *whole_state, *own_state, *slot_state;
+    float *whole, *own, *slots;
+    int64_t slot_rows;
+    size_t bytes;
+};
+SharedPlaces shared_places(void *workspace, int64_t group, int64_t q_heads, int64_t dim, int64_t max_new, int64_t tokens) {
+    size_t used = om::kv_workspace_bytes(group, dim, max_new);
+    auto take = [&](int64_t bytes) {
+        used = (used + 15) / 16 * 16;
+        uint8_t *const at = static_cast<uint8_t *>(workspace) + used;
+        used += static_cast<size_t>(bytes);
+        return workspace ? at : nullptr;
+    };
+    SharedPlaces p{};
+    const int64_t rows = tokens * q_heads;
+    p.slot_rows = tokens * group < om::kSharedRows ? tokens * group : om::kSharedRows;
+    const int64_t slots = 2 * om::kSharedMostBlocks * p.slot_rows;
+    p.whole_state = reinterpret_cast<float2 *>(take(rows * 8));
+    p.own_state = reinterpret_cast<float2 *>(take(rows * 8));
+    p.slot_state = reinterpret_cast<float2 *>(take(slots * 8));
+    p.whole = reinterpret_cast<float *>(take(rows * dim * 4));
+    p.own = reinterpret_cast<float *>(take(rows * dim * 4));
+    p.slots = reinterpret_cast<float *>(take(slots * dim * 4));
+    p.bytes = used;
+    return p;
+}
+
 bool same(const Heads &a, const Heads &b) { return a.p == b.p && a.ts == b.ts && a.hs == b.hs; }
 
 }  // namespace
@@ -354,6 +383,87 @@ int om_kv_attention(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int6
                     int64_t o_hs, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
     return om_kv_attention_sinks(cache, seqs, tokens, max_new, q_heads, q, q_ts, q_hs, dtype, block_table, width, ctx_len, cu, scale, window, 0, out,
                                  o_ts, o_hs, lse, workspace, workspace_bytes, stream);
+}
+
+size_t om_kv_shared_workspace_bytes(int64_t kv_heads, int64_t q_heads, int64_t dim, int64_t max_new, int64_t tokens) {
+    if (kv_heads < 1 || q_heads < 1 || q_heads % kv_heads != 0 || dim < 1 || max_new < 1 || dim > 65536 || tokens < 1) return 0;
+    if (q_heads > 65535 || tokens > kLim31 / q_heads) return 0;
+    return shared_places(nullptr, q_heads / kv_heads, q_heads, dim, max_new, tokens).bytes;
+}
+
+int om_kv_shared_attention(const om_kv_cache *cache, int64_t groups, const int32_t *prefix_table, int64_t prefix_width, const int32_t *prefix_len,
+                           const int32_t *group_offsets, int64_t seqs, int64_t tokens, int64_t max_new, int64_t q_heads, const void *q, int64_t q_ts,
+                           int64_t q_hs, int dtype, const int32_t *block_table, int64_t width, const int32_t *ctx_len, const int32_t *cu, float scale,
+                           void *out, int64_t o_ts, int64_t o_hs, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
+    const int cst = check_cache(cache);
+    if (cst != OM_OK) return cst;
+    const om_kv_cache &c = *cache;
+    if (groups < 0 || seqs < 0 || tokens < 0 || max_new < 0 || q_heads < 1 || q_heads % c.heads != 0) return OM_ERR_INVALID_ARG;
+    if (!float_type(dtype)) return OM_ERR_UNSUPPORTED;
+    if (seqs == 0 || tokens == 0) return OM_OK;
+    if (max_new < 1) return OM_ERR_INVALID_ARG;
+    int st = check_batch(seqs, tokens, block_table, width, c.page, ctx_len, cu);
+    if (st == OM_OK && groups > 0) st = check_batch(groups, tokens, prefix_table, prefix_width, c.page, prefix_len, group_offsets);
+    if (st != OM_OK) return st;
+    if (q_heads > 65535 || tokens * q_heads > kLim31 - kMargin) return OM_ERR_TOO_LARGE;
+    const int64_t group = q_heads / c.heads;
+    // pieces of 64 positions of every key head and eight query rows, at most
+    const __int128 units = static_cast<__int128>(width * c.page / 64 + 1) * c.heads * (tokens * group / 8 + seqs);
+    // and of the prefixes, for every 128 rows
+    const __int128 prefix_units = groups > 0 ? static_cast<__int128>(prefix_width * c.page / 64 + 1) * c.heads * (tokens * group / om::kSharedRows + groups) : 0;
+    if (units > kLim31 - (1 << 20) || prefix_units > kLim31 - (1 << 21)) return OM_ERR_TOO_LARGE;
+    const Heads hq{q, q_ts, q_hs}, ho{out, o_ts, o_hs};
+    st = check_heads(hq, tokens, q_heads, c.dim, dtype, false);
+    if (st == OM_OK) st = check_heads(ho, tokens, q_heads, c.dim, dtype, true);
+    if (st != OM_OK) return st;
+    if (!workspace) return OM_ERR_NULL_PTR;
+    if (!aligned(lse, 4) || !aligned(workspace, 16)) return OM_ERR_ALIGNMENT;
+    const SharedPlaces at = shared_places(workspace, group, q_heads, c.dim, max_new, tokens);
+    if (workspace_bytes < at.bytes) return OM_ERR_INVALID_ARG;
+    const CacheBlocks cb(c);
+    const BatchBlocks bb(seqs, block_table, width, ctx_len, cu), pb(groups, prefix_table, prefix_width, prefix_len, groups > 0 ? group_offsets : cu);
+    const Block rq = heads_block(hq, tokens, q_heads, c.dim, dtype);
+    const Block w[3] = {heads_block(ho, tokens, q_heads, c.dim, dtype), flat(lse, lse ? static_cast<__int128>(tokens) * q_heads * 4 : 0),
+                        flat(workspace, static_cast<__int128>(workspace_bytes))};
+    for (int i = 0; i < 3; ++i) {
+        if (cb.overlap(w[i]) || bb.overlap(w[i]) || (groups > 0 && pb.overlap(w[i])) || overlaps(w[i], rq)) return OM_ERR_ALIAS;
+        for (int j = 0; j < i; ++j)
+            if (overlaps(w[i], w[j])) return OM_ERR_ALIAS;
+    }
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int tile = om::shared_tile(c.dim, dtype == OM_F32 ? 2 : 1);
+    int64_t blocks = static_cast<int64_t>(om::num_sms()) * (c.dim == 256 ? 1 : 2);
+    if (blocks > om::kSharedMostBlocks) blocks = om::kSharedMostBlocks;
+    if (prefix_units < blocks) blocks = static_cast<int64_t>(prefix_units);
+    if (blocks < 1) blocks = 1;
+    const int64_t eb = type_bytes(dtype);
+    om::SharedProblem p{};
+    p.c = c;
+    p.seqs = seqs; p.tokens = tokens; p.q_heads = q_heads; p.groups = groups;
+    p.q = hq;
+    p.dtype = dtype;
+    p.group = static_cast<int>(group);
+    p.q_fours = aligned(q, 4 * eb) && q_ts % 4 == 0 && q_hs % 4 == 0;
+    p.prefix_table = prefix_table; p.prefix_width = prefix_width; p.prefix_len = prefix_len; p.group_at = group_offsets; p.cu = cu;
+    p.scale = scale;
+    p.tile_log = tile == 64 ? 6 : 7;
+    p.blocks = blocks;
+    p.slot_rows = at.slot_rows;
+    p.whole_state = at.whole_state; p.slot_state = at.slot_state; p.whole = at.whole; p.slots = at.slots;
+    p.own_state = at.own_state; p.own = at.own;
+    p.out = ho;
+    p.lse = lse;
+    p.status = static_cast<unsigned *>(workspace) + om::kWsStatusWord;
+    if (groups > 0) {
+        const cudaError_t e = c.dtype == OM_I8 ? om::launch_kv_shared_i8(p, s) : om::launch_kv_shared_e4m3(p, s);
+        if (e != cudaSuccess) return OM_ERR_CUDA;
+    }
+    const om::KvAttentionProblem own{c, seqs, tokens, max_new, q_heads, hq, {at.own, q_heads * c.dim, c.dim}, dtype, reinterpret_cast<float *>(at.own_state),
+                                     block_table, width, ctx_len, cu, scale, 0, workspace, 0};
+    const cudaError_t e = dtype == OM_F32 ? om::launch_kv_attention_part_f32(own, s)
+                          : dtype == OM_F16 ? om::launch_kv_attention_part_f16(own, s) : om::launch_kv_attention_part_bf16(own, s);
+    if (e != cudaSuccess) return OM_ERR_CUDA;
+    return from_cuda(om::launch_kv_shared_join(p, s));
 }
 
 }  // extern "C"

@@ -166,6 +166,10 @@ __device__ __forceinline__ uint32_t widen(uint32_t w) {  // bytes 0, 1 (or 2, 3)
     }
 }
 
+// What a kernel is compiled for: attention as it is, with first tokens that stay visible, or as a part of a larger
+// softmax (outputs in 32 bits, maximum and sum in place of the log of the sum, for shared prefixes).
+enum Form : int { kPlainForm, kSinksForm, kPartForm };
+
 struct Args {
     KvAttentionProblem p;
     bool out_fours, q_fours;  // outputs and queries are aligned for stores and loads of four
@@ -220,8 +224,9 @@ struct Part {
 };
 
 // Finished rows, [row][DIM + 4] floats in shared memory, to the outputs; every thread of the block.
-template <typename T, int DIM>
+template <typename TIN, int DIM, int FORM>
 __device__ __forceinline__ void write_rows(const Args &a, const Part &part, int group, const float *stage) {
+    using T = std::conditional_t<FORM == kPartForm, float, TIN>;
     constexpr int kQuads = DIM / 4;
 #pragma unroll 1
     for (int i = threadIdx.x; i < part.rows * kQuads; i += kThreads) {
@@ -237,8 +242,14 @@ __device__ __forceinline__ void write_rows(const Args &a, const Part &part, int 
     }
 }
 
+template <int FORM>
 __device__ __forceinline__ void write_lse(const KvAttentionProblem &p, const Part &part, int group, int col, float top, float sum) {
     const int r = part.row0 + col;
+    if constexpr (FORM == kPartForm) {
+        if (col < part.rows)
+            reinterpret_cast<float2 *>(p.lse)[(part.t0 + r / group) * p.q_heads + static_cast<int64_t>(part.h) * group + r % group] = make_float2(top, sum);
+        return;
+    }
     if (p.lse && col < part.rows)
         p.lse[(part.t0 + r / group) * p.q_heads + static_cast<int64_t>(part.h) * group + r % group] =
             sum == 0.0f ? -INFINITY : __fmul_rn(__fadd_rn(top - kBias, log2f(sum)), 0.6931471805599453f);
@@ -270,7 +281,7 @@ struct Config {
 // BLOCKS: of an SM, at least. Three where the registers allow it (heads of up to 128, 8 rows of 16 bits), two elsewhere. With two, 256
 // sequences of 500 tokens, 8 key heads, take 66 us instead of 57, 64 of up to 8000 tokens with heads of 64 101 instead of 89; one of
 // 131071 tokens, whose parts are more with three, the same (float16 59.5 and 59.9 us, bfloat16 59.4 and 57.9).
-template <typename T, int KV, int DIM, int NT, int BLOCKS, bool SINKS>
+template <typename T, int KV, int DIM, int NT, int BLOCKS, int FORM>
 __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __grid_constant__ Args a) {
     using S = Shape<DIM>;
     using C = Config<T, DIM, NT>;
@@ -279,6 +290,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
     constexpr bool kQShared = C::kQShared;
     constexpr int kFrag = S::kSteps * NT;  // float4 of O per lane
     const KvAttentionProblem &p = a.p;
+    constexpr bool SINKS = FORM == kSinksForm;
     const int sinks = SINKS ? p.sinks : 0;
     unsigned *const counters = static_cast<unsigned *>(p.workspace);
     float *const slots = reinterpret_cast<float *>(static_cast<uint8_t *>(p.workspace) + kKvCounterBytes);
@@ -668,11 +680,11 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
                             for (int st = 0; st < S::kSteps; ++st)
                                 *reinterpret_cast<float2 *>(dst + (DIM >= 128 ? st / 8 * 128 + st % 8 * 2 : st * 2)) =
                                     make_float2(o[st][nt][j], o[st][nt][j + 2]);
-                            if (g == 0) write_lse(p, last, group, col, m[nt][j], l[nt][j]);
+                            if (g == 0) write_lse<FORM>(p, last, group, col, m[nt][j], l[nt][j]);
                         }
                 }
                 __syncthreads();
-                write_rows<T, DIM>(a, last, group, join);
+                write_rows<T, DIM, FORM>(a, last, group, join);
             } else if (warp == 0) {
                 // a part of an item: kept for the block that joins them. A block has at most
                 // two, one that starts with its share (slot 2j) and one that ends with it (2j + 1).
@@ -1090,7 +1102,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
         mass = 0.0f;
 #pragma unroll
         for (int s = 0; s < kSets; ++s) mass = __fadd_rn(mass, part_sum[s * kRows + row]);
-        if (set == 0) write_lse(p, done, group, row, best, mass);
+        if (set == 0) write_lse<FORM>(p, done, group, row, best, mass);
         const float inv = inverse(mass);
         for (int j = set; j < n; j += kSets) weight[j * kRows + row] = __fmul_rn(weight[j * kRows + row], inv);
         __syncthreads();
@@ -1124,21 +1136,21 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
             *reinterpret_cast<float2 *>(dst + DIM + 4) = make_float2(acc.y, acc.w);
         }
         __syncthreads();
-        write_rows<T, DIM>(a, done, group, stage);
+        write_rows<T, DIM, FORM>(a, done, group, stage);
     }
 }
 
-template <typename T, int KV, int DIM, int NT, int BLOCKS, bool SINKS>
+template <typename T, int KV, int DIM, int NT, int BLOCKS, int FORM>
 cudaError_t launch(const Args &a, cudaStream_t s) {
     constexpr int kSmem = Config<T, DIM, NT>::kSmem;
     static PerDevice blocks;
     std::atomic<int> *const kept = blocks.here();
     int blocks_per_sm = kept ? kept->load(std::memory_order_relaxed) : 0;
     if (blocks_per_sm == 0) {
-        cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<T, KV, DIM, NT, BLOCKS, SINKS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        cudaError_t e = cudaFuncSetAttribute(kv_attention_kernel<T, KV, DIM, NT, BLOCKS, FORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         int n = 0;
-        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kv_attention_kernel<T, KV, DIM, NT, BLOCKS, SINKS>, kThreads, kSmem);
+        e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kv_attention_kernel<T, KV, DIM, NT, BLOCKS, FORM>, kThreads, kSmem);
         if (e != cudaSuccess) return e;
         blocks_per_sm = n < 1 ? 1 : n;
         if (kept) kept->store(blocks_per_sm, std::memory_order_relaxed);
@@ -1151,32 +1163,32 @@ cudaError_t launch(const Args &a, cudaStream_t s) {
     if (grid > Config<T, DIM, NT>::kMaxBlocks) grid = Config<T, DIM, NT>::kMaxBlocks;
     if (units < grid * kMinUnits) grid = static_cast<int64_t>((units + kMinUnits - 1) / kMinUnits);
     if (grid < 1) grid = 1;
-    return launch_behind(kv_attention_kernel<T, KV, DIM, NT, BLOCKS, SINKS>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmem, s, a);
+    return launch_behind(kv_attention_kernel<T, KV, DIM, NT, BLOCKS, FORM>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), kSmem, s, a);
 }
 
-template <typename T, bool SINKS, int KV, int DIM>
+template <typename T, int FORM, int KV, int DIM>
 cudaError_t by_rows(const Args &a, cudaStream_t s) {
     const int64_t rows = kv_block_rows(a.p.q_heads / a.p.c.heads, a.p.max_new);
-    if (rows == 8) return launch<T, KV, DIM, 1, DIM <= 128 && sizeof(T) == 2 ? 3 : 2, SINKS>(a, s);
-    return launch<T, KV, DIM, 2, 2, SINKS>(a, s);
+    if (rows == 8) return launch<T, KV, DIM, 1, DIM <= 128 && sizeof(T) == 2 ? 3 : 2, FORM>(a, s);
+    return launch<T, KV, DIM, 2, 2, FORM>(a, s);
 }
 
-template <typename T, bool SINKS, int KV>
+template <typename T, int FORM, int KV>
 cudaError_t by_dim(const Args &a, cudaStream_t s) {
-    if (a.p.c.dim == 64) return by_rows<T, SINKS, KV, 64>(a, s);
-    if (a.p.c.dim == 128) return by_rows<T, SINKS, KV, 128>(a, s);
-    return by_rows<T, SINKS, KV, 256>(a, s);
+    if (a.p.c.dim == 64) return by_rows<T, FORM, KV, 64>(a, s);
+    if (a.p.c.dim == 128) return by_rows<T, FORM, KV, 128>(a, s);
+    return by_rows<T, FORM, KV, 256>(a, s);
 }
 
-template <typename T, bool SINKS>
+template <typename T, int FORM>
 cudaError_t by_codes(const Args &a, cudaStream_t s) {
-    return a.p.c.dtype == OM_I8 ? by_dim<T, SINKS, OM_I8>(a, s) : by_dim<T, SINKS, OM_E4M3>(a, s);
+    return a.p.c.dtype == OM_I8 ? by_dim<T, FORM, OM_I8>(a, s) : by_dim<T, FORM, OM_E4M3>(a, s);
 }
 
-template <typename T, bool SINKS>
+template <typename T, int FORM>
 cudaError_t run_kv_attention(const KvAttentionProblem &p, cudaStream_t s) {
-    auto fours = [](const Heads &x) { return reinterpret_cast<uintptr_t>(x.p) % (4 * sizeof(T)) == 0 && x.ts % 4 == 0 && x.hs % 4 == 0; };
-    return by_codes<T, SINKS>(Args{p, fours(p.out), fours(p.q)}, s);
+    auto fours = [](const Heads &x, size_t bytes) { return reinterpret_cast<uintptr_t>(x.p) % (4 * bytes) == 0 && x.ts % 4 == 0 && x.hs % 4 == 0; };
+    return by_codes<T, FORM>(Args{p, fours(p.out, FORM == kPartForm ? 4 : sizeof(T)), fours(p.q, sizeof(T))}, s);
 }
 
 }  // namespace

@@ -2,5 +2,5 @@
 #include "kv_attention.cuh"
 
 namespace om {
-cudaError_t launch_kv_attention_f32(const KvAttentionProblem &p, cudaStream_t s) { return run_kv_attention<float, false>(p, s); }
+cudaError_t launch_kv_attention_f32(const KvAttentionProblem &p, cudaStream_t s) { return run_kv_attention<float, kPlainForm>(p, s); }
 }  // namespace om

@@ -1,0 +1,6 @@
+// kv_attention_part_bf16.cu -- attention over the paged 8-bit cache, bfloat16 queries, as a part of a larger softmax.
+#include "kv_attention.cuh"
+
+namespace om {
+cudaError_t launch_kv_attention_part_bf16(const KvAttentionProblem &p, cudaStream_t s) { return run_kv_attention<__nv_bfloat16, kPartForm>(p, s); }
+}  // namespace om

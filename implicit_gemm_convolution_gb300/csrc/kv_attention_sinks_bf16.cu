@@ -2,5 +2,5 @@
 #include "kv_attention.cuh"
 
 namespace om {
-cudaError_t launch_kv_attention_sinks_bf16(const KvAttentionProblem &p, cudaStream_t s) { return run_kv_attention<__nv_bfloat16, true>(p, s); }
+cudaError_t launch_kv_attention_sinks_bf16(const KvAttentionProblem &p, cudaStream_t s) { return run_kv_attention<__nv_bfloat16, kSinksForm>(p, s); }
 }  // namespace om

@@ -2,5 +2,5 @@
 #include "kv_attention.cuh"
 
 namespace om {
-cudaError_t launch_kv_attention_sinks_f16(const KvAttentionProblem &p, cudaStream_t s) { return run_kv_attention<__half, true>(p, s); }
+cudaError_t launch_kv_attention_sinks_f16(const KvAttentionProblem &p, cudaStream_t s) { return run_kv_attention<__half, kSinksForm>(p, s); }
 }  // namespace om

@@ -1,0 +1,132 @@
+// kv_shared_items.cuh -- how the work on shared prefixes is cut: the same arithmetic for the blocks that attend
+// (kv_shared.cuh) and the ones that join their parts (kv_shared_join.cu). Whole warps.
+#pragma once
+
+#include <climits>
+
+#include "decode_device.cuh"
+
+namespace om {
+
+// A group of sequences: its tokens and its prefix. Rows are its tokens times the query heads of a key head. Whatever the offsets
+// hold, tokens lie in the batch and positions in the table.
+struct SharedGroup {
+    int t0, rows, row_blocks, len;
+    int units;  // tiles of the prefix
+    int64_t n;  // units of all its items, [key head][row block][unit]
+};
+__device__ __forceinline__ SharedGroup shared_group(const SharedProblem &p, int64_t j) {
+    SharedGroup g{};
+    if (j >= p.groups) return g;
+    const int64_t a = min(max(static_cast<int64_t>(p.group_at[j]), static_cast<int64_t>(0)), p.seqs);
+    const int64_t b = min(max(static_cast<int64_t>(p.group_at[j + 1]), a), p.seqs);
+    const int64_t lo = min(max(static_cast<int64_t>(p.cu[a]), static_cast<int64_t>(0)), p.tokens);
+    const int64_t hi = min(max(static_cast<int64_t>(p.cu[b]), lo), p.tokens);
+    g.t0 = static_cast<int>(lo);
+    g.rows = static_cast<int>((hi - lo) * p.group);
+    g.row_blocks = (g.rows + kSharedRows - 1) / kSharedRows;
+    g.len = static_cast<int>(min(max(static_cast<int64_t>(p.prefix_len[j]), static_cast<int64_t>(0)), p.prefix_width * p.c.page));
+    g.units = (g.len + (1 << p.tile_log) - 1) >> p.tile_log;
+    g.n = p.c.heads * g.row_blocks * static_cast<int64_t>(g.units);
+    return g;
+}
+
+// Units of all groups, 0 where they pass 32 bits (offsets that decrease count tokens twice; others the host has bounded). find: the
+// group with token `t` and the units before it, -1 for none.
+__device__ __forceinline__ int shared_units(const SharedProblem &p) {
+    int64_t total = 0;
+#pragma unroll 1
+    for (int64_t j = threadIdx.x & 31; j < p.groups; j += 32) total += shared_group(p, j).n;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    return total > INT_MAX - (1 << 20) ? 0 : static_cast<int>(total);
+}
+__device__ __forceinline__ int shared_per_block(const SharedProblem &p, int total) {
+    return max((total + static_cast<int>(p.blocks) - 1) / static_cast<int>(p.blocks), kSharedMinUnits);
+}
+
+// A block's part of an item: rows row0 .. row0 + rows - 1 of a group and key head, units from .. to - 1 of all `units`.
+struct SharedItem {
+    int group, h, t0, row0, rows, len;
+    int units, from, to;
+    bool at_start;  // of the block's share
+    bool more;      // false: there was none
+};
+
+// The parts of a block's share one after the other. Kept in shared memory, one for each warp that walks: registers are short where
+// it is used.
+struct SharedItems {
+    SharedItem item;
+    SharedGroup g;
+    int u, begin, stop, before, j;
+
+    __device__ __forceinline__ void start(const SharedProblem &p, int block) {
+        const int total = shared_units(p), per = shared_per_block(p, total), lane = threadIdx.x & 31;
+        const int from = static_cast<int>(min(static_cast<int64_t>(block) * per, static_cast<int64_t>(total)));
+        int units = 0, at = 0;
+        if (from < total) {
+#pragma unroll 1
+            for (int64_t base = 0; base < p.groups; base += 32) {
+                const int n = static_cast<int>(shared_group(p, base + lane).n);
+                int up = n;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int x = __shfl_up_sync(0xffffffffu, up, o);
+                    if (lane >= o) up += x;
+                }
+                const unsigned here = __ballot_sync(0xffffffffu, from < units + up);
+                if (here != 0) {
+                    at = __ffs(here) - 1;
+                    units += __shfl_sync(0xffffffffu, up - n, at);
+                    at += static_cast<int>(base);
+                    break;
+                }
+                units += __shfl_sync(0xffffffffu, up, 31);
+            }
+        }
+        if (lane == 0) {
+            g = from < total ? shared_group(p, at) : SharedGroup{};
+            begin = u = from;
+            stop = min(total - from, per) + from;
+            before = units;
+            j = at;
+        }
+        __syncwarp();
+    }
+    // The next part, in item; false behind the last.
+    __device__ __forceinline__ bool next(const SharedProblem &p) {
+        __syncwarp();  // every lane is done with the last one
+        if ((threadIdx.x & 31) == 0 && u < stop) {
+            while (u >= before + static_cast<int>(g.n) && j < p.groups) {
+                before += static_cast<int>(g.n);
+                g = shared_group(p, ++j);
+            }
+            const int units = max(g.units, 1), i = (u - before) / units, first = before + i * units;
+            item.group = j;
+            item.h = i / max(g.row_blocks, 1);
+            item.t0 = g.t0;
+            item.row0 = (i - item.h * g.row_blocks) * kSharedRows;
+            item.rows = min(g.rows - item.row0, kSharedRows);
+            item.len = g.len;
+            item.units = units;
+            item.from = u - first;
+            item.to = min(units, stop - first);
+            item.at_start = u == begin;
+            u = first + item.to;
+            item.more = true;
+        } else if ((threadIdx.x & 31) == 0) {
+            item.more = false;
+        }
+        __syncwarp();
+        return item.more;
+    }
+};
+
+// 1 / x to a unit in the last place, and 0 for a sum of nothing.
+__device__ __forceinline__ float shared_inverse(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return x == 0.0f ? 0.0f : y;
+}
+
+}  // namespace om

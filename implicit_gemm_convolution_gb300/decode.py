@@ -58,6 +58,10 @@ def _declare(L: ctypes.CDLL) -> None:
     L.om_kv_attention.argtypes = batch + rest
     L.om_kv_attention_sinks.restype = ci
     L.om_kv_attention_sinks.argtypes = batch + [i64] + rest
+    L.om_kv_shared_workspace_bytes.restype = ctypes.c_size_t
+    L.om_kv_shared_workspace_bytes.argtypes = [i64] * 5
+    L.om_kv_shared_attention.restype = ci
+    L.om_kv_shared_attention.argtypes = [vp, i64, vp, i64, vp, vp] + [i64] * 4 + [vp, i64, i64, ci, vp, i64, vp, vp, f32] + rest
 
 
 _functions = None
@@ -279,18 +283,18 @@ class PagedKVCache:
         return cls(k, v, ks, vs)
 
 
-def _batch(block_table, lens, cu, lens_name, device):
+def _batch(block_table, lens, cu, lens_name, device, table_name="block_table", cu_name="cu"):
     """Pointers and sizes of a batch's lookups: (block_table, width, lens, cu), sequences."""
     if not (block_table.get_device() == lens.get_device() == cu.get_device() == device and block_table.dtype is lens.dtype is cu.dtype is _int32
             and block_table.dim() == 2 and lens.dim() == 1 and cu.dim() == 1 and block_table.is_contiguous() and lens.is_contiguous()
             and cu.is_contiguous()):
-        _cuda(block_table, "block_table", 2, _I32, device)
+        _cuda(block_table, table_name, 2, _I32, device)
         _cuda(lens, lens_name, 1, _I32, device)
-        _cuda(cu, "cu", 1, _I32, device)
-        raise ValueError("block_table must be contiguous")
+        _cuda(cu, cu_name, 1, _I32, device)
+        raise ValueError(f"{table_name} must be contiguous")
     seqs, width = block_table.shape
     if lens.numel() != seqs or cu.numel() != seqs + 1:
-        raise ValueError(f"block_table, {lens_name} and cu are of different batches")
+        raise ValueError(f"{table_name}, {lens_name} and {cu_name} are of different batches")
     return (block_table.data_ptr(), width, lens.data_ptr(), cu.data_ptr()), seqs
 
 
@@ -451,4 +455,56 @@ def kv_attention(cache, q, block_table, ctx_len, cu, max_new: int, scale=None, w
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _call("om_kv_attention_sinks", device, stream, cache._ref, seqs, tokens, max_new, q_heads, q.data_ptr(), ts, hs, DTYPES[dtype], *batch,
           dim ** -0.5 if scale is None else scale, window, sinks, *oa, lp, ws, ws_bytes)
+    return out
+
+
+def new_shared_workspace(cache, q_heads: int, max_new: int, tokens: int):
+    """A device tensor usable as the workspace of kv_shared_attention for calls of these heads
+    with at most `tokens` tokens and max_new queries a sequence; one per stream."""
+    n = lib().om_kv_shared_workspace_bytes(cache.heads, q_heads, cache.dim, max_new, tokens)
+    if n == 0:
+        raise ValueError("q_heads must be a multiple of the cache's heads, max_new and tokens positive")
+    return torch.zeros((n + 3) // 4, dtype=torch.int32, device=cache.k.device)
+
+
+def kv_shared_attention(cache, q, prefix_table, prefix_len, groups, block_table, ctx_len, cu, max_new: int, scale=None, out=None, lse=None,
+                        workspace=None, stream=None):
+    """kv_attention of a batch whose sequences share prefixes, each of which is read once for all of them.
+
+    groups (int32 [prefixes + 1], not decreasing): sequences groups[j] .. groups[j + 1] - 1 begin with the prefix_len[j] tokens
+    (int32 [prefixes]) in the pages prefix_table[j] (int32 [prefixes, width]); block_table, ctx_len and cu are
+    the sequences' own tokens behind it, which start on a page of their own. A query sees its whole
+    prefix and its sequence's own tokens up to itself. workspace: from new_shared_workspace (None: a new one). scale, lse,
+    and what is returned, as in kv_attention.
+    """
+    device = cache.device
+    _cuda(q, "q", 3, DTYPES, device)
+    dtype, shape = q.dtype, q.shape
+    tokens, q_heads, dim = shape
+    if dim != cache.dim:
+        raise ValueError("q and the cache have different head dimensions")
+    ts, hs, _ = q.stride()
+    batch, seqs = _batch(block_table, ctx_len, cu, "ctx_len", device)
+    (pp, pwidth, lens, offsets), count = _batch(prefix_table, prefix_len, groups, "prefix_len", device, "prefix_table", "groups")
+    if out is None:
+        out = _empty(shape, dtype, q.device, stream)
+        oa = out.data_ptr(), q_heads * dim, dim
+    else:
+        oa = _heads(out, "out", shape, dtype, device)
+    lp = None
+    if lse is not None:
+        _cuda(lse, "lse", 2, (torch.float32,), device)
+        if lse.shape != (tokens, q_heads) or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous (tokens, q heads) tensor")
+        lp = lse.data_ptr()
+    if tokens == 0 or seqs == 0:
+        return out
+    if workspace is None:
+        n = _lib().om_kv_shared_workspace_bytes(cache.heads, q_heads, dim, max_new, tokens)
+        with torch.cuda.stream(stream):
+            workspace = torch.zeros((n + 3) // 4, dtype=torch.int32, device=q.device)
+    elif workspace.get_device() != device or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the cache's device")
+    _call("om_kv_shared_attention", device, stream, cache._ref, count, pp, pwidth, lens, offsets, seqs, tokens, max_new, q_heads, q.data_ptr(), ts, hs,
+          DTYPES[dtype], *batch, dim ** -0.5 if scale is None else scale, *oa, lp, workspace.data_ptr(), workspace.numel() * workspace.element_size())
     return out

@@ -558,6 +558,36 @@ OM_API int om_kv_attention_sinks(const om_kv_cache *cache, int64_t seqs, int64_t
                                  void *workspace, size_t workspace_bytes, void *stream);
 
 /*
+ * Bytes of the scratch of om_kv_shared_attention for calls of these heads with at most `tokens` tokens and max_new queries a
+ * sequence (0 for invalid arguments).
+ */
+OM_API size_t om_kv_shared_workspace_bytes(int64_t kv_heads, int64_t q_heads, int64_t dim, int64_t max_new, int64_t tokens);
+
+/*
+ * Attention of a batch whose sequences share long prefixes, each read and multiplied once for all of them.
+ * `groups` prefixes: group j's is prefix_len[j] tokens in the pages prefix_table[j] (rows of prefix_width), and the sequences
+ * group_offsets[j] .. group_offsets[j + 1] - 1 (int32 [groups + 1], not decreasing) all begin with it; other sequences have none. What
+ * follows is each sequence's own: block_table, width, ctx_len and cu as in om_kv_attention, counted from the end of the prefix (a sequence's
+ * own tokens start a page of their own; its positions go on from the prefix only in the rotation of its queries and keys, which is
+ * the caller's). The query at a sequence's own position p sees its whole prefix and its own positions 0 .. p:
+ *   out[t][h] = sum_i softmax_i(scale * q[t][h] . key_i) value_i over both;  lse as in om_kv_attention.
+ * Rows that see nothing, scores that are NaN, table entries outside the cache, tokens that no sequence owns, the precision of queries and
+ * weights: as there. Products over the prefix run on the tensor cores (sums of 32 bits).
+ * workspace: device memory, 16-byte aligned, of om_kv_shared_workspace_bytes for this call's heads, max_new and tokens or more, zeroed once before its
+ * first use; calls that may run at the same time need distinct ones. A bounded device wait that runs out is recorded in its
+ * status word (om_workspace_status), and the outputs are then incomplete. Results do not depend on timing.
+ */
+OM_API int om_kv_shared_attention(const om_kv_cache *cache, int64_t groups,
+                                  const int32_t *prefix_table, int64_t prefix_width, const int32_t *prefix_len,
+                                  const int32_t *group_offsets,
+                                  int64_t seqs, int64_t tokens, int64_t max_new, int64_t q_heads,
+                                  const void *q, int64_t q_ts, int64_t q_hs, int dtype,
+                                  const int32_t *block_table, int64_t width,
+                                  const int32_t *ctx_len, const int32_t *cu, float scale,
+                                  void *out, int64_t o_ts, int64_t o_hs, float *lse,
+                                  void *workspace, size_t workspace_bytes, void *stream);
+
+/*
  * Synchronises stream, then reads and clears the library's device-wide status
  * words for the current device. Every device-side wait in the library's
  * kernels (mbarrier waits of the TMA and tensor-core pipelines) is bounded;
