@@ -15,7 +15,7 @@
 //              second product's operand; rows of sums are multiplied only when a unit or maximum changes; queries in, sums out.
 //   warps 4-7  codes from the pages (values on their way beside a tile's scores, the next keys beside its weights) to 16-bit floats in shared memory, rows of 128 bytes with
 //              the tensor cores' exclusive-or; keys and values have the same layout (as k-major and n-major operands).
-//   warp 8     tensor memory, and one thread that issues the products.
+//   warp 8     tensor memory, and one thread that issues the products;  warp 9  finds the block's parts of items.
 // Every mbarrier wait is bounded; on a timeout the block records the error, stops and frees its tensor memory.
 //
 // Split. The tiles of all items (group, key head, 128 rows) in equal shares of the blocks that fit at once, as lengths on the
@@ -37,7 +37,7 @@ namespace {
 
 constexpr int kRowWarps = 4, kCopyWarps = 4;
 constexpr int kThreads = 384;  // three warpgroups: registers are handed out by them
-constexpr int kProductWarp = kRowWarps + kCopyWarps;
+constexpr int kProductWarp = kRowWarps + kCopyWarps, kWalkWarp = kProductWarp + 1;
 constexpr float kLog2e = 1.4426950408889634f;
 // as in kv_attention.cuh
 constexpr float kBias = 8.0f, kMost = 32768.0f, kLeast = 0.5f, kMostExp = 1099511627776.0f;
@@ -94,32 +94,33 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// 32 (16) columns of a warp's lanes; a load has arrived when it returns.
-__device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,"
-        "%28,%29,%30,%31}, [%32];\n\ttcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]),
-          "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]),
-          "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-        : "r"(at)
-        : "memory");
-}
+// 16 columns of a warp's lanes. What a load brings is there after tmem_loaded, through which the compiler sees it pass.
 __device__ __forceinline__ void tmem_load(uint32_t at, uint32_t (&r)[16]) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
                    "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
                  : "r"(at)
                  : "memory");
 }
-__device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%32], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,"
-        "%27,%28,%29,%30,%31};" ::"r"(r[0]),
-        "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]),
-        "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]),
-        "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]), "r"(at)
-        : "memory");
+__device__ __forceinline__ void tmem_loaded(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]),
+                   "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+// work(g, columns) for each group of 16 columns from `at` on, the next group on its way meanwhile.
+template <int GROUPS, typename F>
+__device__ __forceinline__ void for_groups(uint32_t at, F work) {
+    uint32_t a[16], b[16];
+    tmem_load(at, a);
+#pragma unroll 1
+    for (int g = 0; g < GROUPS; g += 2) {
+        tmem_loaded(a);
+        tmem_load(at + g * 16 + 16, b);
+        work(g, a);
+        tmem_loaded(b);
+        if (g + 2 < GROUPS) tmem_load(at + g * 16 + 32, a);
+        work(g + 1, b);
+    }
 }
 __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[16]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15};" ::"r"(r[0]), "r"(r[1]), "r"(r[2]),
@@ -139,6 +140,19 @@ __device__ __forceinline__ float2 unpack_half(uint32_t x) {
     __half2 h;
     memcpy(&h, &x, 4);
     return __half22float2(h);
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+__device__ __forceinline__ float2 mul2_rn(float2 a, float2 b) {
+    unsigned long long r;
+    asm("{\n\t.reg .b64 ra, rb;\n\tmov.b64 ra, {%1, %2};\n\tmov.b64 rb, {%3, %4};\n\tmul.rn.f32x2 %0, ra, rb;\n\t}" : "=l"(r) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    float2 o;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
+    return o;
 }
 
 // A word's four codes as 16-bit floats, exactly. A whole number c becomes 1024 + (c + 128) by placing its byte (sign bit
@@ -162,15 +176,27 @@ __device__ __forceinline__ uint2 widen(uint32_t w) {
 
 struct Bars {
     uint64_t q_full, k_full, v_full, scored, weighed, summed, drained;
+    uint64_t item_full[2], item_free[2];
+    SharedItem item[2];  // rows 0: there are no more
     uint32_t tmem;
     int abort;
 };
 __device__ __forceinline__ bool aborted(Bars *b) { return *reinterpret_cast<volatile int *>(&b->abort) != 0; }
-// Bounded wait that also gives up once another role has failed.
+// Bounded wait that also gives up once another role has failed. The barrier holds a waiting thread for up to the hint: polling takes
+// issue slots from the warps that work.
+constexpr uint32_t kHoldNs = 20000;
+__device__ __forceinline__ bool held_wait(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(smem_u32(bar)), "r"(parity), "r"(kHoldNs)
+                 : "memory");
+    return ok != 0;
+}
 __device__ __forceinline__ bool wait(Bars *b, uint64_t *bar, uint32_t parity, unsigned *status) {
-    if (mbar_try_wait(bar, parity)) return true;
+    if (held_wait(bar, parity)) return true;
     const unsigned long long t0 = global_ns();
-    while (!mbar_try_wait(bar, parity)) {
+    while (!held_wait(bar, parity)) {
         if (aborted(b)) return false;
         if (global_ns() - t0 > kWaitLimitNs) {
             atomicOr(status, kDevErrTimeout);
@@ -180,22 +206,53 @@ __device__ __forceinline__ bool wait(Bars *b, uint64_t *bar, uint32_t parity, un
     }
     return true;
 }
-
 // The same for all lanes of a warp.
 __device__ __forceinline__ bool wait_warp(Bars *b, uint64_t *bar, uint32_t parity, unsigned *status) {
     return __all_sync(0xffffffffu, wait(b, bar, parity, status));
 }
 
-// Four elements of a row of queries.
-template <int PARTS>
-__device__ __forceinline__ void load_query(const SharedProblem &p, int64_t at, float *v) {
-    if constexpr (PARTS == 2)
-        p.q_fours ? load4<float, true>(static_cast<const float *>(p.q.p) + at, v) : load4<float, false>(static_cast<const float *>(p.q.p) + at, v);
-    else if (p.dtype == OM_F16)
-        p.q_fours ? load4<__half, true>(static_cast<const __half *>(p.q.p) + at, v) : load4<__half, false>(static_cast<const __half *>(p.q.p) + at, v);
-    else
-        p.q_fours ? load4<__nv_bfloat16, true>(static_cast<const __nv_bfloat16 *>(p.q.p) + at, v)
-                  : load4<__nv_bfloat16, false>(static_cast<const __nv_bfloat16 *>(p.q.p) + at, v);
+// The page of a position, -1 behind the end. Nothing here looks at what was loaded, which would wait for it.
+__device__ __forceinline__ int load_page(const int32_t *table, int pos, int len, int page_log) {
+    int id;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\tmov.s32 %0, -1;\n\t@p ld.global.s32 %0, [%1];\n\t}"
+                 : "=&r"(id)
+                 : "l"(table + (pos >> page_log)), "r"(static_cast<uint32_t>(pos < len)));
+    return id;
+}
+// 16 codes, zeros where there are none.
+__device__ __forceinline__ uint4 load_codes(const uint8_t *at, bool there) {
+    uint4 x;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.u32 %0, 0;\n\tmov.u32 %1, 0;\n\tmov.u32 %2, 0;\n\tmov.u32 %3, 0;\n\t"
+                 "@p ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                 : "=&r"(x.x), "=&r"(x.y), "=&r"(x.z), "=&r"(x.w)
+                 : "l"(at), "r"(static_cast<uint32_t>(there)));
+    return x;
+}
+
+// A row's queries in a lane, two 16-bit elements or one of 32 bits a word; zeros where there is no row.
+template <int WORDS>
+__device__ __forceinline__ void load_query(const SharedProblem &p, int64_t at, bool live, uint32_t (&w)[WORDS]) {
+    constexpr int kEach = 4;  // bytes of a word
+    const int bytes = p.dtype == OM_F32 ? 4 : 2;
+    const uint8_t *const from = static_cast<const uint8_t *>(p.q.p) + at * bytes;
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i) w[i] = 0;
+    if (!live) return;
+    if (p.q_fours) {
+        // eight bytes at least are aligned
+#pragma unroll
+        for (int i = 0; i < WORDS; i += 2) {
+            const uint2 x = *reinterpret_cast<const uint2 *>(from + i * kEach);
+            w[i] = x.x;
+            w[i + 1] = x.y;
+        }
+    } else if (bytes == 4) {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = reinterpret_cast<const uint32_t *>(from)[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) w[i] = reinterpret_cast<const uint16_t *>(from)[2 * i] | static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(from)[2 * i + 1]) << 16;
+    }
 }
 
 template <int KV, int DIM, int PARTS>
@@ -208,6 +265,8 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
     uint8_t *const smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
     const uint32_t q_at = smem_u32(smem), k_at = q_at + C::kQBytes, v_at = k_at + C::kTile;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+    __shared__ float4 groups_[kRowWarps][kGroups];  // a row warp's own
+    float4 *const groups = groups_[warp % kRowWarps];
     unsigned *const status = p.status;
     if (threadIdx.x == 0) {
         mbar_init(&bars->q_full, kRowWarps);
@@ -217,6 +276,10 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
         mbar_init(&bars->weighed, kRowWarps);
         mbar_init(&bars->summed, 1);
         mbar_init(&bars->drained, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->item_full[i], 1);
+            mbar_init(&bars->item_free[i], kProductWarp + 1);
+        }
         bars->abort = 0;
         fence_mbar_init();
         fence_proxy_async_smem();
@@ -231,141 +294,164 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
     const uint32_t tmem = bars->tmem, sums = tmem + kPos;
     wait_for_earlier();
 
-    __shared__ SharedItems walks[kProductWarp + 1];
-    SharedItems &items = walks[min(warp, kProductWarp)];
-    if (warp <= kProductWarp) items.start(p, blockIdx.x);
     const int page = static_cast<int>(p.c.page), page_log = 31 - __clz(page), heads = static_cast<int>(p.c.heads);
+    const unsigned pages = static_cast<unsigned>(p.c.pages);
+    auto there = [&](int id) { return static_cast<unsigned>(id) < pages; };
     int n = 0;  // tiles of this block so far, the phase of its barriers
+    int items = 0;
     bool ok = true;
+    // the block's next part of an item (rows 0: none), and the end of a warp's work on it
+    auto take = [&]() -> const SharedItem & {
+        ok = wait_warp(bars, &bars->item_full[items & 1], items / 2 & 1, status);
+        return bars->item[items & 1];
+    };
+    auto done = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->item_free[items & 1]);
+        ++items;
+    };
 
     // two blocks of 384 threads have 80 registers a thread: 240 for the three warpgroups
     if (warp < kRowWarps) {
         // ------------------------------------------------------------ rows
-        if constexpr (DIM != 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 128;");
+        if constexpr (DIM != 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
         const int row = warp * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
 #pragma unroll 1
-        for (; ok && items.next(p);) {
-            const SharedItem &it = items.item;
-            // queries: 16 lanes a row, two rows at a time, scaled by a power of two
-            constexpr int kEach = DIM / 16;
+        for (;;) {
+            const SharedItem &it = take();
+            if (!ok || it.rows == 0) break;
+            // queries: 16 lanes a row, two rows at a time, scaled by a power of two; eight rows' loads are on their way together
+            constexpr int kEach = DIM / 16, kWords = PARTS == 2 ? kEach : kEach / 2;
             float factor = 0.0f;
             const int half = lane / 16, q_d = lane % 16 * kEach;
-#pragma unroll 2
-            for (int i = 0; i < 16; ++i) {
-                const int r = warp * 32 + 2 * i + half, R = it.row0 + r;
-                float v[kEach];
-                if (r < it.rows) {
+#pragma unroll 1
+            for (int i0 = 0; i0 < 16; i0 += 4) {
+                uint32_t w[4][kWords];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int r = warp * 32 + 2 * (i0 + j) + half, R = it.row0 + r;
                     const int64_t at = (it.t0 + R / p.group) * p.q.ts + (static_cast<int64_t>(it.h) * p.group + R % p.group) * p.q.hs + q_d;
-#pragma unroll
-                    for (int e = 0; e < kEach; e += 4) load_query<PARTS>(p, at + e, v + e);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < kEach; ++e) v[e] = 0.0f;
+                    load_query<kWords>(p, at, r < it.rows, w[j]);
                 }
-                unsigned top = 0;
 #pragma unroll
-                for (int e = 0; e < kEach; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+                for (int j = 0; j < 4; ++j) {
+                    const int i = i0 + j, r = warp * 32 + 2 * i + half;
+                    float v[kEach];
 #pragma unroll
-                for (int x = 1; x < 16; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
-                // the row's largest element to [2^13, 2^14)
-                int e2 = static_cast<int>(top >> 23) - 127;
-                e2 = e2 < -100 ? -100 : e2;
-                const float up = power_of_two(13 - e2);
-                const float f = __shfl_sync(0xffffffffu, __fmul_rn(power_of_two(e2 - 13), __fmul_rn(p.scale, kLog2e)), (lane & 1) * 16);
-                if (lane / 2 == i) factor = f;
-#pragma unroll
-                for (int e = 0; e < kEach; ++e) v[e] = __fmul_rn(v[e], up);
-#pragma unroll
-                for (int part = 0; part < PARTS; ++part)
-#pragma unroll
-                    for (int e = 0; e < kEach; e += 4) {
-                        const int d = q_d + e;
-                        const uint2 w = make_uint2(pack_half(v[e], v[e + 1]), pack_half(v[e + 2], v[e + 3]));
-                        uint8_t *const to = smem + part * C::kQPart + d / 64 * (kSharedRows * 128) + r * 128 + ((d % 64 / 8 ^ (r & 7)) * 16) + d % 8 * 2;
-                        *reinterpret_cast<uint2 *>(to) = w;
-                        if (part + 1 < PARTS) {
-                            const float2 y = unpack_half(w.x), z = unpack_half(w.y);
-                            v[e] -= y.x;
-                            v[e + 1] -= y.y;
-                            v[e + 2] -= z.x;
-                            v[e + 3] -= z.y;
+                    for (int e = 0; e < kWords; ++e) {
+                        if constexpr (PARTS == 2) {
+                            v[e] = __uint_as_float(w[j][e]);
+                        } else {
+                            const float2 f = p.dtype == OM_F16 ? unpack_half(w[j][e]) : make_float2(__uint_as_float(w[j][e] << 16), __uint_as_float(w[j][e] & 0xffff0000u));
+                            v[2 * e] = f.x;
+                            v[2 * e + 1] = f.y;
                         }
                     }
+                    unsigned top = 0;
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+#pragma unroll
+                    for (int x = 1; x < 16; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
+                    // the row's largest element to [2^13, 2^14)
+                    int e2 = static_cast<int>(top >> 23) - 127;
+                    e2 = e2 < -100 ? -100 : e2;
+                    const float up = power_of_two(13 - e2);
+                    const float f = __shfl_sync(0xffffffffu, __fmul_rn(power_of_two(e2 - 13), __fmul_rn(p.scale, kLog2e)), (lane & 1) * 16);
+                    if (lane / 2 == i) factor = f;
+#pragma unroll
+                    for (int e = 0; e < kEach; ++e) v[e] = __fmul_rn(v[e], up);
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+                        for (int e = 0; e < kEach; e += 4) {
+                            const int d = q_d + e;
+                            const uint2 x = make_uint2(pack_half(v[e], v[e + 1]), pack_half(v[e + 2], v[e + 3]));
+                            uint8_t *const to = smem + part * C::kQPart + d / 64 * (kSharedRows * 128) + r * 128 + ((d % 64 / 8 ^ (r & 7)) * 16) + d % 8 * 2;
+                            *reinterpret_cast<uint2 *>(to) = x;
+                            if (part + 1 < PARTS) {
+                                const float2 y = unpack_half(x.x), z = unpack_half(x.y);
+                                v[e] -= y.x;
+                                v[e + 1] -= y.y;
+                                v[e + 2] -= z.x;
+                                v[e + 3] -= z.y;
+                            }
+                        }
+                }
             }
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->q_full);
 
             float m = kNone, l = 0.0f, per_unit = 1.0f;
-            // pages of the tile's groups of 16 positions: lane g has group g's, a tile ahead
-            auto page_of = [&](int pos0) -> int {
-                const int pos = pos0 + lane * 16;
-                const int id = lane < kGroups && pos < it.len ? p.prefix_table[it.group * p.prefix_width + (pos >> page_log)] : -1;
-                return id < p.c.pages ? id : -1;
-            };
+            // pages of the tile's groups of 16 positions: lane g has group g's, a tile ahead (and looks at it only when it is needed)
+            const int len = it.len, to = it.to;
+            const int32_t *const table = p.prefix_table + it.group * p.prefix_width;
+            auto page_of = [&](int pos0) { return load_page(table, pos0 + lane * 16, lane < kGroups ? len : 0, page_log); };
             auto scales_of = [&](int id, float *ka, float *va) {
                 const int64_t at = static_cast<int64_t>(id) * heads + it.h;
-                *ka = id < 0 ? 0.0f : p.c.k_scale[at];
-                *va = id < 0 ? 0.0f : p.c.v_scale[at];
+                *ka = there(id) ? p.c.k_scale[at] : 0.0f;
+                *va = there(id) ? p.c.v_scale[at] : 0.0f;
             };
             int id = page_of(it.from * kPos), id_next = page_of((it.from + 1) * kPos);
-            float ka, va, ka_next, va_next;
+            float ka, va;
             scales_of(id, &ka, &va);
 #pragma unroll 1
-            for (int u = it.from; ok && u < it.to; ++u, ++n) {
-                scales_of(id_next, &ka_next, &va_next);
-                const int id_after = page_of((u + 2) * kPos), pos0 = u * kPos;
-                // positions that are visible in this lane's group
-                const int mine = id < 0 ? 0 : min(max(it.len - (pos0 + lane * 16), 0), 16);
-                const bool all = __all_sync(0xffffffffu, lane >= kGroups || mine == 16);
+            for (int u = it.from; ok && u < to; ++u, ++n) {
+                const int pos0 = u * kPos;
+                // what every lane needs of the groups: scales (an infinite one counts as NaN), the log of the values', visible positions
+                const int mine = there(id) ? min(max(len - (pos0 + lane * 16), 0), 16) : 0;
+                const float magnitude = fabsf(va) <= FLT_MAX ? fabsf(va) : 0.0f;
+                __syncwarp();
+                if (lane < kGroups) groups[lane] = make_float4(ka, fabsf(va) <= FLT_MAX ? va : __int_as_float(0x7FC00000), log2f(magnitude), __int_as_float(mine));
+                // plain: every position is visible, and larger products are larger scores
+                const bool plain = __all_sync(0xffffffffu, lane >= kGroups || (mine == 16 && __fmul_rn(ka, p.scale) >= 0.0f));
+                id = id_next;
+                scales_of(id, &ka, &va);
+                id_next = page_of((u + 2) * kPos);
                 ok = wait_warp(bars, &bars->scored, n & 1, status);
                 if (!ok) break;
                 fence_after();
-                float xg[kGroups];
-                float top = -INFINITY;
+                // the tile's largest score, and the largest log of a score's weight times its value scale; scores that are all NaN leave none
+                float top = -INFINITY, heavy = -INFINITY;
+                auto note = [&](float x, float log_scale) {
+                    top = fmaxf(top, x);
+                    heavy = fmaxf(heavy, __fadd_rn(x, log_scale));
+                };
+                if (plain) {
+                    for_groups<kGroups>(tmem + lanes, [&](int g, const uint32_t (&s)[16]) {
+                        const float4 of = groups[g];
+                        float hi = max3(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2])), lo = max3(__uint_as_float(s[3]), __uint_as_float(s[4]), __uint_as_float(s[5]));
 #pragma unroll
-                for (int c = 0; c < kPos / 32; ++c) {
-                    uint32_t s[32];
-                    tmem_load(tmem + lanes + c * 32, s);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int g = 2 * c + h;
-                        float hi = -INFINITY, lo = INFINITY;
-                        if (all) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                hi = fmaxf(hi, __uint_as_float(s[16 * h + i]));
-                                lo = fminf(lo, __uint_as_float(s[16 * h + i]));
-                            }
-                        } else {
-                            const int many = __shfl_sync(0xffffffffu, mine, g);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                if (i < many) {
-                                    hi = fmaxf(hi, __uint_as_float(s[16 * h + i]));
-                                    lo = fminf(lo, __uint_as_float(s[16 * h + i]));
-                                }
+                        for (int i = 6; i < 14; i += 4) {
+                            hi = max3(hi, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+                            lo = max3(lo, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
                         }
-                        const float kf = __fmul_rn(__shfl_sync(0xffffffffu, ka, g), factor);
-                        // nothing visible, or all of it NaN: -infinity either way
-                        xg[g] = hi == -INFINITY && lo == INFINITY ? -INFINITY : __fmul_rn(kf >= 0.0f ? hi : lo, kf);
-                        top = fmaxf(top, xg[g]);
-                    }
+                        hi = max3(hi, __uint_as_float(s[14]), __uint_as_float(s[15]));
+                        note(__fmul_rn(fmaxf(hi, lo), __fmul_rn(of.x, factor)), of.z);
+                    });
+                } else {
+                    for_groups<kGroups>(tmem + lanes, [&](int g, const uint32_t (&s)[16]) {
+                        const float4 of = groups[g];
+                        const float kf = __fmul_rn(of.x, factor);
+                        const int many = __float_as_int(of.w);
+                        float hi = -INFINITY, lo = INFINITY;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (i < many) {
+                                hi = fmaxf(hi, __uint_as_float(s[i]));
+                                lo = fminf(lo, __uint_as_float(s[i]));
+                            }
+                        if (hi >= lo) note(__fmul_rn(kf >= 0.0f ? hi : lo, kf), of.z);
+                    });
                 }
                 // does the tile fit the row's maximum and unit
-                const float odd_va = fabsf(va) <= FLT_MAX ? fabsf(va) : 0.0f;  // an infinite scale counts as NaN, and sets no unit
-                float most_w = 0.0f;
-                bool live = false;
                 float less = m - kBias;
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g) {
-                    const float s = __shfl_sync(0xffffffffu, odd_va, g);
-                    live |= s > 0.0f && xg[g] > -INFINITY;
-                    most_w = fmaxf(most_w, __fmul_rn(__fmul_rn(ex2(xg[g] - less), s), per_unit));
-                }
+                const bool live = heavy > -INFINITY;
+                const float most_w = __fmul_rn(ex2(heavy - less), per_unit);
                 const bool fits = (!live || most_w >= kLeast) && most_w <= kMost && ex2(top - less) <= kMostExp;
                 if (!__all_sync(0xffffffffu, fits)) {
+                    const float largest = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < kGroups && mine > 0 ? __float_as_uint(magnitude) : 0u));
                     float by = 1.0f;  // what the sums are multiplied by
                     int raise = 0;    // the unit goes down by so many powers of two
                     if (!fits && top > kNone) {
@@ -374,16 +460,11 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                             m = top;
                             l = __fmul_rn(l, by);
                         }
-                    }
-                    float to = 0.0f;
-#pragma unroll
-                    for (int g = 0; g < kGroups; ++g) {
-                        const float s = __shfl_sync(0xffffffffu, odd_va, g);
-                        if (s > 0.0f && xg[g] > -INFINITY) to = fmaxf(to, __fmul_rn(fmaxf(ex2(xg[g] - m), kLeastOfScale), s));
-                    }
-                    if (!fits && live && top > kNone) {
-                        const unsigned unit = min(__float_as_uint(fmaxf(to, kLeastUnit)) & 0x7f800000u, kMostUnit);
-                        raise = (static_cast<int>((254u << 23) - unit) - static_cast<int>(__float_as_uint(per_unit))) >> 23;
+                        if (live) {
+                            const float to = fmaxf(ex2(heavy - m), __fmul_rn(kLeastOfScale, largest));
+                            const unsigned unit = min(__float_as_uint(fmaxf(to, kLeastUnit)) & 0x7f800000u, kMostUnit);
+                            raise = (static_cast<int>((254u << 23) - unit) - static_cast<int>(__float_as_uint(per_unit))) >> 23;
+                        }
                     }
                     if (u > it.from) {
                         // earlier tiles' sums are complete before they are touched
@@ -396,6 +477,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                             for (int c = 0; c < DIM; c += 16) {
                                 uint32_t o[16];
                                 tmem_load(sums + lanes + c, o);
+                                tmem_loaded(o);
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) most = max(most, o[i] & 0x7fffffffu);
                             }
@@ -408,6 +490,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                         for (int c = 0; c < DIM; c += 16) {
                             uint32_t o[16];
                             tmem_load(sums + lanes + c, o);
+                            tmem_loaded(o);
 #pragma unroll
                             for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(o[i]), one), two));
                             tmem_store(sums + lanes + c, o);
@@ -417,51 +500,45 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                     per_unit = __uint_as_float(__float_as_uint(per_unit) + (static_cast<unsigned>(raise) << 23));
                     less = m - kBias;
                 }
-                // weights: their parts take the scores' place, 16 columns of the first and 16 of the second for 32 positions
-                float tile_sum = 0.0f;
-#pragma unroll
-                for (int c = 0; c < kPos / 32; ++c) {
-                    uint32_t s[32], w[32];
-                    tmem_load(tmem + lanes + c * 32, s);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int g = 2 * c + h;
-                        const float kf = __fmul_rn(__shfl_sync(0xffffffffu, ka, g), factor), value = __shfl_sync(0xffffffffu, va, g);
-                        const float vf = fabsf(value) <= FLT_MAX ? in_units(value, per_unit) : __int_as_float(0x7FC00000);
-                        const int many = all ? 16 : __shfl_sync(0xffffffffu, mine, g);
-                        float e[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            e[i] = ex2(__fmaf_rn(__uint_as_float(s[16 * h + i]), kf, -less));
-                            if (!all && i >= many) e[i] = 0.0f;
-                        }
-                        float2 part = make_float2(0.0f, 0.0f);
+                // weights: their parts take the scores' place, for 16 positions eight columns of the first and eight of the second
+                float2 tile_sum = make_float2(0.0f, 0.0f);
+                auto weigh = [&](auto every) {
+                    for_groups<kGroups>(tmem + lanes, [&](int g, const uint32_t (&s)[16]) {
+                        const float4 of = groups[g];
+                        const float kf = __fmul_rn(of.x, factor), vf = of.y == of.y ? in_units(of.y, per_unit) : of.y;
+                        const int many = every.value ? 16 : __float_as_int(of.w);
+                        uint32_t w[16];
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
-                            part = add2_rn(part, make_float2(e[i], e[i + 1]));
-                            float a = __fmul_rn(e[i], vf), b = __fmul_rn(e[i + 1], vf);
-                            if (!all) {  // a scale that is not finite does not count where nothing is seen
-                                if (i >= many) a = 0.0f;
-                                if (i + 1 >= many) b = 0.0f;
+                            const float2 x = fma2_rn(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(kf, kf), make_float2(-less, -less));
+                            float2 e = make_float2(ex2(x.x), ex2(x.y));
+                            if (!every.value) {
+                                if (i >= many) e.x = 0.0f;
+                                if (i + 1 >= many) e.y = 0.0f;
                             }
-                            const uint32_t x = pack_half(a, b);
-                            const float2 y = unpack_half(x);
-                            w[8 * h + i / 2] = x;
-                            w[16 + 8 * h + i / 2] = pack_half(__fsub_rn(a, y.x), __fsub_rn(b, y.y));
+                            tile_sum = add2_rn(tile_sum, e);
+                            float2 a = mul2_rn(e, make_float2(vf, vf));
+                            if (!every.value) {  // a scale that is not finite does not count where nothing is seen
+                                if (i >= many) a.x = 0.0f;
+                                if (i + 1 >= many) a.y = 0.0f;
+                            }
+                            w[i / 2] = pack_half(a.x, a.y);
+                            const float2 y = unpack_half(w[i / 2]);
+                            a = add2_rn(a, make_float2(-y.x, -y.y));
+                            w[8 + i / 2] = pack_half(a.x, a.y);
                         }
-                        tile_sum = __fadd_rn(tile_sum, __fadd_rn(part.x, part.y));
-                    }
-                    tmem_store(tmem + lanes + c * 32, w);
-                }
-                l = __fadd_rn(l, tile_sum);
+                        tmem_store(tmem + lanes + g * 16, w);
+                    });
+                };
+                if (plain)
+                    weigh(std::true_type{});
+                else
+                    weigh(std::false_type{});
+                l = __fadd_rn(l, __fadd_rn(tile_sum.x, tile_sum.y));
                 tmem_stored();
                 fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bars->weighed);
-                id = id_next;
-                id_next = id_after;
-                ka = ka_next;
-                va = va_next;
             }
             if (!ok) break;
             // ---- the part's sums as weighted means (no larger than the values), by rows of 64 bytes through the queries' memory
@@ -485,6 +562,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
             for (int c = 0; c < DIM; c += 16) {
                 uint32_t o[16];
                 tmem_load(sums + lanes + c, o);
+                tmem_loaded(o);
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) {
@@ -506,34 +584,33 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
             }
             // the tensor memory has been read before the next item's first product writes it, and the staging memory before queries take it
             fence_before();
-            __syncwarp();
+            done();
         }
     } else if (warp < kRowWarps + kCopyWarps) {
         // ------------------------------------------------------------ codes
-        if constexpr (DIM != 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if constexpr (DIM != 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         constexpr int kPieces = DIM / 16;                            // 16-byte pieces of a row
         constexpr int kRowsAtOnce = kCopyWarps * 32 / kPieces, kPasses = kPos / kRowsAtOnce;
-        const int tid = threadIdx.x - kRowWarps * 32, piece = tid % kPieces, first_row = tid / kPieces;
-        // a piece's 32 bytes of floats: two of a row's 16-byte chunks; pieces of every other 64 dimensions store them in the other
-        // order, so that eight lanes meet all banks
-        const int block_of = piece / 4, swap = block_of & 1;
-        const uint32_t chunk = piece % 4 * 2;
+        // four lanes take 64 dimensions of a row, the next four the row below: their stores of 16 bytes, of every other chunk, meet all banks
+        const int tid = threadIdx.x - kRowWarps * 32, quad = tid / 4, block_of = quad / 2 % kBlocks, first_row = quad / 2 / kBlocks * 2 + quad % 2;
+        const int piece = block_of * 4 + tid % 4;
+        const uint32_t chunk = tid % 4 * 2;
         const int64_t page_bytes = static_cast<int64_t>(heads) * page * DIM;
 #pragma unroll 1
-        for (; ok && items.next(p);) {
-            const SharedItem &it = items.item;
-            auto page_of = [&](int pos0) -> int {
-                const int pos = pos0 + lane * 16;
-                const int id = lane < kGroups && pos < it.len ? p.prefix_table[it.group * p.prefix_width + (pos >> page_log)] : -1;
-                return id < p.c.pages ? id : -1;
-            };
+        for (;;) {
+            const SharedItem &it = take();
+            if (!ok || it.rows == 0) break;
+            const int len = it.len, to = it.to;
+            const int32_t *const table = p.prefix_table + it.group * p.prefix_width;
+            auto page_of = [&](int pos0) { return load_page(table, pos0 + lane * 16, lane < kGroups ? len : 0, page_log); };
+            const int64_t head_at = static_cast<int64_t>(it.h) * page * DIM + piece * 16;
             auto load = [&](const void *codes, int pos0, int ids, uint4 (&x)[kPasses]) {
-                const uint8_t *const base = static_cast<const uint8_t *>(codes) + static_cast<int64_t>(it.h) * page * DIM + piece * 16;
+                const uint8_t *const base = static_cast<const uint8_t *>(codes) + head_at;
 #pragma unroll
                 for (int i = 0; i < kPasses; ++i) {
                     const int r = i * kRowsAtOnce + first_row, pos = pos0 + r, id = __shfl_sync(0xffffffffu, ids, r / 16);
                     // positions that are not there: zeros, which no weight of zero can turn into a NaN
-                    x[i] = id >= 0 && pos < it.len ? __ldg(reinterpret_cast<const uint4 *>(base + id * page_bytes + (pos & (page - 1)) * DIM)) : make_uint4(0, 0, 0, 0);
+                    x[i] = load_codes(base + id * page_bytes + (pos & (page - 1)) * DIM, there(id) && pos < len);
                 }
             };
             auto store = [&](uint8_t *tile, const uint4 (&x)[kPasses]) {
@@ -541,44 +618,61 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                 for (int i = 0; i < kPasses; ++i) {
                     const int r = i * kRowsAtOnce + first_row;
                     const uint2 a = widen<KV>(x[i].x), b = widen<KV>(x[i].y), c = widen<KV>(x[i].z), d = widen<KV>(x[i].w);
-                    const uint4 lo = make_uint4(a.x, a.y, b.x, b.y), hi = make_uint4(c.x, c.y, d.x, d.y);
                     uint8_t *const at = tile + block_of * (kPos * 128) + r * 128;
-                    *reinterpret_cast<uint4 *>(at + (((chunk + swap) ^ (r & 7)) * 16)) = swap ? hi : lo;
-                    *reinterpret_cast<uint4 *>(at + (((chunk + 1 - swap) ^ (r & 7)) * 16)) = swap ? lo : hi;
+                    *reinterpret_cast<uint4 *>(at + ((chunk ^ (r & 7)) * 16)) = make_uint4(a.x, a.y, b.x, b.y);
+                    *reinterpret_cast<uint4 *>(at + (((chunk + 1) ^ (r & 7)) * 16)) = make_uint4(c.x, c.y, d.x, d.y);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
             };
-            int ids = page_of(it.from * kPos);
+            int ids = page_of(it.from * kPos), u = it.from;
             uint4 x[kPasses];
-            load(p.c.k, it.from * kPos, ids, x);
+            load(p.c.k, u * kPos, ids, x);
+            int ids_next = page_of((u + 1) * kPos);
+            // keys, then values of a tile, by the same instructions
 #pragma unroll 1
-            for (int u = it.from; u < it.to; ++u, ++n) {
-                const int ids_next = page_of((u + 1) * kPos);
-                ok = n == 0 || wait_warp(bars, &bars->scored, (n - 1) & 1, status);
+            for (bool values = false;; values = !values) {
+                ok = n == 0 || wait_warp(bars, values ? &bars->summed : &bars->scored, (n - 1) & 1, status);
                 if (!ok) break;
-                store(smem + C::kQBytes, x);
-                if (lane == 0) mbar_arrive(&bars->k_full);
-                load(p.c.v, u * kPos, ids, x);
-                ok = n == 0 || wait_warp(bars, &bars->summed, (n - 1) & 1, status);
-                if (!ok) break;
-                store(smem + C::kQBytes + C::kTile, x);
-                if (lane == 0) mbar_arrive(&bars->v_full);
-                ids = ids_next;
-                if (u + 1 < it.to) load(p.c.k, (u + 1) * kPos, ids, x);
+                store(smem + C::kQBytes + (values ? C::kTile : 0), x);
+                if (lane == 0) mbar_arrive(values ? &bars->v_full : &bars->k_full);
+                if (values) {
+                    ++n;
+                    ids = ids_next;
+                    if (++u == to) break;
+                    ids_next = page_of((u + 1) * kPos);
+                }
+                load(values ? p.c.k : p.c.v, u * kPos, ids, x);
             }
+            if (!ok) break;
+            done();
         }
     } else {
         // ------------------------------------------------------------ products
-        if constexpr (DIM != 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 48;");
-        int segment = 0;
+        if constexpr (DIM != 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if (warp == kWalkWarp) {
+            SharedItems walk;
+            walk.start(p, blockIdx.x);
 #pragma unroll 1
-        for (; warp == kProductWarp && ok && items.next(p); ++segment) {
-            const SharedItem &it = items.item;
+            for (bool more = true; ok && more; ++items) {
+                if (items >= 2) ok = wait_warp(bars, &bars->item_free[items & 1], items / 2 - 1 & 1, status);
+                SharedItem it{};
+                more = walk.next(p, &it);
+                if (lane == 0) {
+                    bars->item[items & 1] = it;
+                    mbar_arrive(&bars->item_full[items & 1]);
+                }
+                __syncwarp();
+            }
+        }
+#pragma unroll 1
+        for (; warp == kProductWarp;) {
+            const SharedItem &it = take();
+            if (!ok || it.rows == 0) break;
             if (lane == 0) {
 #pragma unroll 1
                 for (int u = it.from; ok && u < it.to; ++u, ++n) {
-                    ok = (u > it.from || wait(bars, &bars->q_full, segment & 1, status)) && wait(bars, &bars->k_full, n & 1, status) &&
+                    ok = (u > it.from || wait(bars, &bars->q_full, items & 1, status)) && wait(bars, &bars->k_full, n & 1, status) &&
                          (n == 0 || wait(bars, &bars->summed, (n - 1) & 1, status));  // the weights, in the scores' place, have been read
                     if (!ok) break;
                     fence_after();
@@ -601,13 +695,15 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                     for (int k = 0; k < kPos / 16; ++k)
 #pragma unroll
                         for (int part = 1; part >= 0; --part) {  // small parts first
-                            mma_tmem(sums, tmem + k / 2 * 32 + part * 16 + k % 2 * 8, operand(v_at + k * 2048, kPos * 128), C::kSums, add);
+                            mma_tmem(sums, tmem + k * 16 + part * 8, operand(v_at + k * 2048, kPos * 128), C::kSums, add);
                             add = true;
                         }
                     commit(&bars->summed);
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            done();
         }
         if (warp == kProductWarp && lane == 0) {
             // no product may still read shared memory or write tensor memory when the block frees them

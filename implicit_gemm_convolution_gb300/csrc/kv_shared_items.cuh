@@ -50,75 +50,60 @@ struct SharedItem {
     int group, h, t0, row0, rows, len;
     int units, from, to;
     bool at_start;  // of the block's share
-    bool more;      // false: there was none
 };
 
-// The parts of a block's share one after the other. Kept in shared memory, one for each warp that walks: registers are short where
-// it is used.
+// The parts of a block's share one after the other, by one warp.
 struct SharedItems {
-    SharedItem item;
     SharedGroup g;
     int u, begin, stop, before, j;
 
     __device__ __forceinline__ void start(const SharedProblem &p, int block) {
         const int total = shared_units(p), per = shared_per_block(p, total), lane = threadIdx.x & 31;
-        const int from = static_cast<int>(min(static_cast<int64_t>(block) * per, static_cast<int64_t>(total)));
-        int units = 0, at = 0;
-        if (from < total) {
+        begin = u = static_cast<int>(min(static_cast<int64_t>(block) * per, static_cast<int64_t>(total)));
+        stop = min(total - u, per) + u;
+        before = j = 0;
+        g = SharedGroup{};
+        if (u >= stop) return;
 #pragma unroll 1
-            for (int64_t base = 0; base < p.groups; base += 32) {
-                const int n = static_cast<int>(shared_group(p, base + lane).n);
-                int up = n;
+        for (int64_t base = 0; base < p.groups; base += 32) {
+            const int n = static_cast<int>(shared_group(p, base + lane).n);
+            int up = n;
 #pragma unroll
-                for (int o = 1; o < 32; o <<= 1) {
-                    const int x = __shfl_up_sync(0xffffffffu, up, o);
-                    if (lane >= o) up += x;
-                }
-                const unsigned here = __ballot_sync(0xffffffffu, from < units + up);
-                if (here != 0) {
-                    at = __ffs(here) - 1;
-                    units += __shfl_sync(0xffffffffu, up - n, at);
-                    at += static_cast<int>(base);
-                    break;
-                }
-                units += __shfl_sync(0xffffffffu, up, 31);
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, up, o);
+                if (lane >= o) up += x;
             }
+            const unsigned here = __ballot_sync(0xffffffffu, u < before + up);
+            if (here != 0) {
+                const int at = __ffs(here) - 1;
+                before += __shfl_sync(0xffffffffu, up - n, at);
+                j = static_cast<int>(base) + at;
+                break;
+            }
+            before += __shfl_sync(0xffffffffu, up, 31);
         }
-        if (lane == 0) {
-            g = from < total ? shared_group(p, at) : SharedGroup{};
-            begin = u = from;
-            stop = min(total - from, per) + from;
-            before = units;
-            j = at;
-        }
-        __syncwarp();
+        g = shared_group(p, j);
     }
-    // The next part, in item; false behind the last.
-    __device__ __forceinline__ bool next(const SharedProblem &p) {
-        __syncwarp();  // every lane is done with the last one
-        if ((threadIdx.x & 31) == 0 && u < stop) {
-            while (u >= before + static_cast<int>(g.n) && j < p.groups) {
-                before += static_cast<int>(g.n);
-                g = shared_group(p, ++j);
-            }
-            const int units = max(g.units, 1), i = (u - before) / units, first = before + i * units;
-            item.group = j;
-            item.h = i / max(g.row_blocks, 1);
-            item.t0 = g.t0;
-            item.row0 = (i - item.h * g.row_blocks) * kSharedRows;
-            item.rows = min(g.rows - item.row0, kSharedRows);
-            item.len = g.len;
-            item.units = units;
-            item.from = u - first;
-            item.to = min(units, stop - first);
-            item.at_start = u == begin;
-            u = first + item.to;
-            item.more = true;
-        } else if ((threadIdx.x & 31) == 0) {
-            item.more = false;
+    // The next part; false behind the last.
+    __device__ __forceinline__ bool next(const SharedProblem &p, SharedItem *item) {
+        if (u >= stop) return false;
+        while (u >= before + static_cast<int>(g.n) && j < p.groups) {
+            before += static_cast<int>(g.n);
+            g = shared_group(p, ++j);
         }
-        __syncwarp();
-        return item.more;
+        const int units = max(g.units, 1), i = (u - before) / units, first = before + i * units;
+        item->group = j;
+        item->h = i / max(g.row_blocks, 1);
+        item->t0 = g.t0;
+        item->row0 = (i - item->h * g.row_blocks) * kSharedRows;
+        item->rows = min(g.rows - item->row0, kSharedRows);
+        item->len = g.len;
+        item->units = units;
+        item->from = u - first;
+        item->to = min(units, stop - first);
+        item->at_start = u == begin;
+        u = first + item->to;
+        return true;
     }
 };
 
