@@ -167,8 +167,7 @@ cudaError_t launch_kv_attention_part_bf16(const KvAttentionProblem &p, cudaStrea
 constexpr int kSharedRows = 128;       // rows of an item: token times query head of a key head
 constexpr int kSharedMinUnits = 1;     // tiles that a block takes at least
 constexpr int kSharedMostBlocks = 304; // two an SM
-// Positions of a tile: what leaves two blocks of an SM their shared and tensor memory (heads of 256: one block).
-constexpr int shared_tile(int64_t dim, int parts) { return dim == 256 || (dim == 128 && parts == 2) ? 64 : 128; }
+constexpr int kSharedTile = 64;        // positions of a tile
 struct SharedProblem {
     om_kv_cache c;
     int64_t seqs, tokens, q_heads, groups;
@@ -179,7 +178,6 @@ struct SharedProblem {
     int64_t prefix_width;
     const int32_t *prefix_len, *group_at, *cu;
     float scale;
-    int tile_log;
     int64_t blocks, slot_rows;
     float2 *whole_state, *slot_state;  // [tokens][q_heads], [2 blocks][slot_rows]
     float *whole, *slots;              // and their values, [dim] each

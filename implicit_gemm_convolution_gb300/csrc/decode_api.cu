@@ -431,7 +431,6 @@ int om_kv_shared_attention(const om_kv_cache *cache, int64_t groups, const int32
             if (overlaps(w[i], w[j])) return OM_ERR_ALIAS;
     }
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int tile = om::shared_tile(c.dim, dtype == OM_F32 ? 2 : 1);
     int64_t blocks = static_cast<int64_t>(om::num_sms()) * (c.dim == 256 ? 1 : 2);
     if (blocks > om::kSharedMostBlocks) blocks = om::kSharedMostBlocks;
     if (prefix_units < blocks) blocks = static_cast<int64_t>(prefix_units);
@@ -446,7 +445,6 @@ int om_kv_shared_attention(const om_kv_cache *cache, int64_t groups, const int32
     p.q_fours = aligned(q, 4 * eb) && q_ts % 4 == 0 && q_hs % 4 == 0;
     p.prefix_table = prefix_table; p.prefix_width = prefix_width; p.prefix_len = prefix_len; p.group_at = group_offsets; p.cu = cu;
     p.scale = scale;
-    p.tile_log = tile == 64 ? 6 : 7;
     p.blocks = blocks;
     p.slot_rows = at.slot_rows;
     p.whole_state = at.whole_state; p.slot_state = at.slot_state; p.whole = at.whole; p.slots = at.slots;

@@ -10,12 +10,13 @@
 // with a power-of-two unit u for each row, set anew when a tile's largest weight leaves [2^-1, 2^15]: a weight is off by no more
 // than 2^-22 of itself or 2^-24 of its tile's largest.
 //
-// Block (two an SM for heads of up to 128: one's products run beside the other's exponentials):
-//   warps 0-3  a row of scores a thread: the tile's maxima from tensor memory, then weights, whose parts replace the scores as the
+// Block (12 warps, two blocks an SM for heads of up to 128), on tiles of 64 positions:
+//   warps 0-3  a row of scores a thread: the tile's maximum from tensor memory, then weights, whose parts replace the scores as the
 //              second product's operand; rows of sums are multiplied only when a unit or maximum changes; queries in, sums out.
-//   warps 4-7  codes from the pages (values on their way beside a tile's scores, the next keys beside its weights) to 16-bit floats in shared memory, rows of 128 bytes with
+//   warps 4-7  codes from the pages (on their way while earlier ones are used) to 16-bit floats in shared memory, rows of 128 bytes with
 //              the tensor cores' exclusive-or; keys and values have the same layout (as k-major and n-major operands).
-//   warp 8     tensor memory, and one thread that issues the products;  warp 9  finds the block's parts of items.
+//   warp 8     tensor memory, and one thread that issues the products: the next tile's scores beside the rows' work on this one.
+//   warp 9     finds the block's parts of items;  warp 10 lays out the tiles' scales.
 // Every mbarrier wait is bounded; on a timeout the block records the error, stops and frees its tensor memory.
 //
 // Split. The tiles of all items (group, key head, 128 rows) in equal shares of the blocks that fit at once, as lengths on the
@@ -37,7 +38,7 @@ namespace {
 
 constexpr int kRowWarps = 4, kCopyWarps = 4;
 constexpr int kThreads = 384;  // three warpgroups: registers are handed out by them
-constexpr int kProductWarp = kRowWarps + kCopyWarps, kWalkWarp = kProductWarp + 1;
+constexpr int kProductWarp = kRowWarps + kCopyWarps, kWalkWarp = kProductWarp + 1, kScaleWarp = kWalkWarp + 1;
 constexpr float kLog2e = 1.4426950408889634f;
 // as in kv_attention.cuh
 constexpr float kBias = 8.0f, kMost = 32768.0f, kLeast = 0.5f, kMostExp = 1099511627776.0f;
@@ -59,16 +60,17 @@ constexpr uint32_t descriptor_of(int n, bool b_n_major) {
     return (1u << 4) | (b_n_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(kSharedRows >> 4) << 24);
 }
 
-// PARTS: of a query. Positions of a tile: what leaves two blocks of an SM their shared and tensor memory (heads of 256: one block).
+// PARTS: of a query. Shared memory holds two blocks of an SM (heads of 256: one), tensor memory the scores of two tiles and the sums.
 template <int DIM, int PARTS>
 struct Config {
-    static constexpr int kPos = shared_tile(DIM, PARTS);
+    static constexpr int kPos = kSharedTile;
     static constexpr int kQPart = kSharedRows * DIM * 2;
     static constexpr int kQBytes = PARTS * kQPart;
     static constexpr int kTile = kPos * DIM * 2;
-    static constexpr int kSmem = 1024 + kQBytes + 2 * kTile;
-    static constexpr int kColumns = kPos + DIM <= 256 ? 256 : 512;  // of tensor memory: scores, then sums
-    static constexpr int kGroups = kPos / 16;                       // 16 positions have one page
+    static constexpr int kValueTiles = DIM * PARTS > 256 || DIM == 128 && PARTS == 2 ? 1 : 2;  // as many as fit
+    static constexpr int kSmem = 1024 + kQBytes + (1 + kValueTiles) * kTile;
+    static constexpr int kColumns = 2 * kPos + DIM <= 256 ? 256 : 512;
+    static constexpr int kGroups = kPos / 16;  // 16 positions have one page
     static constexpr uint32_t kScores = descriptor_of(kPos, false), kSums = descriptor_of(DIM, true);
 };
 
@@ -174,10 +176,20 @@ __device__ __forceinline__ uint2 widen(uint32_t w) {
     return o;
 }
 
+// What a tile's groups of 16 positions have: scale of the keys, of the values (NaN if it is not finite), the log of its
+// magnitude, visible positions.
+struct TileScales {
+    float4 group[kSharedTile / 16];
+    float largest;  // magnitude of a visible group's value scale
+    int plain;      // every position is visible, and larger products are larger scores
+};
+// Barriers of what there are two of (tiles by their number's parity, items) belong to one of them: a wait for a phase never
+// meets the phase after the next.
 struct Bars {
-    uint64_t q_full, k_full, v_full, scored, weighed, summed, drained;
+    uint64_t q_full, k_full, v_full[2], scaled[2], scored[2], weighed[2], summed[2], drained;
     uint64_t item_full[2], item_free[2];
     SharedItem item[2];  // rows 0: there are no more
+    TileScales scales[2];
     uint32_t tmem;
     int abort;
 };
@@ -265,20 +277,19 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
     uint8_t *const smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
     const uint32_t q_at = smem_u32(smem), k_at = q_at + C::kQBytes, v_at = k_at + C::kTile;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
-    __shared__ float4 groups_[kRowWarps][kGroups];  // a row warp's own
-    float4 *const groups = groups_[warp % kRowWarps];
     unsigned *const status = p.status;
     if (threadIdx.x == 0) {
         mbar_init(&bars->q_full, kRowWarps);
         mbar_init(&bars->k_full, kCopyWarps);
-        mbar_init(&bars->v_full, kCopyWarps);
-        mbar_init(&bars->scored, 1);
-        mbar_init(&bars->weighed, kRowWarps);
-        mbar_init(&bars->summed, 1);
         mbar_init(&bars->drained, 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->v_full[i], kCopyWarps);
+            mbar_init(&bars->scaled[i], 1);
+            mbar_init(&bars->scored[i], 1);
+            mbar_init(&bars->weighed[i], kRowWarps);
+            mbar_init(&bars->summed[i], 1);
             mbar_init(&bars->item_full[i], 1);
-            mbar_init(&bars->item_free[i], kProductWarp + 1);
+            mbar_init(&bars->item_free[i], kRowWarps + kCopyWarps + 2);
         }
         bars->abort = 0;
         fence_mbar_init();
@@ -291,15 +302,17 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = bars->tmem, sums = tmem + kPos;
+    const uint32_t tmem = bars->tmem, sums = tmem + 2 * kPos;
     wait_for_earlier();
 
     const int page = static_cast<int>(p.c.page), page_log = 31 - __clz(page), heads = static_cast<int>(p.c.heads);
     const unsigned pages = static_cast<unsigned>(p.c.pages);
     auto there = [&](int id) { return static_cast<unsigned>(id) < pages; };
-    int n = 0;  // tiles of this block so far, the phase of its barriers
+    int n = 0;  // tiles of this block so far
     int items = 0;
     bool ok = true;
+    // waits for tile i at a barrier of two
+    auto wait_tile = [&](uint64_t (&bar)[2], int i) { return wait_warp(bars, &bar[i & 1], i / 2 & 1, status); };
     // the block's next part of an item (rows 0: none), and the end of a warp's work on it
     auto take = [&]() -> const SharedItem & {
         ok = wait_warp(bars, &bars->item_full[items & 1], items / 2 & 1, status);
@@ -384,34 +397,15 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
             if (lane == 0) mbar_arrive(&bars->q_full);
 
             float m = kNone, l = 0.0f, per_unit = 1.0f;
-            // pages of the tile's groups of 16 positions: lane g has group g's, a tile ahead (and looks at it only when it is needed)
-            const int len = it.len, to = it.to;
-            const int32_t *const table = p.prefix_table + it.group * p.prefix_width;
-            auto page_of = [&](int pos0) { return load_page(table, pos0 + lane * 16, lane < kGroups ? len : 0, page_log); };
-            auto scales_of = [&](int id, float *ka, float *va) {
-                const int64_t at = static_cast<int64_t>(id) * heads + it.h;
-                *ka = there(id) ? p.c.k_scale[at] : 0.0f;
-                *va = there(id) ? p.c.v_scale[at] : 0.0f;
-            };
-            int id = page_of(it.from * kPos), id_next = page_of((it.from + 1) * kPos);
-            float ka, va;
-            scales_of(id, &ka, &va);
+            const int from = it.from, to = it.to;
 #pragma unroll 1
-            for (int u = it.from; ok && u < to; ++u, ++n) {
-                const int pos0 = u * kPos;
-                // what every lane needs of the groups: scales (an infinite one counts as NaN), the log of the values', visible positions
-                const int mine = there(id) ? min(max(len - (pos0 + lane * 16), 0), 16) : 0;
-                const float magnitude = fabsf(va) <= FLT_MAX ? fabsf(va) : 0.0f;
-                __syncwarp();
-                if (lane < kGroups) groups[lane] = make_float4(ka, fabsf(va) <= FLT_MAX ? va : __int_as_float(0x7FC00000), log2f(magnitude), __int_as_float(mine));
-                // plain: every position is visible, and larger products are larger scores
-                const bool plain = __all_sync(0xffffffffu, lane >= kGroups || (mine == 16 && __fmul_rn(ka, p.scale) >= 0.0f));
-                id = id_next;
-                scales_of(id, &ka, &va);
-                id_next = page_of((u + 2) * kPos);
-                ok = wait_warp(bars, &bars->scored, n & 1, status);
+            for (int u = from; u < to; ++u, ++n) {
+                const uint32_t scores = tmem + lanes + (n & 1) * kPos;
+                const float4 *const groups = bars->scales[n & 1].group;
+                ok = wait_tile(bars->scaled, n) && wait_tile(bars->scored, n);
                 if (!ok) break;
                 fence_after();
+                const bool plain = bars->scales[n & 1].plain;
                 // the tile's largest score, and the largest log of a score's weight times its value scale; scores that are all NaN leave none
                 float top = -INFINITY, heavy = -INFINITY;
                 auto note = [&](float x, float log_scale) {
@@ -419,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                     heavy = fmaxf(heavy, __fadd_rn(x, log_scale));
                 };
                 if (plain) {
-                    for_groups<kGroups>(tmem + lanes, [&](int g, const uint32_t (&s)[16]) {
+                    for_groups<kGroups>(scores, [&](int g, const uint32_t (&s)[16]) {
                         const float4 of = groups[g];
                         float hi = max3(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2])), lo = max3(__uint_as_float(s[3]), __uint_as_float(s[4]), __uint_as_float(s[5]));
 #pragma unroll
@@ -431,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                         note(__fmul_rn(fmaxf(hi, lo), __fmul_rn(of.x, factor)), of.z);
                     });
                 } else {
-                    for_groups<kGroups>(tmem + lanes, [&](int g, const uint32_t (&s)[16]) {
+                    for_groups<kGroups>(scores, [&](int g, const uint32_t (&s)[16]) {
                         const float4 of = groups[g];
                         const float kf = __fmul_rn(of.x, factor);
                         const int many = __float_as_int(of.w);
@@ -451,7 +445,6 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                 const float most_w = __fmul_rn(ex2(heavy - less), per_unit);
                 const bool fits = (!live || most_w >= kLeast) && most_w <= kMost && ex2(top - less) <= kMostExp;
                 if (!__all_sync(0xffffffffu, fits)) {
-                    const float largest = __uint_as_float(__reduce_max_sync(0xffffffffu, lane < kGroups && mine > 0 ? __float_as_uint(magnitude) : 0u));
                     float by = 1.0f;  // what the sums are multiplied by
                     int raise = 0;    // the unit goes down by so many powers of two
                     if (!fits && top > kNone) {
@@ -461,14 +454,14 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                             l = __fmul_rn(l, by);
                         }
                         if (live) {
-                            const float to = fmaxf(ex2(heavy - m), __fmul_rn(kLeastOfScale, largest));
+                            const float to = fmaxf(ex2(heavy - m), __fmul_rn(kLeastOfScale, bars->scales[n & 1].largest));
                             const unsigned unit = min(__float_as_uint(fmaxf(to, kLeastUnit)) & 0x7f800000u, kMostUnit);
                             raise = (static_cast<int>((254u << 23) - unit) - static_cast<int>(__float_as_uint(per_unit))) >> 23;
                         }
                     }
-                    if (u > it.from) {
+                    if (u > from) {
                         // earlier tiles' sums are complete before they are touched
-                        ok = wait_warp(bars, &bars->summed, (n - 1) & 1, status);
+                        ok = wait_tile(bars->summed, n - 1);
                         if (!ok) break;
                         fence_after();
                         if (__any_sync(0xffffffffu, raise > 0)) {
@@ -503,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                 // weights: their parts take the scores' place, for 16 positions eight columns of the first and eight of the second
                 float2 tile_sum = make_float2(0.0f, 0.0f);
                 auto weigh = [&](auto every) {
-                    for_groups<kGroups>(tmem + lanes, [&](int g, const uint32_t (&s)[16]) {
+                    for_groups<kGroups>(scores, [&](int g, const uint32_t (&s)[16]) {
                         const float4 of = groups[g];
                         const float kf = __fmul_rn(of.x, factor), vf = of.y == of.y ? in_units(of.y, per_unit) : of.y;
                         const int many = every.value ? 16 : __float_as_int(of.w);
@@ -527,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                             a = add2_rn(a, make_float2(-y.x, -y.y));
                             w[8 + i / 2] = pack_half(a.x, a.y);
                         }
-                        tmem_store(tmem + lanes + g * 16, w);
+                        tmem_store(scores + g * 16, w);
                     });
                 };
                 if (plain)
@@ -538,11 +531,11 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                 tmem_stored();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bars->weighed);
+                if (lane == 0) mbar_arrive(&bars->weighed[n & 1]);
             }
             if (!ok) break;
             // ---- the part's sums as weighted means (no larger than the values), by rows of 64 bytes through the queries' memory
-            ok = wait_warp(bars, &bars->summed, (n - 1) & 1, status);
+            ok = wait_tile(bars->summed, n - 1);
             if (!ok) break;
             fence_after();
             const float inv = shared_inverse(l), back = reciprocal(per_unit);
@@ -629,13 +622,14 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
             uint4 x[kPasses];
             load(p.c.k, u * kPos, ids, x);
             int ids_next = page_of((u + 1) * kPos);
-            // keys, then values of a tile, by the same instructions
+            // keys, then values of a tile, by the same instructions; each waits for the products that read what it takes the place of
 #pragma unroll 1
             for (bool values = false;; values = !values) {
-                ok = n == 0 || wait_warp(bars, values ? &bars->summed : &bars->scored, (n - 1) & 1, status);
+                const int last = values ? n - C::kValueTiles : n - 1, stage = values ? n % C::kValueTiles : 0;
+                ok = last < 0 || wait_tile(values ? bars->summed : bars->scored, last);
                 if (!ok) break;
-                store(smem + C::kQBytes + (values ? C::kTile : 0), x);
-                if (lane == 0) mbar_arrive(values ? &bars->v_full : &bars->k_full);
+                store(smem + C::kQBytes + (values ? 1 + stage : 0) * C::kTile, x);
+                if (lane == 0) mbar_arrive(values ? &bars->v_full[stage] : &bars->k_full);
                 if (values) {
                     ++n;
                     ids = ids_next;
@@ -655,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
             walk.start(p, blockIdx.x);
 #pragma unroll 1
             for (bool more = true; ok && more; ++items) {
-                if (items >= 2) ok = wait_warp(bars, &bars->item_free[items & 1], items / 2 - 1 & 1, status);
+                if (items >= 2) ok = wait_warp(bars, &bars->item_free[items & 1], (items / 2 - 1) & 1, status);
                 SharedItem it{};
                 more = walk.next(p, &it);
                 if (lane == 0) {
@@ -664,46 +658,94 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                 }
                 __syncwarp();
             }
-        }
+        } else if (warp == kScaleWarp) {
 #pragma unroll 1
-        for (; warp == kProductWarp;) {
-            const SharedItem &it = take();
-            if (!ok || it.rows == 0) break;
-            if (lane == 0) {
+            for (;;) {
+                const SharedItem &it = take();
+                if (!ok || it.rows == 0) break;
+                const int len = it.len, to = it.to;
+                const int32_t *const table = p.prefix_table + it.group * p.prefix_width;
+                // lane g has group g's page, a tile ahead
+                auto page_of = [&](int pos0) { return load_page(table, pos0 + lane * 16, lane < kGroups ? len : 0, page_log); };
+                int id = page_of(it.from * kPos);
 #pragma unroll 1
-                for (int u = it.from; ok && u < it.to; ++u, ++n) {
-                    ok = (u > it.from || wait(bars, &bars->q_full, items & 1, status)) && wait(bars, &bars->k_full, n & 1, status) &&
-                         (n == 0 || wait(bars, &bars->summed, (n - 1) & 1, status));  // the weights, in the scores' place, have been read
+                for (int u = it.from; u < to; ++u, ++n) {
+                    const int id_next = page_of((u + 1) * kPos);
+                    const int64_t at = static_cast<int64_t>(id) * heads + it.h;
+                    const float ka = there(id) ? p.c.k_scale[at] : 0.0f, va = there(id) ? p.c.v_scale[at] : 0.0f;
+                    const int many = there(id) ? min(max(len - (u * kPos + lane * 16), 0), 16) : 0;
+                    const bool finite = fabsf(va) <= FLT_MAX;  // an infinite scale counts as NaN, and sets no unit
+                    const float magnitude = finite ? fabsf(va) : 0.0f;
+                    const bool plain = __all_sync(0xffffffffu, lane >= kGroups || (many == 16 && __fmul_rn(ka, p.scale) >= 0.0f));
+                    const unsigned largest = __reduce_max_sync(0xffffffffu, many > 0 ? __float_as_uint(magnitude) : 0u);
+                    ok = n < 2 || wait_tile(bars->weighed, n - 2);
                     if (!ok) break;
-                    fence_after();
-                    bool add = false;
+                    TileScales &s = bars->scales[n & 1];
+                    if (lane < kGroups) s.group[lane] = make_float4(ka, finite ? va : __int_as_float(0x7FC00000), log2f(magnitude), __int_as_float(many));
+                    if (lane == 0) {
+                        s.largest = __uint_as_float(largest);
+                        s.plain = plain;
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->scaled[n & 1]);
+                    id = id_next;
+                }
+                if (!ok) break;
+                done();
+            }
+        } else if (warp == kProductWarp) {
+#pragma unroll 1
+            for (;;) {
+                const SharedItem &it = take();
+                if (!ok || it.rows == 0) break;
+                const int from = it.from, to = it.to;
+                if (lane == 0) {
+                    // the scores of tile i: their place is free when the products with the weights two tiles earlier are done
+                    auto score = [&](int i) {
+                        if (!(wait(bars, &bars->k_full, i & 1, status) && (i < 2 || wait(bars, &bars->summed[i & 1], (i / 2 - 1) & 1, status)))) return false;
+                        fence_after();
+                        const uint32_t to_scores = tmem + (i & 1) * kPos;
+                        bool add = false;
 #pragma unroll
-                    for (int part = PARTS - 1; part >= 0; --part)
+                        for (int part = PARTS - 1; part >= 0; --part)
 #pragma unroll
-                        for (int b = 0; b < kBlocks; ++b)
+                            for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                mma_smem(tmem, operand(q_at + part * C::kQPart + b * (kSharedRows * 128) + k * 32, 16), operand(k_at + b * (kPos * 128) + k * 32, 16), C::kScores, add);
+                                for (int k = 0; k < 4; ++k) {
+                                    mma_smem(to_scores, operand(q_at + part * C::kQPart + b * (kSharedRows * 128) + k * 32, 16), operand(k_at + b * (kPos * 128) + k * 32, 16),
+                                             C::kScores, add);
+                                    add = true;
+                                }
+                        commit(&bars->scored[i & 1]);
+                        return true;
+                    };
+                    ok = wait(bars, &bars->q_full, items & 1, status);
+                    // the next tile's scores are taken beside the rows' work on this one
+#pragma unroll 1
+                    for (int u = from - 1; ok && u < to; ++u) {
+                        if (u + 1 < to) ok = score(n + (u < from ? 0 : 1));
+                        if (!ok || u < from) continue;
+                        const int stage = n % C::kValueTiles;
+                        ok = wait(bars, &bars->v_full[stage], n / C::kValueTiles & 1, status) && wait(bars, &bars->weighed[n & 1], n / 2 & 1, status);
+                        if (!ok) break;
+                        fence_after();
+                        const uint32_t values = v_at + stage * C::kTile, weights = tmem + (n & 1) * kPos;
+                        bool add = u > from;
+#pragma unroll
+                        for (int k = 0; k < kPos / 16; ++k)
+#pragma unroll
+                            for (int part = 1; part >= 0; --part) {  // small parts first
+                                mma_tmem(sums, weights + k * 16 + part * 8, operand(values + k * 2048, kPos * 128), C::kSums, add);
                                 add = true;
                             }
-                    commit(&bars->scored);
-                    ok = wait(bars, &bars->v_full, n & 1, status) && wait(bars, &bars->weighed, n & 1, status);
-                    if (!ok) break;
-                    fence_after();
-                    add = u > it.from;
-#pragma unroll
-                    for (int k = 0; k < kPos / 16; ++k)
-#pragma unroll
-                        for (int part = 1; part >= 0; --part) {  // small parts first
-                            mma_tmem(sums, tmem + k * 16 + part * 8, operand(v_at + k * 2048, kPos * 128), C::kSums, add);
-                            add = true;
-                        }
-                    commit(&bars->summed);
+                        commit(&bars->summed[n & 1]);
+                        ++n;
+                    }
                 }
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) break;
+                done();
             }
-            ok = __shfl_sync(0xffffffffu, ok, 0);
-            if (!ok) break;
-            done();
         }
         if (warp == kProductWarp && lane == 0) {
             // no product may still read shared memory or write tensor memory when the block frees them

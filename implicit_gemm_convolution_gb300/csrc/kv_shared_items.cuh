@@ -26,7 +26,7 @@ __device__ __forceinline__ SharedGroup shared_group(const SharedProblem &p, int6
     g.rows = static_cast<int>((hi - lo) * p.group);
     g.row_blocks = (g.rows + kSharedRows - 1) / kSharedRows;
     g.len = static_cast<int>(min(max(static_cast<int64_t>(p.prefix_len[j]), static_cast<int64_t>(0)), p.prefix_width * p.c.page));
-    g.units = (g.len + (1 << p.tile_log) - 1) >> p.tile_log;
+    g.units = (g.len + kSharedTile - 1) / kSharedTile;
     g.n = p.c.heads * g.row_blocks * static_cast<int64_t>(g.units);
     return g;
 }
