@@ -10,13 +10,13 @@
 // with a power-of-two unit u for each row, set anew when a tile's largest weight leaves [2^-1, 2^15]: a weight is off by no more
 // than 2^-22 of itself or 2^-24 of its tile's largest.
 //
-// Block (12 warps, two blocks an SM for heads of up to 128), on tiles of 64 positions:
-//   warps 0-3  a row of scores a thread: the tile's maximum from tensor memory, then weights, whose parts replace the scores as the
-//              second product's operand; rows of sums are multiplied only when a unit or maximum changes; queries in, sums out.
-//   warps 4-7  codes from the pages (on their way while earlier ones are used) to 16-bit floats in shared memory, rows of 128 bytes with
-//              the tensor cores' exclusive-or; keys and values have the same layout (as k-major and n-major operands).
-//   warp 8     tensor memory, and one thread that issues the products: the next tile's scores beside the rows' work on this one.
-//   warp 9     finds the block's parts of items;  warp 10 lays out the tiles' scales.
+// Block (16 warps, two blocks an SM for heads of up to 128), on tiles of 64 positions:
+//   warps 0-3   a row of scores a thread: the tile's maximum from tensor memory, then weights, whose parts replace the scores as the
+//               second product's operand; rows of sums are multiplied only when a unit or maximum changes; queries in, sums out.
+//   warps 4-11  codes of keys (4-7) and values from the pages, the next tile's on their way, to 16-bit floats in shared memory: rows of
+//               128 bytes with the tensor cores' exclusive-or, the same layout for both (k-major and n-major operands).
+//   warp 12     tensor memory, and one lane that issues the products: the next tile's scores beside the rows' work on this one.
+//   warp 13     finds the block's parts of items;  warp 14 lays out the tiles' scales.
 // Every mbarrier wait is bounded; on a timeout the block records the error, stops and frees its tensor memory.
 //
 // Split. The tiles of all items (group, key head, 128 rows) in equal shares of the blocks that fit at once, as lengths on the
@@ -36,9 +36,10 @@
 namespace om {
 namespace {
 
-constexpr int kRowWarps = 4, kCopyWarps = 4;
-constexpr int kThreads = 384;  // three warpgroups: registers are handed out by them
-constexpr int kProductWarp = kRowWarps + kCopyWarps, kWalkWarp = kProductWarp + 1, kScaleWarp = kWalkWarp + 1;
+// four warpgroups, which registers are handed out by: rows, keys, values, and the warps that steer
+constexpr int kRowWarps = 4, kCopyWarps = 4;  // copy warps: of keys, and as many of values
+constexpr int kProductWarp = kRowWarps + 2 * kCopyWarps, kWalkWarp = kProductWarp + 1, kScaleWarp = kWalkWarp + 1;
+constexpr int kThreads = 512;
 constexpr float kLog2e = 1.4426950408889634f;
 // as in kv_attention.cuh
 constexpr float kBias = 8.0f, kMost = 32768.0f, kLeast = 0.5f, kMostExp = 1099511627776.0f;
@@ -67,8 +68,8 @@ struct Config {
     static constexpr int kQPart = kSharedRows * DIM * 2;
     static constexpr int kQBytes = PARTS * kQPart;
     static constexpr int kTile = kPos * DIM * 2;
-    static constexpr int kValueTiles = DIM * PARTS > 256 || DIM == 128 && PARTS == 2 ? 1 : 2;  // as many as fit
-    static constexpr int kSmem = 1024 + kQBytes + (1 + kValueTiles) * kTile;
+    static constexpr int kTiles = DIM * PARTS > 256 || (DIM == 128 && PARTS == 2) ? 1 : 2;  // of keys and of values: as many as fit
+    static constexpr int kSmem = 1024 + kQBytes + 2 * kTiles * kTile;
     static constexpr int kColumns = 2 * kPos + DIM <= 256 ? 256 : 512;
     static constexpr int kGroups = kPos / 16;  // 16 positions have one page
     static constexpr uint32_t kScores = descriptor_of(kPos, false), kSums = descriptor_of(DIM, true);
@@ -80,18 +81,20 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t block) {
     return static_cast<uint64_t>((addr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(block >> 4) << 16) | (static_cast<uint64_t>(1024 >> 4) << 32) |
            (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
 }
-__device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b),
-                 "r"(desc), "r"(static_cast<uint32_t>(add))
+__device__ __forceinline__ void mma_smem(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool add, bool leader) {
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %5, 0;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a),
+                 "l"(b), "r"(desc), "r"(static_cast<uint32_t>(add)), "r"(static_cast<uint32_t>(leader))
                  : "memory");
 }
-__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b),
-                 "r"(desc), "r"(static_cast<uint32_t>(add))
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool add, bool leader) {
+    asm volatile("{\n\t.reg .pred p, e;\n\tsetp.ne.u32 p, %4, 0;\n\tsetp.ne.u32 e, %5, 0;\n\t@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a),
+                 "l"(b), "r"(desc), "r"(static_cast<uint32_t>(add)), "r"(static_cast<uint32_t>(leader))
                  : "memory");
 }
-__device__ __forceinline__ void commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+__device__ __forceinline__ void commit(uint64_t *bar, bool leader) {
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.u32 e, %1, 0;\n\t@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+                 "r"(static_cast<uint32_t>(leader))
+                 : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -186,7 +189,7 @@ struct TileScales {
 // Barriers of what there are two of (tiles by their number's parity, items) belong to one of them: a wait for a phase never
 // meets the phase after the next.
 struct Bars {
-    uint64_t q_full, k_full, v_full[2], scaled[2], scored[2], weighed[2], summed[2], drained;
+    uint64_t q_full, k_full[2], v_full[2], scaled[2], scored[2], weighed[2], summed[2], drained;
     uint64_t item_full[2], item_free[2];
     SharedItem item[2];  // rows 0: there are no more
     TileScales scales[2];
@@ -194,33 +197,30 @@ struct Bars {
     int abort;
 };
 __device__ __forceinline__ bool aborted(Bars *b) { return *reinterpret_cast<volatile int *>(&b->abort) != 0; }
-// Bounded wait that also gives up once another role has failed. The barrier holds a waiting thread for up to the hint: polling takes
-// issue slots from the warps that work.
-constexpr uint32_t kHoldNs = 20000;
-__device__ __forceinline__ bool held_wait(uint64_t *bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-                 : "=r"(ok)
-                 : "r"(smem_u32(bar)), "r"(parity), "r"(kHoldNs)
-                 : "memory");
-    return ok != 0;
-}
+// Bounded wait of a warp that also gives up once another role has failed. SLEEP: nanoseconds between tests, for the roles that are ahead;
+// what a waiting warp issues, the working ones cannot.
+template <int SLEEP>
 __device__ __forceinline__ bool wait(Bars *b, uint64_t *bar, uint32_t parity, unsigned *status) {
-    if (held_wait(bar, parity)) return true;
-    const unsigned long long t0 = global_ns();
-    while (!held_wait(bar, parity)) {
-        if (aborted(b)) return false;
-        if (global_ns() - t0 > kWaitLimitNs) {
+    unsigned long long t0 = 0;
+    bool ok = true;
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 256; ++i) {
+            if (mbar_try_wait(bar, parity)) goto arrived;
+            if (SLEEP > 0) __nanosleep(SLEEP);
+        }
+        ok = !aborted(b);
+        const unsigned long long now = global_ns();
+        if (t0 == 0) t0 = now;
+        if (ok && now - t0 > kWaitLimitNs) {
             atomicOr(status, kDevErrTimeout);
             *reinterpret_cast<volatile int *>(&b->abort) = 1;
-            return false;
+            ok = false;
         }
+        if (!ok) break;
     }
-    return true;
-}
-// The same for all lanes of a warp.
-__device__ __forceinline__ bool wait_warp(Bars *b, uint64_t *bar, uint32_t parity, unsigned *status) {
-    return __all_sync(0xffffffffu, wait(b, bar, parity, status));
+arrived:
+    return __all_sync(0xffffffffu, ok);
 }
 
 // The page of a position, -1 behind the end. Nothing here looks at what was loaded, which would wait for it.
@@ -275,21 +275,21 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
     __shared__ Bars bars_;
     Bars *const bars = &bars_;
     uint8_t *const smem = raw_smem + ((1024u - (smem_u32(raw_smem) & 1023u)) & 1023u);
-    const uint32_t q_at = smem_u32(smem), k_at = q_at + C::kQBytes, v_at = k_at + C::kTile;
+    const uint32_t q_at = smem_u32(smem), k_at = q_at + C::kQBytes, v_at = k_at + C::kTiles * C::kTile;
     const int warp = threadIdx.x / 32, lane = threadIdx.x & 31;
     unsigned *const status = p.status;
     if (threadIdx.x == 0) {
         mbar_init(&bars->q_full, kRowWarps);
-        mbar_init(&bars->k_full, kCopyWarps);
         mbar_init(&bars->drained, 1);
         for (int i = 0; i < 2; ++i) {
+            mbar_init(&bars->k_full[i], kCopyWarps);
             mbar_init(&bars->v_full[i], kCopyWarps);
             mbar_init(&bars->scaled[i], 1);
             mbar_init(&bars->scored[i], 1);
             mbar_init(&bars->weighed[i], kRowWarps);
             mbar_init(&bars->summed[i], 1);
             mbar_init(&bars->item_full[i], 1);
-            mbar_init(&bars->item_free[i], kRowWarps + kCopyWarps + 2);
+            mbar_init(&bars->item_free[i], kRowWarps + 2 * kCopyWarps + 2);
         }
         bars->abort = 0;
         fence_mbar_init();
@@ -312,22 +312,24 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
     int items = 0;
     bool ok = true;
     // waits for tile i at a barrier of two
-    auto wait_tile = [&](uint64_t (&bar)[2], int i) { return wait_warp(bars, &bar[i & 1], i / 2 & 1, status); };
+    auto wait_tile = [&](auto sleep, uint64_t (&bar)[2], int i) { return wait<sleep.value>(bars, &bar[i & 1], i / 2 & 1, status); };
     // the block's next part of an item (rows 0: none), and the end of a warp's work on it
     auto take = [&]() -> const SharedItem & {
-        ok = wait_warp(bars, &bars->item_full[items & 1], items / 2 & 1, status);
+        ok = wait<32>(bars, &bars->item_full[items & 1], items / 2 & 1, status);
         return bars->item[items & 1];
     };
+    constexpr std::integral_constant<int, 0> at_once{};
+    constexpr std::integral_constant<int, 100> ahead{};
     auto done = [&]() {
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->item_free[items & 1]);
         ++items;
     };
 
-    // two blocks of 384 threads have 80 registers a thread: 240 for the three warpgroups
+    // two blocks of 512 threads have 64 registers a thread: 256 for the four warpgroups
     if (warp < kRowWarps) {
         // ------------------------------------------------------------ rows
-        if constexpr (DIM != 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        if constexpr (DIM != 256) asm volatile("setmaxnreg.inc.sync.aligned.u32 88;");
         const int row = warp * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
 #pragma unroll 1
@@ -402,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
             for (int u = from; u < to; ++u, ++n) {
                 const uint32_t scores = tmem + lanes + (n & 1) * kPos;
                 const float4 *const groups = bars->scales[n & 1].group;
-                ok = wait_tile(bars->scaled, n) && wait_tile(bars->scored, n);
+                ok = wait_tile(at_once, bars->scaled, n) && wait_tile(at_once, bars->scored, n);
                 if (!ok) break;
                 fence_after();
                 const bool plain = bars->scales[n & 1].plain;
@@ -461,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                     }
                     if (u > from) {
                         // earlier tiles' sums are complete before they are touched
-                        ok = wait_tile(bars->summed, n - 1);
+                        ok = wait_tile(at_once, bars->summed, n - 1);
                         if (!ok) break;
                         fence_after();
                         if (__any_sync(0xffffffffu, raise > 0)) {
@@ -535,7 +537,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
             }
             if (!ok) break;
             // ---- the part's sums as weighted means (no larger than the values), by rows of 64 bytes through the queries' memory
-            ok = wait_tile(bars->summed, n - 1);
+            ok = wait_tile(at_once, bars->summed, n - 1);
             if (!ok) break;
             fence_after();
             const float inv = shared_inverse(l), back = reciprocal(per_unit);
@@ -579,16 +581,17 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
             fence_before();
             done();
         }
-    } else if (warp < kRowWarps + kCopyWarps) {
+    } else if (warp < kRowWarps + 2 * kCopyWarps) {
         // ------------------------------------------------------------ codes
-        if constexpr (DIM != 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if constexpr (DIM != 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
         constexpr int kPieces = DIM / 16;                            // 16-byte pieces of a row
         constexpr int kRowsAtOnce = kCopyWarps * 32 / kPieces, kPasses = kPos / kRowsAtOnce;
         // four lanes take 64 dimensions of a row, the next four the row below: their stores of 16 bytes, of every other chunk, meet all banks
-        const int tid = threadIdx.x - kRowWarps * 32, quad = tid / 4, block_of = quad / 2 % kBlocks, first_row = quad / 2 / kBlocks * 2 + quad % 2;
+        const int tid = (threadIdx.x - kRowWarps * 32) % (kCopyWarps * 32), quad = tid / 4, block_of = quad / 2 % kBlocks, first_row = quad / 2 / kBlocks * 2 + quad % 2;
         const int piece = block_of * 4 + tid % 4;
         const uint32_t chunk = tid % 4 * 2;
         const int64_t page_bytes = static_cast<int64_t>(heads) * page * DIM;
+        const bool values = warp >= kRowWarps + kCopyWarps;
 #pragma unroll 1
         for (;;) {
             const SharedItem &it = take();
@@ -618,38 +621,36 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                 fence_proxy_async_smem();
                 __syncwarp();
             };
-            int ids = page_of(it.from * kPos), u = it.from;
+            const void *const codes = values ? p.c.v : p.c.k;
+            int ids = page_of(it.from * kPos);
             uint4 x[kPasses];
-            load(p.c.k, u * kPos, ids, x);
-            int ids_next = page_of((u + 1) * kPos);
-            // keys, then values of a tile, by the same instructions; each waits for the products that read what it takes the place of
+            load(codes, it.from * kPos, ids, x);
+            ids = page_of((it.from + 1) * kPos);
 #pragma unroll 1
-            for (bool values = false;; values = !values) {
-                const int last = values ? n - C::kValueTiles : n - 1, stage = values ? n % C::kValueTiles : 0;
-                ok = last < 0 || wait_tile(values ? bars->summed : bars->scored, last);
+            for (int u = it.from; u < to; ++u, ++n) {
+                // the products that read what this takes the place of
+                const int last = n - C::kTiles, stage = n % C::kTiles;
+                ok = last < 0 || wait_tile(ahead, values ? bars->summed : bars->scored, last);
                 if (!ok) break;
-                store(smem + C::kQBytes + (values ? 1 + stage : 0) * C::kTile, x);
-                if (lane == 0) mbar_arrive(values ? &bars->v_full[stage] : &bars->k_full);
-                if (values) {
-                    ++n;
-                    ids = ids_next;
-                    if (++u == to) break;
-                    ids_next = page_of((u + 1) * kPos);
-                }
-                load(values ? p.c.k : p.c.v, u * kPos, ids, x);
+                store(smem + C::kQBytes + ((values ? C::kTiles : 0) + stage) * C::kTile, x);
+                if (lane == 0) mbar_arrive(values ? &bars->v_full[stage] : &bars->k_full[stage]);
+                if (u + 1 < to) load(codes, (u + 1) * kPos, ids, x);
+                ids = page_of((u + 2) * kPos);
             }
             if (!ok) break;
             done();
         }
     } else {
         // ------------------------------------------------------------ products
-        if constexpr (DIM != 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+        if constexpr (DIM != 256) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        // one lane issues the products; the whole warp walks beside it, so that descriptors are uniform
+        const bool leader = lane == 0;
         if (warp == kWalkWarp) {
             SharedItems walk;
             walk.start(p, blockIdx.x);
 #pragma unroll 1
             for (bool more = true; ok && more; ++items) {
-                if (items >= 2) ok = wait_warp(bars, &bars->item_free[items & 1], (items / 2 - 1) & 1, status);
+                if (items >= 2) ok = wait<100>(bars, &bars->item_free[items & 1], (items / 2 - 1) & 1, status);
                 SharedItem it{};
                 more = walk.next(p, &it);
                 if (lane == 0) {
@@ -678,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                     const float magnitude = finite ? fabsf(va) : 0.0f;
                     const bool plain = __all_sync(0xffffffffu, lane >= kGroups || (many == 16 && __fmul_rn(ka, p.scale) >= 0.0f));
                     const unsigned largest = __reduce_max_sync(0xffffffffu, many > 0 ? __float_as_uint(magnitude) : 0u);
-                    ok = n < 2 || wait_tile(bars->weighed, n - 2);
+                    ok = n < 2 || wait_tile(ahead, bars->weighed, n - 2);
                     if (!ok) break;
                     TileScales &s = bars->scales[n & 1];
                     if (lane < kGroups) s.group[lane] = make_float4(ka, finite ? va : __int_as_float(0x7FC00000), log2f(magnitude), __int_as_float(many));
@@ -699,57 +700,45 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                 const SharedItem &it = take();
                 if (!ok || it.rows == 0) break;
                 const int from = it.from, to = it.to;
-                if (lane == 0) {
-                    // the scores of tile i: their place is free when the products with the weights two tiles earlier are done
-                    auto score = [&](int i) {
-                        if (!(wait(bars, &bars->k_full, i & 1, status) && (i < 2 || wait(bars, &bars->summed[i & 1], (i / 2 - 1) & 1, status)))) return false;
-                        fence_after();
-                        const uint32_t to_scores = tmem + (i & 1) * kPos;
-                        bool add = false;
+                // the scores of tile i: their place is free when the products with the weights two tiles earlier are done
+                auto score = [&](int i) {
+                    const int stage = i % C::kTiles;
+                    ok = wait<0>(bars, &bars->k_full[stage], i / C::kTiles & 1, status) && (i < 2 || wait_tile(at_once, bars->summed, i - 2));
+                    if (!ok) return;
+                    fence_after();
+                    const uint32_t to_scores = tmem + (i & 1) * kPos, keys = k_at + stage * C::kTile;
 #pragma unroll
-                        for (int part = PARTS - 1; part >= 0; --part)
-#pragma unroll
-                            for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    mma_smem(to_scores, operand(q_at + part * C::kQPart + b * (kSharedRows * 128) + k * 32, 16), operand(k_at + b * (kPos * 128) + k * 32, 16),
-                                             C::kScores, add);
-                                    add = true;
-                                }
-                        commit(&bars->scored[i & 1]);
-                        return true;
-                    };
-                    ok = wait(bars, &bars->q_full, items & 1, status);
-                    // the next tile's scores are taken beside the rows' work on this one
-#pragma unroll 1
-                    for (int u = from - 1; ok && u < to; ++u) {
-                        if (u + 1 < to) ok = score(n + (u < from ? 0 : 1));
-                        if (!ok || u < from) continue;
-                        const int stage = n % C::kValueTiles;
-                        ok = wait(bars, &bars->v_full[stage], n / C::kValueTiles & 1, status) && wait(bars, &bars->weighed[n & 1], n / 2 & 1, status);
-                        if (!ok) break;
-                        fence_after();
-                        const uint32_t values = v_at + stage * C::kTile, weights = tmem + (n & 1) * kPos;
-                        bool add = u > from;
-#pragma unroll
-                        for (int k = 0; k < kPos / 16; ++k)
-#pragma unroll
-                            for (int part = 1; part >= 0; --part) {  // small parts first
-                                mma_tmem(sums, weights + k * 16 + part * 8, operand(values + k * 2048, kPos * 128), C::kSums, add);
-                                add = true;
-                            }
-                        commit(&bars->summed[n & 1]);
-                        ++n;
+                    for (int j = 0; j < PARTS * kBlocks * 4; ++j) {
+                        const int part = PARTS - 1 - j / (kBlocks * 4), b = j / 4 % kBlocks, k = j % 4;
+                        mma_smem(to_scores, operand(q_at + part * C::kQPart + b * (kSharedRows * 128) + k * 32, 16), operand(keys + b * (kPos * 128) + k * 32, 16),
+                                 C::kScores, j > 0, leader);
                     }
+                    commit(&bars->scored[i & 1], leader);
+                };
+                ok = wait<0>(bars, &bars->q_full, items & 1, status);
+                if (ok) score(n);
+#pragma unroll 1
+                for (int u = from; ok && u < to; ++u, ++n) {
+                    if (u + 1 < to) score(n + 1);  // the next tile's, beside the rows' work on this one
+                    const int stage = n % C::kTiles;
+                    ok = ok && wait<0>(bars, &bars->v_full[stage], n / C::kTiles & 1, status) && wait_tile(at_once, bars->weighed, n);
+                    if (!ok) break;
+                    fence_after();
+                    const uint32_t values = v_at + stage * C::kTile, weights = tmem + (n & 1) * kPos;
+#pragma unroll
+                    for (int k = 0; k < kPos / 16; ++k) {  // small parts first
+                        mma_tmem(sums, weights + k * 16 + 8, operand(values + k * 2048, kPos * 128), C::kSums, k > 0 || u > from, leader);
+                        mma_tmem(sums, weights + k * 16, operand(values + k * 2048, kPos * 128), C::kSums, true, leader);
+                    }
+                    commit(&bars->summed[n & 1], leader);
                 }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) break;
                 done();
             }
         }
-        if (warp == kProductWarp && lane == 0) {
+        if (warp == kProductWarp) {
             // no product may still read shared memory or write tensor memory when the block frees them
-            commit(&bars->drained);
+            commit(&bars->drained, leader);
             (void)mbar_wait(&bars->drained, 0);
         }
         __syncwarp();
