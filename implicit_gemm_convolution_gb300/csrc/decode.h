@@ -173,7 +173,7 @@ struct SharedProblem {
     int64_t seqs, tokens, q_heads, groups;
     Heads q;
     int dtype, group;  // group: query heads of a key head
-    bool q_fours;
+    bool q_sixteens;  // queries can be copied in 16 bytes
     const int32_t *prefix_table;
     int64_t prefix_width;
     const int32_t *prefix_len, *group_at, *cu;

@@ -442,7 +442,7 @@ int om_kv_shared_attention(const om_kv_cache *cache, int64_t groups, const int32
     p.q = hq;
     p.dtype = dtype;
     p.group = static_cast<int>(group);
-    p.q_fours = aligned(q, 4 * eb) && q_ts % 4 == 0 && q_hs % 4 == 0;
+    p.q_sixteens = aligned(q, 16) && q_ts * eb % 16 == 0 && q_hs * eb % 16 == 0;
     p.prefix_table = prefix_table; p.prefix_width = prefix_width; p.prefix_len = prefix_len; p.group_at = group_offsets; p.cu = cu;
     p.scale = scale;
     p.blocks = blocks;

@@ -112,19 +112,17 @@ __device__ __forceinline__ void tmem_loaded(uint32_t (&r)[16]) {
                  : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]),
                    "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
 }
-// work(g, columns) for each group of 16 columns from `at` on, the next group on its way meanwhile.
+// work(g, columns of g, columns of g + 1) for each two groups of 16 columns from `at` on.
 template <int GROUPS, typename F>
 __device__ __forceinline__ void for_groups(uint32_t at, F work) {
-    uint32_t a[16], b[16];
-    tmem_load(at, a);
 #pragma unroll 1
     for (int g = 0; g < GROUPS; g += 2) {
-        tmem_loaded(a);
+        uint32_t a[16], b[16];
+        tmem_load(at + g * 16, a);
         tmem_load(at + g * 16 + 16, b);
-        work(g, a);
+        tmem_loaded(a);
         tmem_loaded(b);
-        if (g + 2 < GROUPS) tmem_load(at + g * 16 + 32, a);
-        work(g + 1, b);
+        work(g, a, b);
     }
 }
 __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[16]) {
@@ -189,7 +187,7 @@ struct TileScales {
 // Barriers of what there are two of (tiles by their number's parity, items) belong to one of them: a wait for a phase never
 // meets the phase after the next.
 struct Bars {
-    uint64_t q_full, k_full[2], v_full[2], scaled[2], scored[2], weighed[2], summed[2], drained;
+    uint64_t q_full, k_full[2], scored[2], weighed[2], summed[2], drained;
     uint64_t item_full[2], item_free[2];
     SharedItem item[2];  // rows 0: there are no more
     TileScales scales[2];
@@ -241,32 +239,6 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t *at, bool there) {
     return x;
 }
 
-// A row's queries in a lane, two 16-bit elements or one of 32 bits a word; zeros where there is no row.
-template <int WORDS>
-__device__ __forceinline__ void load_query(const SharedProblem &p, int64_t at, bool live, uint32_t (&w)[WORDS]) {
-    constexpr int kEach = 4;  // bytes of a word
-    const int bytes = p.dtype == OM_F32 ? 4 : 2;
-    const uint8_t *const from = static_cast<const uint8_t *>(p.q.p) + at * bytes;
-#pragma unroll
-    for (int i = 0; i < WORDS; ++i) w[i] = 0;
-    if (!live) return;
-    if (p.q_fours) {
-        // eight bytes at least are aligned
-#pragma unroll
-        for (int i = 0; i < WORDS; i += 2) {
-            const uint2 x = *reinterpret_cast<const uint2 *>(from + i * kEach);
-            w[i] = x.x;
-            w[i + 1] = x.y;
-        }
-    } else if (bytes == 4) {
-#pragma unroll
-        for (int i = 0; i < WORDS; ++i) w[i] = reinterpret_cast<const uint32_t *>(from)[i];
-    } else {
-#pragma unroll
-        for (int i = 0; i < WORDS; ++i) w[i] = reinterpret_cast<const uint16_t *>(from)[2 * i] | static_cast<uint32_t>(reinterpret_cast<const uint16_t *>(from)[2 * i + 1]) << 16;
-    }
-}
-
 template <int KV, int DIM, int PARTS>
 __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel(const __grid_constant__ SharedProblem p) {
     using C = Config<DIM, PARTS>;
@@ -283,10 +255,8 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
         mbar_init(&bars->drained, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bars->k_full[i], kCopyWarps);
-            mbar_init(&bars->v_full[i], kCopyWarps);
-            mbar_init(&bars->scaled[i], 1);
-            mbar_init(&bars->scored[i], 1);
-            mbar_init(&bars->weighed[i], kRowWarps);
+            mbar_init(&bars->scored[i], 2);  // by the products, and by the warp that lays out the scales
+            mbar_init(&bars->weighed[i], kRowWarps + kCopyWarps);  // by the weights' rows, and by the copies of the values
             mbar_init(&bars->summed[i], 1);
             mbar_init(&bars->item_full[i], 1);
             mbar_init(&bars->item_free[i], kRowWarps + 2 * kCopyWarps + 2);
@@ -336,62 +306,85 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
         for (;;) {
             const SharedItem &it = take();
             if (!ok || it.rows == 0) break;
-            // queries: 16 lanes a row, two rows at a time, scaled by a power of two; eight rows' loads are on their way together
-            constexpr int kEach = DIM / 16, kWords = PARTS == 2 ? kEach : kEach / 2;
-            float factor = 0.0f;
-            const int half = lane / 16, q_d = lane % 16 * kEach;
+            // queries: raw to where their 16-bit floats will be (32-bit ones: four elements where the first parts of eight go, four where the
+            // second parts go), then each lane scales its row by a power of two, in place
+            constexpr int kElements = PARTS == 2 ? 4 : 8, kRaw = DIM / kElements;  // of 16 bytes; 16-byte chunks of a row
+            const int bytes = PARTS == 2 ? 4 : 2, live = it.rows - warp * 32;
+            auto chunk_at = [&](int r, int c) { return static_cast<uint32_t>(c / 8 * (kSharedRows * 128) + (warp * 32 + r) * 128 + ((c % 8 ^ (r & 7)) * 16)); };
+            {
+                const int R = it.row0 + row, token = R / p.group;
+                const int64_t mine = (it.t0 + token) * p.q.ts + (static_cast<int64_t>(it.h) * p.group + R - token * p.group) * p.q.hs;
 #pragma unroll 1
-            for (int i0 = 0; i0 < 16; i0 += 4) {
-                uint32_t w[4][kWords];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = warp * 32 + 2 * (i0 + j) + half, R = it.row0 + r;
-                    const int64_t at = (it.t0 + R / p.group) * p.q.ts + (static_cast<int64_t>(it.h) * p.group + R % p.group) * p.q.hs + q_d;
-                    load_query<kWords>(p, at, r < it.rows, w[j]);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int i = i0 + j, r = warp * 32 + 2 * i + half;
-                    float v[kEach];
-#pragma unroll
-                    for (int e = 0; e < kWords; ++e) {
-                        if constexpr (PARTS == 2) {
-                            v[e] = __uint_as_float(w[j][e]);
-                        } else {
-                            const float2 f = p.dtype == OM_F16 ? unpack_half(w[j][e]) : make_float2(__uint_as_float(w[j][e] << 16), __uint_as_float(w[j][e] & 0xffff0000u));
-                            v[2 * e] = f.x;
-                            v[2 * e + 1] = f.y;
+                for (int i = lane; i < 32 * kRaw; i += 32) {
+                    const int r = i / kRaw, k = i % kRaw;
+                    const uint8_t *const from = static_cast<const uint8_t *>(p.q.p) + (__shfl_sync(0xffffffffu, mine, r) + k * kElements) * bytes;
+                    const uint32_t to = q_at + (PARTS == 2 ? k % 2 * C::kQPart + chunk_at(r, k / 2) : chunk_at(r, k));
+                    if (p.q_sixteens) {
+                        cp_async_16(to, r < live ? from : static_cast<const uint8_t *>(p.q.p), r < live ? 16 : 0);
+                    } else {
+#pragma unroll 1
+                        for (int e = 0; e < kElements; ++e) {
+                            if constexpr (PARTS == 2)
+                                *reinterpret_cast<uint32_t *>(smem + (to - q_at) + 4 * e) = r < live ? reinterpret_cast<const uint32_t *>(from)[e] : 0;
+                            else
+                                *reinterpret_cast<uint16_t *>(smem + (to - q_at) + 2 * e) = r < live ? reinterpret_cast<const uint16_t *>(from)[e] : 0;
                         }
                     }
-                    unsigned top = 0;
+                }
+                cp_async_wait_all();
+                __syncwarp();
+            }
+            // eight elements of the lane's row
+            auto eight = [&](int c, float (&v)[8]) {
+                const uint4 a = *reinterpret_cast<const uint4 *>(smem + chunk_at(lane, c));
+                const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+                if constexpr (PARTS == 2) {
+                    const uint4 b = *reinterpret_cast<const uint4 *>(smem + C::kQPart + chunk_at(lane, c));
+                    const uint32_t z[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-                    for (int e = 0; e < kEach; ++e) top = max(top, __float_as_uint(v[e]) & 0x7fffffffu);
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] = __uint_as_float(w[e]);
+                        v[4 + e] = __uint_as_float(z[e]);
+                    }
+                } else {
 #pragma unroll
-                    for (int x = 1; x < 16; x <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, x));
-                    // the row's largest element to [2^13, 2^14)
-                    int e2 = static_cast<int>(top >> 23) - 127;
-                    e2 = e2 < -100 ? -100 : e2;
-                    const float up = power_of_two(13 - e2);
-                    const float f = __shfl_sync(0xffffffffu, __fmul_rn(power_of_two(e2 - 13), __fmul_rn(p.scale, kLog2e)), (lane & 1) * 16);
-                    if (lane / 2 == i) factor = f;
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 f = p.dtype == OM_F16 ? unpack_half(w[e]) : make_float2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xffff0000u));
+                        v[2 * e] = f.x;
+                        v[2 * e + 1] = f.y;
+                    }
+                }
+            };
+            unsigned most = 0;
+#pragma unroll 1
+            for (int c = 0; c < DIM / 8; ++c) {
+                float v[8];
+                eight(c, v);
 #pragma unroll
-                    for (int e = 0; e < kEach; ++e) v[e] = __fmul_rn(v[e], up);
+                for (int e = 0; e < 8; ++e) most = max(most, __float_as_uint(v[e]) & 0x7fffffffu);
+            }
+            // the row's largest element to [2^13, 2^14)
+            const int e2 = max(static_cast<int>(most >> 23) - 127, -100);
+            const float up = power_of_two(13 - e2), factor = __fmul_rn(power_of_two(e2 - 13), __fmul_rn(p.scale, kLog2e));
+#pragma unroll 1
+            for (int c = 0; c < DIM / 8; ++c) {
+                float v[8];
+                eight(c, v);
+                uint32_t x[4];
 #pragma unroll
-                    for (int part = 0; part < PARTS; ++part)
+                for (int e = 0; e < 4; ++e) {
+                    v[2 * e] = __fmul_rn(v[2 * e], up);
+                    v[2 * e + 1] = __fmul_rn(v[2 * e + 1], up);
+                    x[e] = pack_half(v[2 * e], v[2 * e + 1]);
+                }
+                *reinterpret_cast<uint4 *>(smem + chunk_at(lane, c)) = make_uint4(x[0], x[1], x[2], x[3]);
+                if constexpr (PARTS == 2) {
 #pragma unroll
-                        for (int e = 0; e < kEach; e += 4) {
-                            const int d = q_d + e;
-                            const uint2 x = make_uint2(pack_half(v[e], v[e + 1]), pack_half(v[e + 2], v[e + 3]));
-                            uint8_t *const to = smem + part * C::kQPart + d / 64 * (kSharedRows * 128) + r * 128 + ((d % 64 / 8 ^ (r & 7)) * 16) + d % 8 * 2;
-                            *reinterpret_cast<uint2 *>(to) = x;
-                            if (part + 1 < PARTS) {
-                                const float2 y = unpack_half(x.x), z = unpack_half(x.y);
-                                v[e] -= y.x;
-                                v[e + 1] -= y.y;
-                                v[e + 2] -= z.x;
-                                v[e + 3] -= z.y;
-                            }
-                        }
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 y = unpack_half(x[e]);
+                        x[e] = pack_half(__fsub_rn(v[2 * e], y.x), __fsub_rn(v[2 * e + 1], y.y));
+                    }
+                    *reinterpret_cast<uint4 *>(smem + C::kQPart + chunk_at(lane, c)) = make_uint4(x[0], x[1], x[2], x[3]);
                 }
             }
             fence_proxy_async_smem();
@@ -404,7 +397,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
             for (int u = from; u < to; ++u, ++n) {
                 const uint32_t scores = tmem + lanes + (n & 1) * kPos;
                 const float4 *const groups = bars->scales[n & 1].group;
-                ok = wait_tile(at_once, bars->scaled, n) && wait_tile(at_once, bars->scored, n);
+                ok = wait_tile(at_once, bars->scored, n);
                 if (!ok) break;
                 fence_after();
                 const bool plain = bars->scales[n & 1].plain;
@@ -415,30 +408,42 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                     heavy = fmaxf(heavy, __fadd_rn(x, log_scale));
                 };
                 if (plain) {
-                    for_groups<kGroups>(scores, [&](int g, const uint32_t (&s)[16]) {
-                        const float4 of = groups[g];
-                        float hi = max3(__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2])), lo = max3(__uint_as_float(s[3]), __uint_as_float(s[4]), __uint_as_float(s[5]));
+                    for_groups<kGroups>(scores, [&](int g, const uint32_t (&a)[16], const uint32_t (&b)[16]) {
+                        const float4 of_a = groups[g], of_b = groups[g + 1];
+                        float hi[2], lo[2];
+                        auto at = [](const uint32_t (&s)[16], int i) { return __uint_as_float(s[i]); };
+                        hi[0] = max3(at(a, 0), at(a, 1), at(a, 2));
+                        lo[0] = max3(at(a, 3), at(a, 4), at(a, 5));
+                        hi[1] = max3(at(b, 0), at(b, 1), at(b, 2));
+                        lo[1] = max3(at(b, 3), at(b, 4), at(b, 5));
 #pragma unroll
                         for (int i = 6; i < 14; i += 4) {
-                            hi = max3(hi, __uint_as_float(s[i]), __uint_as_float(s[i + 1]));
-                            lo = max3(lo, __uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
+                            hi[0] = max3(hi[0], at(a, i), at(a, i + 1));
+                            lo[0] = max3(lo[0], at(a, i + 2), at(a, i + 3));
+                            hi[1] = max3(hi[1], at(b, i), at(b, i + 1));
+                            lo[1] = max3(lo[1], at(b, i + 2), at(b, i + 3));
                         }
-                        hi = max3(hi, __uint_as_float(s[14]), __uint_as_float(s[15]));
-                        note(__fmul_rn(fmaxf(hi, lo), __fmul_rn(of.x, factor)), of.z);
+                        note(__fmul_rn(max3(hi[0], lo[0], fmaxf(at(a, 14), at(a, 15))), __fmul_rn(of_a.x, factor)), of_a.z);
+                        note(__fmul_rn(max3(hi[1], lo[1], fmaxf(at(b, 14), at(b, 15))), __fmul_rn(of_b.x, factor)), of_b.z);
                     });
                 } else {
-                    for_groups<kGroups>(scores, [&](int g, const uint32_t (&s)[16]) {
-                        const float4 of = groups[g];
-                        const float kf = __fmul_rn(of.x, factor);
-                        const int many = __float_as_int(of.w);
-                        float hi = -INFINITY, lo = INFINITY;
+                    for_groups<kGroups>(scores, [&](int g, const uint32_t (&a)[16], const uint32_t (&b)[16]) {
+#pragma unroll 1
+                        for (int h = 0; h < 2; ++h) {
+                            const float4 of = groups[g + h];
+                            const float kf = __fmul_rn(of.x, factor);
+                            const int many = __float_as_int(of.w);
+                            float hi = -INFINITY, lo = INFINITY;
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (i < many) {
-                                hi = fmaxf(hi, __uint_as_float(s[i]));
-                                lo = fminf(lo, __uint_as_float(s[i]));
+                            for (int i = 0; i < 16; ++i) {
+                                const float s = __uint_as_float(h == 0 ? a[i] : b[i]);
+                                if (i < many) {
+                                    hi = fmaxf(hi, s);
+                                    lo = fminf(lo, s);
+                                }
                             }
-                        if (hi >= lo) note(__fmul_rn(kf >= 0.0f ? hi : lo, kf), of.z);
+                            if (hi >= lo) note(__fmul_rn(kf >= 0.0f ? hi : lo, kf), of.z);
+                        }
                     });
                 }
                 // does the tile fit the row's maximum and unit
@@ -496,40 +501,51 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                     less = m - kBias;
                 }
                 // weights: their parts take the scores' place, for 16 positions eight columns of the first and eight of the second
-                float2 tile_sum = make_float2(0.0f, 0.0f);
+                float2 tile_sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
                 auto weigh = [&](auto every) {
-                    for_groups<kGroups>(scores, [&](int g, const uint32_t (&s)[16]) {
-                        const float4 of = groups[g];
-                        const float kf = __fmul_rn(of.x, factor), vf = of.y == of.y ? in_units(of.y, per_unit) : of.y;
-                        const int many = every.value ? 16 : __float_as_int(of.w);
-                        uint32_t w[16];
+                    for_groups<kGroups>(scores, [&](int g, const uint32_t (&a)[16], const uint32_t (&b)[16]) {
+                        const float4 of[2] = {groups[g], groups[g + 1]};
+                        float2 kf[2], vf[2];
 #pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const float2 x = fma2_rn(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), make_float2(kf, kf), make_float2(-less, -less));
-                            float2 e = make_float2(ex2(x.x), ex2(x.y));
-                            if (!every.value) {
-                                if (i >= many) e.x = 0.0f;
-                                if (i + 1 >= many) e.y = 0.0f;
-                            }
-                            tile_sum = add2_rn(tile_sum, e);
-                            float2 a = mul2_rn(e, make_float2(vf, vf));
-                            if (!every.value) {  // a scale that is not finite does not count where nothing is seen
-                                if (i >= many) a.x = 0.0f;
-                                if (i + 1 >= many) a.y = 0.0f;
-                            }
-                            w[i / 2] = pack_half(a.x, a.y);
-                            const float2 y = unpack_half(w[i / 2]);
-                            a = add2_rn(a, make_float2(-y.x, -y.y));
-                            w[8 + i / 2] = pack_half(a.x, a.y);
+                        for (int h = 0; h < 2; ++h) {
+                            const float k = __fmul_rn(of[h].x, factor), v = of[h].y == of[h].y ? in_units(of[h].y, per_unit) : of[h].y;
+                            kf[h] = make_float2(k, k);
+                            vf[h] = make_float2(v, v);
                         }
-                        tmem_store(scores + g * 16, w);
+                        uint32_t w[2][16];
+                        // the groups side by side: two chains of operations for every pair
+#pragma unroll
+                        for (int i = 0; i < 16; i += 2)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint32_t s0 = h == 0 ? a[i] : b[i], s1 = h == 0 ? a[i + 1] : b[i + 1];
+                                const float2 x = fma2_rn(make_float2(__uint_as_float(s0), __uint_as_float(s1)), kf[h], make_float2(-less, -less));
+                                float2 e = make_float2(ex2(x.x), ex2(x.y));
+                                const int many = every.value ? 16 : __float_as_int(of[h].w);
+                                if (!every.value) {
+                                    if (i >= many) e.x = 0.0f;
+                                    if (i + 1 >= many) e.y = 0.0f;
+                                }
+                                tile_sum[h] = add2_rn(tile_sum[h], e);
+                                float2 y = mul2_rn(e, vf[h]);
+                                if (!every.value) {  // a scale that is not finite does not count where nothing is seen
+                                    if (i >= many) y.x = 0.0f;
+                                    if (i + 1 >= many) y.y = 0.0f;
+                                }
+                                w[h][i / 2] = pack_half(y.x, y.y);
+                                const float2 z = unpack_half(w[h][i / 2]);
+                                y = add2_rn(y, make_float2(-z.x, -z.y));
+                                w[h][8 + i / 2] = pack_half(y.x, y.y);
+                            }
+                        tmem_store(scores + g * 16, w[0]);
+                        tmem_store(scores + g * 16 + 16, w[1]);
                     });
                 };
                 if (plain)
                     weigh(std::true_type{});
                 else
                     weigh(std::false_type{});
-                l = __fadd_rn(l, __fadd_rn(tile_sum.x, tile_sum.y));
+                l = __fadd_rn(l, __fadd_rn(__fadd_rn(tile_sum[0].x, tile_sum[0].y), __fadd_rn(tile_sum[1].x, tile_sum[1].y)));
                 tmem_stored();
                 fence_before();
                 __syncwarp();
@@ -633,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                 ok = last < 0 || wait_tile(ahead, values ? bars->summed : bars->scored, last);
                 if (!ok) break;
                 store(smem + C::kQBytes + ((values ? C::kTiles : 0) + stage) * C::kTile, x);
-                if (lane == 0) mbar_arrive(values ? &bars->v_full[stage] : &bars->k_full[stage]);
+                if (lane == 0) mbar_arrive(values ? &bars->weighed[n & 1] : &bars->k_full[stage]);
                 if (u + 1 < to) load(codes, (u + 1) * kPos, ids, x);
                 ids = page_of((u + 2) * kPos);
             }
@@ -688,7 +704,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                         s.plain = plain;
                     }
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->scaled[n & 1]);
+                    if (lane == 0) mbar_arrive(&bars->scored[n & 1]);
                     id = id_next;
                 }
                 if (!ok) break;
@@ -700,10 +716,11 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                 const SharedItem &it = take();
                 if (!ok || it.rows == 0) break;
                 const int from = it.from, to = it.to;
-                // the scores of tile i: their place is free when the products with the weights two tiles earlier are done
+                // the scores of tile i. They take the place of weights whose products were issued before: products are executed in
+                // their order
                 auto score = [&](int i) {
                     const int stage = i % C::kTiles;
-                    ok = wait<0>(bars, &bars->k_full[stage], i / C::kTiles & 1, status) && (i < 2 || wait_tile(at_once, bars->summed, i - 2));
+                    ok = wait<0>(bars, &bars->k_full[stage], i / C::kTiles & 1, status);
                     if (!ok) return;
                     fence_after();
                     const uint32_t to_scores = tmem + (i & 1) * kPos, keys = k_at + stage * C::kTile;
@@ -721,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                 for (int u = from; ok && u < to; ++u, ++n) {
                     if (u + 1 < to) score(n + 1);  // the next tile's, beside the rows' work on this one
                     const int stage = n % C::kTiles;
-                    ok = ok && wait<0>(bars, &bars->v_full[stage], n / C::kTiles & 1, status) && wait_tile(at_once, bars->weighed, n);
+                    ok = ok && wait_tile(at_once, bars->weighed, n);
                     if (!ok) break;
                     fence_after();
                     const uint32_t values = v_at + stage * C::kTile, weights = tmem + (n & 1) * kPos;

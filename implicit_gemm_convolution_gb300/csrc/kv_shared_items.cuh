@@ -18,27 +18,30 @@ struct SharedGroup {
 __device__ __forceinline__ SharedGroup shared_group(const SharedProblem &p, int64_t j) {
     SharedGroup g{};
     if (j >= p.groups) return g;
-    const int64_t a = min(max(static_cast<int64_t>(p.group_at[j]), static_cast<int64_t>(0)), p.seqs);
-    const int64_t b = min(max(static_cast<int64_t>(p.group_at[j + 1]), a), p.seqs);
-    const int64_t lo = min(max(static_cast<int64_t>(p.cu[a]), static_cast<int64_t>(0)), p.tokens);
-    const int64_t hi = min(max(static_cast<int64_t>(p.cu[b]), lo), p.tokens);
-    g.t0 = static_cast<int>(lo);
-    g.rows = static_cast<int>((hi - lo) * p.group);
+    const int seqs = static_cast<int>(p.seqs), tokens = static_cast<int>(p.tokens);
+    const int len = p.prefix_len[j], a = min(max(p.group_at[j], 0), seqs), b = min(max(p.group_at[j + 1], a), seqs);
+    const int lo = min(max(p.cu[a], 0), tokens), hi = min(max(p.cu[b], lo), tokens);
+    g.t0 = lo;
+    g.rows = (hi - lo) * p.group;
     g.row_blocks = (g.rows + kSharedRows - 1) / kSharedRows;
-    g.len = static_cast<int>(min(max(static_cast<int64_t>(p.prefix_len[j]), static_cast<int64_t>(0)), p.prefix_width * p.c.page));
+    g.len = min(max(len, 0), static_cast<int>(p.prefix_width * p.c.page));
     g.units = (g.len + kSharedTile - 1) / kSharedTile;
-    g.n = p.c.heads * g.row_blocks * static_cast<int64_t>(g.units);
+    g.n = static_cast<int64_t>(static_cast<int>(p.c.heads) * g.row_blocks) * g.units;
     return g;
 }
 
-// Units of all groups, 0 where they pass 32 bits (offsets that decrease count tokens twice; others the host has bounded). find: the
-// group with token `t` and the units before it, -1 for none.
-__device__ __forceinline__ int shared_units(const SharedProblem &p) {
-    int64_t total = 0;
+// Units of all groups, 0 where they pass 32 bits (offsets that decrease count tokens twice; others the host has bounded). mine: the
+// group of the lane's number.
+__device__ __forceinline__ int shared_units(const SharedProblem &p, const SharedGroup &mine) {
+    int64_t total = mine.n;
 #pragma unroll 1
-    for (int64_t j = threadIdx.x & 31; j < p.groups; j += 32) total += shared_group(p, j).n;
+    for (int64_t j = 32 + (threadIdx.x & 31); j < p.groups; j += 32) total += shared_group(p, j).n;
+    if (p.groups > 1) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    } else {
+        total = __shfl_sync(0xffffffffu, total, 0);
+    }
     return total > INT_MAX - (1 << 20) ? 0 : static_cast<int>(total);
 }
 __device__ __forceinline__ int shared_per_block(const SharedProblem &p, int total) {
@@ -58,31 +61,40 @@ struct SharedItems {
     int u, begin, stop, before, j;
 
     __device__ __forceinline__ void start(const SharedProblem &p, int block) {
-        const int total = shared_units(p), per = shared_per_block(p, total), lane = threadIdx.x & 31;
-        begin = u = static_cast<int>(min(static_cast<int64_t>(block) * per, static_cast<int64_t>(total)));
+        const int lane = threadIdx.x & 31;
+        // up to 32 groups are looked up once, a lane each
+        const SharedGroup mine = shared_group(p, lane);
+        const int total = shared_units(p, mine), per = shared_per_block(p, total);
+        begin = u = block >= (total + per - 1) / per ? total : block * per;
         stop = min(total - u, per) + u;
         before = j = 0;
         g = SharedGroup{};
         if (u >= stop) return;
 #pragma unroll 1
         for (int64_t base = 0; base < p.groups; base += 32) {
-            const int n = static_cast<int>(shared_group(p, base + lane).n);
+            const SharedGroup here = base == 0 ? mine : shared_group(p, base + lane);
+            const int n = static_cast<int>(here.n);
             int up = n;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int x = __shfl_up_sync(0xffffffffu, up, o);
                 if (lane >= o) up += x;
             }
-            const unsigned here = __ballot_sync(0xffffffffu, u < before + up);
-            if (here != 0) {
-                const int at = __ffs(here) - 1;
+            const unsigned found = __ballot_sync(0xffffffffu, u < before + up);
+            if (found != 0) {
+                const int at = __ffs(found) - 1;
                 before += __shfl_sync(0xffffffffu, up - n, at);
                 j = static_cast<int>(base) + at;
+                g.t0 = __shfl_sync(0xffffffffu, here.t0, at);
+                g.rows = __shfl_sync(0xffffffffu, here.rows, at);
+                g.row_blocks = __shfl_sync(0xffffffffu, here.row_blocks, at);
+                g.len = __shfl_sync(0xffffffffu, here.len, at);
+                g.units = __shfl_sync(0xffffffffu, here.units, at);
+                g.n = __shfl_sync(0xffffffffu, n, at);
                 break;
             }
             before += __shfl_sync(0xffffffffu, up, 31);
         }
-        g = shared_group(p, j);
     }
     // The next part; false behind the last.
     __device__ __forceinline__ bool next(const SharedProblem &p, SharedItem *item) {

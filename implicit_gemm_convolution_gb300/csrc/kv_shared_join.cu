@@ -27,23 +27,48 @@ __device__ __forceinline__ float ex2(float x) {
 // Without a maximum a part saw nothing (its sum is 0) or scores that are all NaN (its sum is NaN, and stays).
 __device__ __forceinline__ float joined(float sum, float top, float best) { return top == -INFINITY ? sum : __fmul_rn(sum, ex2(top - best)); }
 
+template <int N>
+__device__ __forceinline__ void load_values(const float *from, float (&v)[N]) {
+    if constexpr (N == 2) {
+        const float2 x = __ldcg(reinterpret_cast<const float2 *>(from));
+        v[0] = x.x;
+        v[1] = x.y;
+    } else {
+#pragma unroll
+        for (int e = 0; e < N; e += 4) {
+            const float4 x = __ldcg(reinterpret_cast<const float4 *>(from + e));
+            v[e] = x.x;
+            v[e + 1] = x.y;
+            v[e + 2] = x.z;
+            v[e + 3] = x.w;
+        }
+    }
+}
+
 template <typename T, int DIM, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads) kv_shared_join_kernel(const __grid_constant__ SharedProblem p) {
     constexpr int kEach = DIM / 32;
     const int lane = threadIdx.x & 31;
-    const int64_t row = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + threadIdx.x / 32;
+    const int row = blockIdx.x * (kThreads / 32) + threadIdx.x / 32, heads = static_cast<int>(p.q_heads);
     wait_for_earlier();
-    if (row >= p.tokens * p.q_heads) return;
-    const int t = static_cast<int>(row / p.q_heads), head = static_cast<int>(row - t * p.q_heads);
-    if (t < p.cu[0] || t >= p.cu[p.seqs]) return;  // no sequence's
+    if (row >= static_cast<int>(p.tokens) * heads) return;
+    const int t = row / heads, head = row - t * heads;
+    // what does not depend on anything is asked for first
+    const float2 own = __ldcg(p.own_state + row);
+    float o[kEach];
+    load_values(p.own + static_cast<int64_t>(row) * DIM + lane * kEach, o);
+    const int t_first = p.cu[0], t_last = p.cu[p.seqs];
     // the row's group, and the units before it
-    int total = shared_units(p), count = 0, first = 0, at = 0;
+    const SharedGroup mine_first = shared_group(p, lane);
+    const int total = shared_units(p, mine_first);
+    if (t < t_first || t >= t_last) return;  // no sequence's
+    int count = 0, first = 0, at = 0;
     if (total > 0) {
         const int per = shared_per_block(p, total);
         int before = 0;
 #pragma unroll 1
         for (int64_t base = 0; base < p.groups; base += 32) {
-            const SharedGroup g = shared_group(p, base + lane);
+            const SharedGroup g = base == 0 ? mine_first : shared_group(p, base + lane);
             const int n = static_cast<int>(g.n);
             int up = n;
 #pragma unroll
@@ -70,13 +95,9 @@ __global__ void __launch_bounds__(kThreads) kv_shared_join_kernel(const __grid_c
     }
     // part j of the prefix; an item that one block had is at its row's place
     const bool whole = count == 1;
-    auto place = [&](int j) -> int64_t { return whole ? row : static_cast<int64_t>(j == 0 ? first : (first | 1) - 1 + 2 * j) * p.slot_rows + at; };
+    auto place = [&](int j) -> int64_t { return whole ? static_cast<int64_t>(row) : static_cast<int64_t>(j == 0 ? first : (first | 1) - 1 + 2 * j) * p.slot_rows + at; };
     const float2 *const states = whole ? p.whole_state : p.slot_state;
     const float *const values = whole ? p.whole : p.slots;
-    const float2 own = __ldcg(p.own_state + row);
-    float o[kEach];
-#pragma unroll
-    for (int e = 0; e < kEach; ++e) o[e] = __ldcg(p.own + row * DIM + lane * kEach + e);
     float best = own.x;
     float2 mine = make_float2(-INFINITY, 0.0f);
 #pragma unroll 1
@@ -102,21 +123,7 @@ __global__ void __launch_bounds__(kThreads) kv_shared_join_kernel(const __grid_c
             float y[kAhead][kEach];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
-                const float *const from = values + place(min(base + j0 + j, count - 1)) * DIM + lane * kEach;
-                if constexpr (kEach == 2) {
-                    const float2 v = __ldcg(reinterpret_cast<const float2 *>(from));
-                    y[j][0] = v.x;
-                    y[j][1] = v.y;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < kEach; e += 4) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(from + e));
-                        y[j][e] = v.x;
-                        y[j][e + 1] = v.y;
-                        y[j][e + 2] = v.z;
-                        y[j][e + 3] = v.w;
-                    }
-                }
+                load_values(values + place(min(base + j0 + j, count - 1)) * DIM + lane * kEach, y[j]);
             }
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
