@@ -58,7 +58,6 @@ constexpr int kTile = 16;              // positions of a warp's step
 constexpr int kUnit = kTile * kWarps;  // positions of a unit of work
 constexpr int kMinUnits = 4;           // a block takes at least so many units
 constexpr int kWholeUnits = 12;        // items of no more units are not split: joining parts takes longer than that many units
-constexpr int kWholePartUnits = 4;
 constexpr float kLog2e = 1.4426950408889634f;
 // A tile's largest weight is 2^8 as its unit is set, and may go to 2^15 and 2^-1 with the same one: inside 16-bit
 // range, its second part above the subnormals. The maximum may lag behind while exponentials are below 2^40.
@@ -345,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, BLOCKS) kv_attention_kernel(const __
         doubts |= scan_doubt[w];
     }
     if (doubts == 3) return;
-    const bool split = p.workspace != nullptr && longest > (FORM == kPartForm ? kWholePartUnits : kWholeUnits);
+    const bool split = p.workspace != nullptr && longest > kWholeUnits;
     const int per = max((total + static_cast<int>(gridDim.x) - 1) / static_cast<int>(gridDim.x), kMinUnits);
     if (static_cast<int64_t>(blockIdx.x) * per >= total) return;
     const int u0 = blockIdx.x * per, u1 = min(u0 + per, total);

@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
         return bars->item[items & 1];
     };
     constexpr std::integral_constant<int, 0> at_once{};
-    constexpr std::integral_constant<int, 100> ahead{};
+    constexpr std::integral_constant<int, 400> ahead{};
     auto done = [&]() {
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars->item_free[items & 1]);
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                                 }
                                 w[h][i / 2] = pack_half(y.x, y.y);
                                 const float2 z = unpack_half(w[h][i / 2]);
-                                y = add2_rn(y, make_float2(-z.x, -z.y));
+                                y = fma2_rn(z, make_float2(-1.0f, -1.0f), y);  // y - z: there is no paired subtraction
                                 w[h][8 + i / 2] = pack_half(y.x, y.y);
                             }
                         tmem_store(scores + g * 16, w[0]);
