@@ -7,14 +7,19 @@
 //
 // Split. A row stays in the registers of its threads between the reductions (a warp, or a block of up to 1024 threads
 // with up to 32 elements each), so every operand is read once. Few rows take as many threads as leave each eight
-// elements: what counts is the latency of the loads and reductions. Many rows take 32 elements a thread
-// (all loads of a row in flight together, several blocks an SM overlap their reductions).
+// elements: what counts is the latency of the loads and reductions. Many rows take up to 32 elements a thread; residual and gate wait in shared
+// memory (asynchronous copies, each thread's own), so that 64 registers do and four blocks of 256 threads an SM hide each other's reductions.
+//
+// Alignment. Vectors of eight elements start at 16-byte boundaries. Rows that do not (odd widths) are taken from the boundary before
+// them, the same one for all operands as they lie in rows of the same width; their first and last vectors go element by element.
+// Operands whose rows lie differently to the boundaries go element by element throughout.
 //
 // Bound: HBM for many rows, latency for few.
 
 #include <type_traits>
 
 #include "decode_device.cuh"
+#include "om_device.cuh"
 #include "om_internal.h"
 
 namespace om {
@@ -24,41 +29,77 @@ constexpr int kVector = 8;  // elements of a thread's load
 
 struct NormArgs {
     NormProblem p;
-    int row_warps;  // warps of a row
+    int row_warps;        // warps of a row
+    int offset, advance;  // elements between a 16-byte boundary and the first row, and from row to row (modulo 8)
+    bool stage_gate;      // the gate waits in shared memory too
+    bool one_gate;        // the gate is one row for all tokens, read as weights are
 };
 
-// Where element e of a thread's vector v lies in its row: with ALIGNED eight neighbours in a vector, else every
-// thread-count-th element (neighbouring lanes take neighbouring elements, at any alignment).
-template <bool ALIGNED>
-__device__ __forceinline__ int place(int v, int e, int thread, int threads) {
-    return ALIGNED ? (v * threads + thread) * kVector + e : (v * kVector + e) * threads + thread;
-}
+// Where element e of a thread's vector v lies in its row. Vectors are pieces of PIECE neighbours, neighbouring lanes' pieces side by side: what 16
+// bytes of the widest operand hold, so that no copy takes half of a 32-byte sector. kApart: single elements instead.
+enum Lie : int { kApart, kEven, kShifted };  // how operands lie to 16-byte boundaries: each differently, on them, all as far off them
+template <int PIECE, int LIE>
+struct Place {
+    int thread, threads, width, shift;  // shift: elements of the first piece that are before the row
+    __device__ __forceinline__ int at(int v, int e) const {
+        if (LIE == kApart) return (v * kVector + e) * threads + thread;
+        return ((v * (kVector / PIECE) + e / PIECE) * threads + thread) * PIECE + e % PIECE - (LIE == kShifted ? shift : 0);
+    }
+    __device__ __forceinline__ bool inside(int v, int e) const { return static_cast<unsigned>(at(v, e)) < static_cast<unsigned>(width); }
+    // the whole piece lies in the row (an even one that does not is outside it)
+    __device__ __forceinline__ bool whole(int v, int q) const { return inside(v, q * PIECE) && (LIE == kEven || inside(v, q * PIECE + PIECE - 1)); }
+};
 
-// A vector as it is read, two 16-bit elements a word; 0 behind the width.
+// A vector as it is read, two 16-bit elements a word; 0 outside the row.
 template <typename T>
 struct Held {
     static constexpr int kWords = kVector * sizeof(T) / 4;
     uint32_t w[kWords];
 };
 
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ Held<T> load_vector(const T *row, int v, int width, int thread, int threads) {
-    Held<T> h;
-    if constexpr (ALIGNED) {
-        const int i = place<true>(v, 0, thread, threads);
-#pragma unroll
-        for (int q = 0; q < Held<T>::kWords; q += 4) {
-            const uint4 x = i < width ? *reinterpret_cast<const uint4 *>(row + i + q * 4 / sizeof(T)) : make_uint4(0, 0, 0, 0);
-            h.w[q] = x.x; h.w[q + 1] = x.y; h.w[q + 2] = x.z; h.w[q + 3] = x.w;
-        }
+// A piece's words between memory and registers: 8 bytes, 16, or 32 (weights of 32 bits) at once.
+template <int WORDS>
+__device__ __forceinline__ void get_words(const void *from, uint32_t *w, bool there = true) {
+    if constexpr (WORDS == 2) {
+        const uint2 x = there ? *static_cast<const uint2 *>(from) : make_uint2(0, 0);
+        w[0] = x.x; w[1] = x.y;
     } else {
-        T x[kVector];
 #pragma unroll
-        for (int e = 0; e < kVector; ++e) {
-            const int i = place<false>(v, e, thread, threads);
-            x[e] = i < width ? row[i] : from_float<T>(0.0f);
+        for (int i = 0; i < WORDS; i += 4) {
+            const uint4 x = there ? static_cast<const uint4 *>(from)[i / 4] : make_uint4(0, 0, 0, 0);
+            w[i] = x.x; w[i + 1] = x.y; w[i + 2] = x.z; w[i + 3] = x.w;
         }
-        memcpy(h.w, x, sizeof(x));
+    }
+}
+template <int WORDS>
+__device__ __forceinline__ void put_words(void *to, const uint32_t *w) {
+    if constexpr (WORDS == 2) {
+        *static_cast<uint2 *>(to) = make_uint2(w[0], w[1]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < WORDS; i += 4) static_cast<uint4 *>(to)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    }
+}
+
+template <typename T, int PIECE, int LIE>
+__device__ __forceinline__ void load_elements(const T *row, int v, int q, const Place<PIECE, LIE> &l, uint32_t *w) {
+    T x[PIECE];
+#pragma unroll
+    for (int e = 0; e < PIECE; ++e) x[e] = l.inside(v, q * PIECE + e) ? row[l.at(v, q * PIECE + e)] : from_float<T>(0.0f);
+    memcpy(w, x, sizeof(x));
+}
+
+template <typename T, int PIECE, int LIE>
+__device__ __forceinline__ Held<T> load_vector(const T *row, int v, const Place<PIECE, LIE> &l) {
+    constexpr int kWords = PIECE * sizeof(T) / 4;
+    Held<T> h;
+#pragma unroll
+    for (int q = 0; q < kVector / PIECE; ++q) {
+        uint32_t *const w = h.w + q * kWords;
+        if (LIE == kEven || (LIE == kShifted && l.whole(v, q)))
+            get_words<kWords>(row + l.at(v, q * PIECE), w, l.whole(v, q));
+        else
+            load_elements(row, v, q, l, w);
     }
     return h;
 }
@@ -71,36 +112,71 @@ __device__ __forceinline__ void expand(const Held<T> &h, float *x) {
     for (int i = 0; i < kVector; ++i) x[i] = to_float(e[i]);
 }
 
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ void store_vector(T *row, int v, int width, int thread, int threads, const float *x) {
+template <typename T, int PIECE, int LIE>
+__device__ __forceinline__ void store_vector(T *row, int v, const Place<PIECE, LIE> &l, const float *x) {
+    constexpr int kWords = PIECE * sizeof(T) / 4;
     T e[kVector];
 #pragma unroll
     for (int i = 0; i < kVector; ++i) e[i] = from_float<T>(x[i]);
-    if constexpr (ALIGNED) {
-        const int i = place<true>(v, 0, thread, threads);
-        Held<T> h;
-        memcpy(h.w, e, sizeof(e));
-        if (i < width) {
 #pragma unroll
-            for (int q = 0; q < Held<T>::kWords; q += 4)
-                *reinterpret_cast<uint4 *>(row + i + q * 4 / sizeof(T)) = make_uint4(h.w[q], h.w[q + 1], h.w[q + 2], h.w[q + 3]);
-        }
-    } else {
+    for (int q = 0; q < kVector / PIECE; ++q) {
+        if (LIE != kApart && l.whole(v, q)) {
+            uint32_t w[kWords];
+            memcpy(w, e + q * PIECE, sizeof(w));
+            put_words<kWords>(row + l.at(v, q * PIECE), w);
+        } else if (LIE != kEven) {
 #pragma unroll
-        for (int j = 0; j < kVector; ++j) {
-            const int i = place<false>(v, j, thread, threads);
-            if (i < width) row[i] = e[j];
+            for (int i = q * PIECE; i < (q + 1) * PIECE; ++i)
+                if (l.inside(v, i)) row[l.at(v, i)] = e[i];
         }
     }
 }
 
-// A vector of weights, of the activations' type or 32 bits.
-template <typename T, bool ALIGNED>
-__device__ __forceinline__ void load_weights(const void *w, bool wide, int v, int width, int thread, int threads, float *x) {
+// A vector on its way to the thread's own place in shared memory, a piece of each thread side by side.
+template <typename T, int PIECE, int LIE>
+__device__ __forceinline__ void stage_vector(const T *row, int v, const Place<PIECE, LIE> &l, uint8_t *stage) {
+    constexpr int kBytes = PIECE * sizeof(T);
+#pragma unroll
+    for (int q = 0; q < kVector / PIECE; ++q) {
+        uint8_t *const to = stage + ((v * (kVector / PIECE) + q) * l.threads + l.thread) * kBytes;
+        if (LIE == kEven || l.whole(v, q)) {
+            const bool there = l.whole(v, q);
+            const T *const from = there ? row + l.at(v, q * PIECE) : row;
+            if constexpr (kBytes == 16)
+                cp_async_16(smem_u32(to), from, there ? 16 : 0);
+            else
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(to)), "l"(from), "r"(there ? 8 : 0) : "memory");
+        } else {
+            uint32_t w[kBytes / 4];
+            load_elements(row, v, q, l, w);
+            put_words<kBytes / 4>(to, w);
+        }
+    }
+}
+template <typename T, int PIECE, int LIE>
+__device__ __forceinline__ Held<T> staged_vector(int v, const Place<PIECE, LIE> &l, const uint8_t *stage) {
+    constexpr int kBytes = PIECE * sizeof(T);
+    Held<T> h;
+#pragma unroll
+    for (int q = 0; q < kVector / PIECE; ++q) get_words<kBytes / 4>(stage + ((v * (kVector / PIECE) + q) * l.threads + l.thread) * kBytes, h.w + q * kBytes / 4);
+    return h;
+}
+
+// A vector of weights, of the activations' type or 32 bits; rows that start off a boundary read them element by element.
+template <typename T, int PIECE, int LIE>
+__device__ __forceinline__ Held<T> load_weight(const T *w, int v, const Place<PIECE, LIE> &l) {
+    if (LIE != kShifted || l.shift == 0) return load_vector(w, v, l);
+    Held<T> h;
+#pragma unroll
+    for (int q = 0; q < kVector / PIECE; ++q) load_elements(w, v, q, l, h.w + q * static_cast<int>(PIECE * sizeof(T) / 4));
+    return h;
+}
+template <typename T, int PIECE, int LIE>
+__device__ __forceinline__ void load_weights(const void *w, bool wide, int v, const Place<PIECE, LIE> &l, float *x) {
     if (std::is_same_v<T, float> || wide)
-        expand(load_vector<float, ALIGNED>(static_cast<const float *>(w), v, width, thread, threads), x);
+        expand(load_weight(static_cast<const float *>(w), v, l), x);
     else
-        expand(load_vector<T, ALIGNED>(static_cast<const T *>(w), v, width, thread, threads), x);
+        expand(load_weight(static_cast<const T *>(w), v, l), x);
 }
 
 // The sum over a row's threads, in one order whatever the timing. held: of this use alone.
@@ -116,12 +192,11 @@ __device__ __forceinline__ float row_sum(float x, int row_warps, float *held) {
     return x;
 }
 
-// x <- N(x). Elements behind the width are 0 and stay out of the sums.
-template <typename T, bool ALIGNED, int V>
-__device__ __forceinline__ void normalise(float (&x)[V][kVector], const NormProblem &p, const void *weight, const void *bias, int thread, int threads,
-                                          int row_warps, float (*held)[32]) {
-    const float count = static_cast<float>(p.width);
-    const int width = static_cast<int>(p.width);
+// x <- N(x). Elements outside the row are 0 and stay out of the sums.
+template <typename T, int V, int PIECE, int LIE>
+__device__ __forceinline__ void normalise(float (&x)[V][kVector], const NormProblem &p, const void *weight, const void *bias, const Place<PIECE, LIE> &l, int row_warps,
+                                          float (*held)[32]) {
+    const float count = static_cast<float>(l.width);
     const bool wide = p.weight_dtype == OM_F32;
     if (p.layer) {
         float sum = 0.0f;
@@ -133,7 +208,7 @@ __device__ __forceinline__ void normalise(float (&x)[V][kVector], const NormProb
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
-            for (int e = 0; e < kVector; ++e) x[v][e] = place<ALIGNED>(v, e, thread, threads) < width ? __fsub_rn(x[v][e], mean) : 0.0f;
+            for (int e = 0; e < kVector; ++e) x[v][e] = l.inside(v, e) ? __fsub_rn(x[v][e], mean) : 0.0f;
     }
     float squares = 0.0f;
 #pragma unroll
@@ -144,103 +219,172 @@ __device__ __forceinline__ void normalise(float (&x)[V][kVector], const NormProb
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         float w[kVector];
-        if (weight) load_weights<T, ALIGNED>(weight, wide, v, width, thread, threads, w);
+        if (weight) load_weights<T>(weight, wide, v, l, w);
 #pragma unroll
         for (int e = 0; e < kVector; ++e) {
             x[v][e] = __fmul_rn(x[v][e], inv);
             if (weight) x[v][e] = __fmul_rn(x[v][e], w[e]);
         }
         if (bias) {
-            load_weights<T, ALIGNED>(bias, wide, v, width, thread, threads, w);
+            load_weights<T>(bias, wide, v, l, w);
 #pragma unroll
             for (int e = 0; e < kVector; ++e) x[v][e] = __fadd_rn(x[v][e], w[e]);
         }
     }
 }
 
+// 1 / (1 + e^-g) within 2^-21: e^-g = 2^h (1 + l ln 2) with h + l = -g log2(e), the product's rounding in l. (expf and a division, which round
+// better, took 447 us of 16000 x 8192 where this takes 330.) Factors below e^-87 are e^-87, and 0 times g.
 __device__ __forceinline__ float gate_factor(float g, int activation) {
     if (activation == OM_GATE_NONE) return g;
-    const float t = __fdiv_rn(1.0f, __fadd_rn(1.0f, expf(-g)));
+    const float c = g > 88.0f ? 88.0f : (g < -87.0f ? -87.0f : g);  // NaN stays
+    constexpr float kHigh = 1.44269502f, kLow = 1.92596303e-8f;     // log2(e)
+    const float h = __fmul_rn(-c, kHigh), l = __fmaf_rn(-c, kLow, __fmaf_rn(-c, kHigh, -h));
+    float e, t;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(h));
+    e = __fmaf_rn(e, __fmul_rn(l, 0.693147182f), e);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(__fadd_rn(1.0f, e)));
     if (activation == OM_GATE_SIGMOID) return t;
-    return t == 0.0f ? 0.0f : __fmul_rn(g, t);  // g t at the low end, minus infinity included, is its limit
+    return g < -87.0f ? 0.0f : __fmul_rn(g, t);
 }
 
-template <typename T, typename R, int V, int THREADS, bool ALIGNED>
-__global__ void __launch_bounds__(THREADS) block_norm_kernel(const __grid_constant__ NormArgs a) {
+template <typename T, typename R, int V, int THREADS, int LIE>
+__global__ void __launch_bounds__(THREADS, LIE == kApart ? 1 : (THREADS == 256 ? 3 : 1024 / THREADS)) block_norm_kernel(const __grid_constant__ NormArgs a) {
     const NormProblem &p = a.p;
+    constexpr bool kStaged = LIE != kApart && V == 4;  // residual and gate wait in shared memory
+    constexpr int kPiece = 16 / sizeof(R);
+    extern __shared__ __align__(16) uint8_t stage[];
     __shared__ float held[4][32];  // the warps' parts of each sum
-    const int threads = a.row_warps * 32, thread = a.row_warps == 1 ? threadIdx.x & 31 : threadIdx.x, width = static_cast<int>(p.width);
     const int64_t row = a.row_warps == 1 ? static_cast<int64_t>(blockIdx.x) * (blockDim.x / 32) + threadIdx.x / 32 : blockIdx.x;
+    const Place<kPiece, LIE> l{a.row_warps == 1 ? static_cast<int>(threadIdx.x & 31) : static_cast<int>(threadIdx.x), a.row_warps * 32, static_cast<int>(p.width),
+                               LIE == kShifted ? (a.offset + static_cast<int>(row & 7) * a.advance) & 7 : 0};
+    const int own = l.threads * V * kVector;  // elements of a row's place
+    uint8_t *const r_stage = stage + (a.row_warps == 1 ? threadIdx.x / 32 * own * (sizeof(R) + sizeof(T)) : 0);
+    uint8_t *const g_stage = r_stage + (p.residual ? own * sizeof(R) : 0);
     wait_for_earlier();
     if (row >= p.tokens) return;  // a warp that has a row of its own, never a part of a block that shares one
-    Held<T> y[V], g[V];
-    Held<R> r[V];
-    // all of the row's operands are on their way together, where the registers hold them: 1024 threads of 32 elements have room for x alone
-    constexpr bool kTogether = V * THREADS <= 2048;
-    auto residual = [&](int v) { return load_vector<R, ALIGNED>(static_cast<const R *>(p.residual) + row * p.ldr, v, width, thread, threads); };
-    auto gate = [&](int v) { return load_vector<T, ALIGNED>(static_cast<const T *>(p.gate) + row * p.ldg, v, width, thread, threads); };
+    const T *const y_row = static_cast<const T *>(p.y) + row * p.ldy, *const g_row = static_cast<const T *>(p.gate) + row * p.ldg;
+    const R *const r_row = static_cast<const R *>(p.residual) + row * p.ldr;
+    Held<T> y[V], g[kStaged ? 1 : V];
+    Held<R> r[kStaged ? 1 : V];
+    // all of the row's operands are on their way together
 #pragma unroll
-    for (int v = 0; v < V; ++v) y[v] = load_vector<T, ALIGNED>(static_cast<const T *>(p.y) + row * p.ldy, v, width, thread, threads);
-    if (kTogether && p.residual) {
+    for (int v = 0; v < V; ++v) y[v] = load_vector(y_row, v, l);
+    if constexpr (kStaged) {
+        if (p.residual) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) r[v] = residual(v);
-    }
-    if (kTogether && p.gate) {
+            for (int v = 0; v < V; ++v) stage_vector(r_row, v, l, r_stage);
+        }
+        if (a.stage_gate) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) g[v] = gate(v);
+            for (int v = 0; v < V; ++v) stage_vector(g_row, v, l, g_stage);
+        }
+    } else {
+        if (p.residual) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) r[v] = load_vector(r_row, v, l);
+        }
+        if (p.gate) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) g[v] = a.one_gate ? load_weight(g_row, v, l) : load_vector(g_row, v, l);
+        }
     }
     float x[V][kVector];
 #pragma unroll
     for (int v = 0; v < V; ++v) expand(y[v], x[v]);
-    if (p.post) normalise<T, ALIGNED, V>(x, p, p.post_weight, p.post_bias, thread, threads, a.row_warps, held);
+    if (p.post) normalise<T>(x, p, p.post_weight, p.post_bias, l, a.row_warps, held);
+    if constexpr (kStaged) cp_async_wait_all();  // a thread's own copies
 #pragma unroll
     for (int v = 0; v < V; ++v) {
         float f[kVector];
         if (p.gate) {
-            expand(kTogether ? g[v] : gate(v), f);
+            if constexpr (kStaged)
+                expand(a.stage_gate ? staged_vector<T>(v, l, g_stage) : (a.one_gate ? load_weight(g_row, v, l) : load_vector(g_row, v, l)), f);
+            else
+                expand(g[v], f);
 #pragma unroll
             for (int e = 0; e < kVector; ++e) x[v][e] = __fmul_rn(x[v][e], gate_factor(f[e], p.activation));
         }
-        if (p.residual) expand(kTogether ? r[v] : residual(v), f);
+        if (p.residual) {
+            if constexpr (kStaged)
+                expand(staged_vector<R>(v, l, r_stage), f);
+            else
+                expand(r[v], f);
+        }
 #pragma unroll
         for (int e = 0; e < kVector; ++e) x[v][e] = p.residual ? __fmaf_rn(p.scale, x[v][e], f[e]) : __fmul_rn(p.scale, x[v][e]);
     }
     if (p.sum) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) store_vector<R, ALIGNED>(static_cast<R *>(p.sum) + row * p.lds, v, width, thread, threads, x[v]);
+        for (int v = 0; v < V; ++v) store_vector(static_cast<R *>(p.sum) + row * p.lds, v, l, x[v]);
     }
     if (!p.out) return;
-    normalise<T, ALIGNED, V>(x, p, p.weight, p.bias, thread, threads, a.row_warps, held + 2);
+    normalise<T>(x, p, p.weight, p.bias, l, a.row_warps, held + 2);
 #pragma unroll
-    for (int v = 0; v < V; ++v) store_vector<T, ALIGNED>(static_cast<T *>(p.out) + row * p.ldo, v, width, thread, threads, x[v]);
+    for (int v = 0; v < V; ++v) store_vector(static_cast<T *>(p.out) + row * p.ldo, v, l, x[v]);
 }
 
-template <typename T, typename R, int V, int THREADS>
-cudaError_t by_alignment(const NormArgs &a, bool aligned, cudaStream_t s) {
+constexpr int kMostStage = 200 * 1024;
+
+template <typename T, typename R, int V, int THREADS, int LIE>
+cudaError_t launch(NormArgs a, cudaStream_t s) {
     const int rows = a.row_warps == 1 ? 4 : 1;  // of a block
     const dim3 grid(static_cast<unsigned>((a.p.tokens + rows - 1) / rows)), block(32 * a.row_warps * rows);
-    return launch_behind(aligned ? block_norm_kernel<T, R, V, THREADS, true> : block_norm_kernel<T, R, V, THREADS, false>, grid, block, 0, s, a);
+    int stage = 0;
+    if (LIE != kApart && V == 4) {
+        const int elements = static_cast<int>(block.x) * V * kVector, r = elements * static_cast<int>(sizeof(R)), g = elements * static_cast<int>(sizeof(T));
+        a.stage_gate = a.p.gate && !a.one_gate && r + g <= kMostStage;
+        // a block of several rows has a place for both of them in each
+        stage = rows > 1 ? r + g : (a.p.residual ? r : 0) + (a.stage_gate ? g : 0);
+        static PerDevice ready;
+        std::atomic<int> *const kept = ready.here();
+        if (!kept || kept->load(std::memory_order_relaxed) == 0) {
+            const cudaError_t e = cudaFuncSetAttribute(block_norm_kernel<T, R, V, THREADS, LIE>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostStage);
+            if (e != cudaSuccess) return e;
+            if (kept) kept->store(1, std::memory_order_relaxed);
+        }
+    }
+    return launch_behind(block_norm_kernel<T, R, V, THREADS, LIE>, grid, block, stage, s, a);
+}
+
+template <typename T, typename R, int LIE>
+cudaError_t by_width(const NormProblem &p, int offset, int advance, cudaStream_t s) {
+    // a row that starts off a boundary can take a vector more
+    const int64_t vectors = (p.width + kVector - 1) / kVector + (LIE == kShifted);
+    auto warps = [&](int v) { return static_cast<int>((vectors + 32 * v - 1) / (32 * v)); };
+    auto args = [&](int v) { return NormArgs{p, warps(v), offset, advance, false, p.tokens > 1 && p.ldg == 0}; };
+    // eight elements a thread where all rows are in flight at once (153 rows of 4096: 4.1 us, with 32 elements 5.4; 192 of 8177: 9.8 against 7.8)
+    if ((warps(1) <= 32 && p.tokens * warps(1) <= 36 * num_sms()) || warps(1) == 1) return launch<T, R, 1, 1024, LIE>(args(1), s);
+    if (warps(2) == 1) return launch<T, R, 2, 512, LIE>(args(2), s);
+    if (warps(4) <= 8) return launch<T, R, 4, 256, LIE>(args(4), s);
+    if (warps(4) <= 16) return launch<T, R, 4, 512, LIE>(args(4), s);
+    if (warps(4) <= 32) return launch<T, R, 4, 1024, LIE>(args(4), s);
+    return launch<T, R, 4, 1024, kApart>(NormArgs{p, static_cast<int>((p.width + 1023) / 1024), 0, 0, false, false}, s);  // the widest rows off their boundaries
 }
 
 template <typename T, typename R>
-cudaError_t by_width(const NormProblem &p, cudaStream_t s) {
-    auto ok = [](const void *x, int64_t ld, int64_t bytes) { return !x || (reinterpret_cast<uintptr_t>(x) % 16 == 0 && ld * bytes % 16 == 0); };
-    const int64_t tb = sizeof(T), rb = sizeof(R);
-    const bool aligned = p.width % kVector == 0 && ok(p.y, p.ldy, tb) && ok(p.residual, p.ldr, rb) && ok(p.gate, p.ldg, tb) && ok(p.sum, p.lds, rb) &&
-                         ok(p.out, p.ldo, tb) && ok(p.weight, 0, tb) && ok(p.bias, 0, tb) && ok(p.post_weight, 0, tb) && ok(p.post_bias, 0, tb);
-    const int64_t vectors = (p.width + kVector - 1) / kVector;
-    auto warps = [&](int v) { return static_cast<int>((vectors + 32 * v - 1) / (32 * v)); };
-    if (warps(1) <= 32 && p.tokens <= 2 * num_sms()) return by_alignment<T, R, 1, 1024>(NormArgs{p, warps(1)}, aligned, s);
-    if (warps(4) <= 16) return by_alignment<T, R, 4, 512>(NormArgs{p, warps(4)}, aligned, s);
-    return by_alignment<T, R, 4, 1024>(NormArgs{p, warps(4)}, aligned, s);
+cudaError_t by_alignment(const NormProblem &p, cudaStream_t s) {
+    // elements from a 16-byte boundary to the operands' first rows and from row to row; vectors where all of them agree
+    const int offset = static_cast<int>(reinterpret_cast<uintptr_t>(p.y) / sizeof(T) % kVector), advance = p.tokens > 1 ? static_cast<int>(p.ldy % kVector) : 0;
+    auto alike = [&](const void *x, int64_t ld, int64_t bytes) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(x);
+        return !x || (static_cast<int>(at / bytes % kVector) == offset && (p.tokens == 1 || static_cast<int>(ld % kVector) == advance));
+    };
+    auto aligned = [&](const void *x) { return reinterpret_cast<uintptr_t>(x) % 16 == 0; };
+    // weights, and a gate of one row, are read by vectors where a row starts on a boundary
+    const bool vectors = alike(p.residual, p.ldr, sizeof(R)) && (p.tokens > 1 && p.ldg == 0 ? aligned(p.gate) : alike(p.gate, p.ldg, sizeof(T))) && alike(p.sum, p.lds, sizeof(R)) && alike(p.out, p.ldo, sizeof(T)) &&
+                         aligned(p.weight) && aligned(p.bias) && aligned(p.post_weight) && aligned(p.post_bias);
+    if (!vectors) return by_width<T, R, kApart>(p, 0, 0, s);
+    if (offset == 0 && advance == 0 && p.width % kVector == 0) return by_width<T, R, kEven>(p, 0, 0, s);
+    return by_width<T, R, kShifted>(p, offset, advance, s);
 }
 
 }  // namespace
 
 cudaError_t launch_block_norm(const NormProblem &p, cudaStream_t s) {
-    if (p.dtype == OM_F32) return by_width<float, float>(p, s);
-    if (p.dtype == OM_F16) return p.stream_dtype == OM_F32 ? by_width<__half, float>(p, s) : by_width<__half, __half>(p, s);
-    return p.stream_dtype == OM_F32 ? by_width<__nv_bfloat16, float>(p, s) : by_width<__nv_bfloat16, __nv_bfloat16>(p, s);
+    if (p.dtype == OM_F32) return by_alignment<float, float>(p, s);
+    if (p.dtype == OM_F16) return p.stream_dtype == OM_F32 ? by_alignment<__half, float>(p, s) : by_alignment<__half, __half>(p, s);
+    return p.stream_dtype == OM_F32 ? by_alignment<__nv_bfloat16, float>(p, s) : by_alignment<__nv_bfloat16, __nv_bfloat16>(p, s);
 }
 
 }  // namespace om

@@ -120,7 +120,7 @@ def _cuda(t, name, dim, dtypes, device=None):
 
 
 _I32 = (torch.int32,)
-_int32 = torch.int32
+_int32, _float32 = torch.int32, torch.float32
 
 
 def w4_matvec(x, weight, scales, zeros=None, group: int = 128, out=None, stream=None):
@@ -162,22 +162,23 @@ def w4_matvec(x, weight, scales, zeros=None, group: int = 128, out=None, stream=
     return out
 
 
-def _row_vector(t, name, width, dtypes, device):
-    """Pointer of a (width,) operand, None without one."""
-    if t is None:
-        return None
-    _cuda(t, name, 1, dtypes, device)
-    if t.shape[0] != width:
+def _vector(t, name, width, dtype, device):
+    """Pointer of a (width,) operand."""
+    if t.get_device() != device or t.dtype is not dtype or t.dim() != 1 or t.shape[0] != width or (width > 1 and t.stride(0) != 1):
+        _cuda(t, name, 1, (dtype,), device)
         raise ValueError(f"{name} must have the shape ({width},)")
     return t.data_ptr()
 
 
-def _row_major(t, name, shape, dtype, device):
+def _rows(t, name, shape, dtype, device):
     """Pointer and row stride of a (tokens, width) operand."""
-    _cuda(t, name, 2, (dtype,), device)
-    if t.shape != shape:
+    if t.get_device() != device or t.dtype is not dtype or t.shape != shape:
+        _cuda(t, name, 2, (dtype,), device)
         raise ValueError(f"{name} must have the shape {tuple(shape)}")
-    return t.data_ptr(), t.stride(0) if shape[0] > 1 else shape[1]
+    ld, one = t.stride()
+    if one != 1 and shape[1] > 1:
+        raise ValueError(f"{name} needs unit stride in its last dimension")
+    return t.data_ptr(), ld if shape[0] > 1 else shape[1]
 
 
 def block_norm(y, residual=None, weight=None, bias=None, *, post_weight=None, post_bias=None, gate=None, activation=None, scale: float = 1.0,
@@ -193,53 +194,56 @@ def block_norm(y, residual=None, weight=None, bias=None, *, post_weight=None, po
     """
     device = _cuda(y, "y", 2, DTYPES)
     shape, dtype = y.shape, y.dtype
-    tokens, width = shape
+    width = shape[1]
     if norm not in NORMS:
         raise ValueError(f"unknown norm {norm!r}")
     if activation not in GATES:
         raise ValueError(f"unknown activation {activation!r}")
-    if post is None:
-        post = post_weight is not None or post_bias is not None
-    rp, ldr, stream_dtype = None, 0, dtype
+    stream_dtype = dtype
+    rp, ldr = None, 0
     if residual is not None:
-        _cuda(residual, "residual", 2, (dtype, torch.float32), device)
-        stream_dtype = residual.dtype
-        rp, ldr = _row_major(residual, "residual", shape, stream_dtype, device)
-    elif sum_out is not None:
-        _cuda(sum_out, "sum_out", 2, (dtype, torch.float32), device)
-        stream_dtype = sum_out.dtype
+        if residual.dtype is _float32:
+            stream_dtype = _float32
+        rp, ldr = _rows(residual, "residual", shape, stream_dtype, device)
+    elif sum_out is not None and sum_out.dtype is _float32:
+        stream_dtype = _float32
+    gp, ldg = None, 0
     if gate is None:
-        gp, ldg = None, 0
-        if activation not in (None, "none"):
+        if GATES[activation]:
             raise ValueError("an activation needs a gate")
     elif gate.dim() == 1:
-        gp, ldg = _row_vector(gate, "gate", width, (dtype,), device), 0
+        gp = _vector(gate, "gate", width, dtype, device)
     else:
-        gp, ldg = _row_major(gate, "gate", shape, dtype, device)
-    kinds = {w.dtype for w in (weight, bias, post_weight, post_bias) if w is not None}
-    if len(kinds) > 1:
-        raise TypeError("weights and biases must be of one type")
-    weight_dtype = kinds.pop() if kinds else dtype
-    vectors = [_row_vector(w, name, width, (dtype, torch.float32), device)
-               for w, name in ((post_weight, "post_weight"), (post_bias, "post_bias"), (weight, "weight"), (bias, "bias"))]
-    if not normed and (weight is not None or bias is not None or out is not None):
-        raise ValueError("weight, bias and out belong to the second norm")
-    if residual is None and sum_out is None:
-        if not normed:
-            raise ValueError("nothing to compute: no residual, no sum_out and no second norm")
-        sp, lds = None, 0
-    else:
+        gp, ldg = _rows(gate, "gate", shape, dtype, device)
+    weight_dtype = dtype
+    pointers = [None] * 4
+    given = [(i, w, name) for i, w, name in ((0, post_weight, "post_weight"), (1, post_bias, "post_bias"), (2, weight, "weight"), (3, bias, "bias")) if w is not None]
+    if given:
+        if given[0][1].dtype is _float32:
+            weight_dtype = _float32
+        for i, w, name in given:
+            pointers[i] = _vector(w, name, width, weight_dtype, device)
+    if post is None:
+        post = post_weight is not None or post_bias is not None
+    sp, lds, op, ldo = None, 0, None, 0
+    if residual is not None or sum_out is not None:
         if sum_out is None:
             sum_out = _empty(shape, stream_dtype, y.device, stream)
-        sp, lds = _row_major(sum_out, "sum_out", shape, stream_dtype, device)
-    if not normed:
-        op, ldo = None, 0
-    else:
+            sp, lds = sum_out.data_ptr(), width
+        else:
+            sp, lds = _rows(sum_out, "sum_out", shape, stream_dtype, device)
+    elif not normed:
+        raise ValueError("nothing to compute: no residual, no sum_out and no second norm")
+    if normed:
         if out is None:
             out = _empty(shape, dtype, y.device, stream)
-        op, ldo = _row_major(out, "out", shape, dtype, device)
-    _call("om_block_norm", device, stream, tokens, width, y.data_ptr(), y.stride(0) if tokens > 1 else width, DTYPES[dtype], rp, ldr,
-          DTYPES[stream_dtype], gp, ldg, GATES[activation], scale, NORMS[norm], int(bool(post)), eps, *vectors, DTYPES[weight_dtype], sp, lds, op, ldo)
+            op, ldo = out.data_ptr(), width
+        else:
+            op, ldo = _rows(out, "out", shape, dtype, device)
+    elif weight is not None or bias is not None or out is not None:
+        raise ValueError("weight, bias and out belong to the second norm")
+    _call("om_block_norm", device, stream, shape[0], width, y.data_ptr(), y.stride(0) if shape[0] > 1 else width, DTYPES[dtype], rp, ldr,
+          DTYPES[stream_dtype], gp, ldg, GATES[activation], scale, NORMS[norm], post, eps, *pointers, DTYPES[weight_dtype], sp, lds, op, ldo)
     return sum_out, out
 
 
