@@ -14,7 +14,10 @@
 // them, the same one for all operands as they lie in rows of the same width; their first and last vectors go element by element.
 // Operands whose rows lie differently to the boundaries go element by element throughout.
 //
-// Bound: HBM for many rows, latency for few.
+// Bound and measured (GB300; 6 786 GB/s is the measured copy bandwidth). HBM for many rows: 16000 x 8192, bfloat16 with a 32-bit stream, a gate of
+// each token and both norms 314 us (5 840 GB/s, 86 %), without gate and first norm 232 us (100 %), all of it bfloat16 158 us (98 %). Residual and
+// gate in registers from the start (124 of them, two blocks an SM) took 447 us of the first; pieces of 32 bytes a lane instead of 16 for 32-bit streams
+// 381 us (each copy took half of a sector). Latency for few: one token 3.2 us in a row of calls in a graph; 192 rows of 8177, layer norm, float16, 8.9 us.
 
 #include <type_traits>
 
@@ -233,8 +236,8 @@ __device__ __forceinline__ void normalise(float (&x)[V][kVector], const NormProb
     }
 }
 
-// 1 / (1 + e^-g) within 2^-21: e^-g = 2^h (1 + l ln 2) with h + l = -g log2(e), the product's rounding in l. (expf and a division, which round
-// better, took 447 us of 16000 x 8192 where this takes 330.) Factors below e^-87 are e^-87, and 0 times g.
+// 1 / (1 + e^-g) within 2^-21: e^-g = 2^h (1 + l ln 2) with h + l = -g log2(e), the product's rounding in l; both approximate instructions are
+// within 2^-22. Factors below e^-87 are e^-87, and 0 times g.
 __device__ __forceinline__ float gate_factor(float g, int activation) {
     if (activation == OM_GATE_NONE) return g;
     const float c = g > 88.0f ? 88.0f : (g < -87.0f ? -87.0f : g);  // NaN stays

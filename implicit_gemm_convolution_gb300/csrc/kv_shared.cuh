@@ -150,12 +150,32 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
     return y;
 }
-__device__ __forceinline__ float2 mul2_rn(float2 a, float2 b) {
-    unsigned long long r;
-    asm("{\n\t.reg .b64 ra, rb;\n\tmov.b64 ra, {%1, %2};\n\tmov.b64 rb, {%3, %4};\n\tmul.rn.f32x2 %0, ra, rb;\n\t}" : "=l"(r) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    float2 o;
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(o.x), "=f"(o.y) : "l"(r));
-    return o;
+// Pairs of 32-bit floats as the paired instructions take them. What is the same for many of them is paired once.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float a, float b) {
+    Pair p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(a), "f"(b));
+    return p;
+}
+__device__ __forceinline__ float2 apart(Pair p) {
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
+    return f;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+    Pair r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ Pair add2(Pair a, Pair b) {
+    Pair r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+    Pair r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // A word's four codes as 16-bit floats, exactly. A whole number c becomes 1024 + (c + 128) by placing its byte (sign bit
@@ -289,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
         return bars->item[items & 1];
     };
     constexpr std::integral_constant<int, 0> at_once{};
+    constexpr std::integral_constant<int, 40> soon{};
     constexpr std::integral_constant<int, 400> ahead{};
     auto done = [&]() {
         __syncwarp();
@@ -314,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
             {
                 const int R = it.row0 + row, token = R / p.group;
                 const int64_t mine = (it.t0 + token) * p.q.ts + (static_cast<int64_t>(it.h) * p.group + R - token * p.group) * p.q.hs;
-#pragma unroll 1
+#pragma unroll 4
                 for (int i = lane; i < 32 * kRaw; i += 32) {
                     const int r = i / kRaw, k = i % kRaw;
                     const uint8_t *const from = static_cast<const uint8_t *>(p.q.p) + (__shfl_sync(0xffffffffu, mine, r) + k * kElements) * bytes;
@@ -356,7 +377,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                 }
             };
             unsigned most = 0;
-#pragma unroll 1
+#pragma unroll 4
             for (int c = 0; c < DIM / 8; ++c) {
                 float v[8];
                 eight(c, v);
@@ -366,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
             // the row's largest element to [2^13, 2^14)
             const int e2 = max(static_cast<int>(most >> 23) - 127, -100);
             const float up = power_of_two(13 - e2), factor = __fmul_rn(power_of_two(e2 - 13), __fmul_rn(p.scale, kLog2e));
-#pragma unroll 1
+#pragma unroll 4
             for (int c = 0; c < DIM / 8; ++c) {
                 float v[8];
                 eight(c, v);
@@ -501,16 +522,17 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                     less = m - kBias;
                 }
                 // weights: their parts take the scores' place, for 16 positions eight columns of the first and eight of the second
-                float2 tile_sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                Pair tile_sum[2] = {pair(0.0f, 0.0f), pair(0.0f, 0.0f)};
+                const Pair base = pair(-less, -less), minus = pair(-1.0f, -1.0f);
                 auto weigh = [&](auto every) {
                     for_groups<kGroups>(scores, [&](int g, const uint32_t (&a)[16], const uint32_t (&b)[16]) {
                         const float4 of[2] = {groups[g], groups[g + 1]};
-                        float2 kf[2], vf[2];
+                        Pair kf[2], vf[2];
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             const float k = __fmul_rn(of[h].x, factor), v = of[h].y == of[h].y ? in_units(of[h].y, per_unit) : of[h].y;
-                            kf[h] = make_float2(k, k);
-                            vf[h] = make_float2(v, v);
+                            kf[h] = pair(k, k);
+                            vf[h] = pair(v, v);
                         }
                         uint32_t w[2][16];
                         // the groups side by side: two chains of operations for every pair
@@ -519,23 +541,27 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
 #pragma unroll
                             for (int h = 0; h < 2; ++h) {
                                 const uint32_t s0 = h == 0 ? a[i] : b[i], s1 = h == 0 ? a[i + 1] : b[i + 1];
-                                const float2 x = fma2_rn(make_float2(__uint_as_float(s0), __uint_as_float(s1)), kf[h], make_float2(-less, -less));
+                                const float2 x = apart(fma2(pair(__uint_as_float(s0), __uint_as_float(s1)), kf[h], base));
                                 float2 e = make_float2(ex2(x.x), ex2(x.y));
                                 const int many = every.value ? 16 : __float_as_int(of[h].w);
                                 if (!every.value) {
                                     if (i >= many) e.x = 0.0f;
                                     if (i + 1 >= many) e.y = 0.0f;
                                 }
-                                tile_sum[h] = add2_rn(tile_sum[h], e);
-                                float2 y = mul2_rn(e, vf[h]);
+                                const Pair both = pair(e.x, e.y);
+                                tile_sum[h] = add2(tile_sum[h], both);
+                                Pair weights = mul2(both, vf[h]);
                                 if (!every.value) {  // a scale that is not finite does not count where nothing is seen
+                                    float2 y = apart(weights);
                                     if (i >= many) y.x = 0.0f;
                                     if (i + 1 >= many) y.y = 0.0f;
+                                    weights = pair(y.x, y.y);
                                 }
+                                const float2 y = apart(weights);
                                 w[h][i / 2] = pack_half(y.x, y.y);
                                 const float2 z = unpack_half(w[h][i / 2]);
-                                y = fma2_rn(z, make_float2(-1.0f, -1.0f), y);  // y - z: there is no paired subtraction
-                                w[h][8 + i / 2] = pack_half(y.x, y.y);
+                                const float2 rest = apart(fma2(pair(z.x, z.y), minus, weights));  // there is no paired subtraction
+                                w[h][8 + i / 2] = pack_half(rest.x, rest.y);
                             }
                         tmem_store(scores + g * 16, w[0]);
                         tmem_store(scores + g * 16 + 16, w[1]);
@@ -545,7 +571,8 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                     weigh(std::true_type{});
                 else
                     weigh(std::false_type{});
-                l = __fadd_rn(l, __fadd_rn(__fadd_rn(tile_sum[0].x, tile_sum[0].y), __fadd_rn(tile_sum[1].x, tile_sum[1].y)));
+                const float2 sum_a = apart(tile_sum[0]), sum_b = apart(tile_sum[1]);
+                l = __fadd_rn(l, __fadd_rn(__fadd_rn(sum_a.x, sum_a.y), __fadd_rn(sum_b.x, sum_b.y)));
                 tmem_stored();
                 fence_before();
                 __syncwarp();
@@ -720,7 +747,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                 // their order
                 auto score = [&](int i) {
                     const int stage = i % C::kTiles;
-                    ok = wait<0>(bars, &bars->k_full[stage], i / C::kTiles & 1, status);
+                    ok = wait<40>(bars, &bars->k_full[stage], i / C::kTiles & 1, status);
                     if (!ok) return;
                     fence_after();
                     const uint32_t to_scores = tmem + (i & 1) * kPos, keys = k_at + stage * C::kTile;
@@ -732,13 +759,13 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                     }
                     commit(&bars->scored[i & 1], leader);
                 };
-                ok = wait<0>(bars, &bars->q_full, items & 1, status);
+                ok = wait<40>(bars, &bars->q_full, items & 1, status);
                 if (ok) score(n);
 #pragma unroll 1
                 for (int u = from; ok && u < to; ++u, ++n) {
                     if (u + 1 < to) score(n + 1);  // the next tile's, beside the rows' work on this one
                     const int stage = n % C::kTiles;
-                    ok = ok && wait_tile(at_once, bars->weighed, n);
+                    ok = ok && wait_tile(soon, bars->weighed, n);
                     if (!ok) break;
                     fence_after();
                     const uint32_t values = v_at + stage * C::kTile, weights = tmem + (n & 1) * kPos;
