@@ -102,6 +102,13 @@ def _empty(shape, dtype, device, stream):
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _like(t, stream):
+    """A new output of a tensor's shape and type, contiguous."""
+    if stream is None and t.is_contiguous():
+        return torch.empty_like(t)
+    return _empty(t.shape, t.dtype, t.device, stream)
+
+
 def _cuda(t, name, dim, dtypes, device=None):
     """Raises unless t is a CUDA tensor of `dim` dimensions, one of the types and
     unit stride in the last dimension, on the device (by number) if one is given. Returns its device."""
@@ -216,19 +223,21 @@ def block_norm(y, residual=None, weight=None, bias=None, *, post_weight=None, po
     else:
         gp, ldg = _rows(gate, "gate", shape, dtype, device)
     weight_dtype = dtype
-    pointers = [None] * 4
-    given = [(i, w, name) for i, w, name in ((0, post_weight, "post_weight"), (1, post_bias, "post_bias"), (2, weight, "weight"), (3, bias, "bias")) if w is not None]
-    if given:
-        if given[0][1].dtype is _float32:
-            weight_dtype = _float32
-        for i, w, name in given:
-            pointers[i] = _vector(w, name, width, weight_dtype, device)
+    for w in (weight, post_weight, bias, post_bias):
+        if w is not None:
+            if w.dtype is _float32:
+                weight_dtype = _float32
+            break
+    wp = None if weight is None else _vector(weight, "weight", width, weight_dtype, device)
+    bp = None if bias is None else _vector(bias, "bias", width, weight_dtype, device)
+    pwp = None if post_weight is None else _vector(post_weight, "post_weight", width, weight_dtype, device)
+    pbp = None if post_bias is None else _vector(post_bias, "post_bias", width, weight_dtype, device)
     if post is None:
         post = post_weight is not None or post_bias is not None
     sp, lds, op, ldo = None, 0, None, 0
     if residual is not None or sum_out is not None:
         if sum_out is None:
-            sum_out = _empty(shape, stream_dtype, y.device, stream)
+            sum_out = _like(residual, stream)
             sp, lds = sum_out.data_ptr(), width
         else:
             sp, lds = _rows(sum_out, "sum_out", shape, stream_dtype, device)
@@ -236,14 +245,14 @@ def block_norm(y, residual=None, weight=None, bias=None, *, post_weight=None, po
         raise ValueError("nothing to compute: no residual, no sum_out and no second norm")
     if normed:
         if out is None:
-            out = _empty(shape, dtype, y.device, stream)
+            out = _like(y, stream)
             op, ldo = out.data_ptr(), width
         else:
             op, ldo = _rows(out, "out", shape, dtype, device)
     elif weight is not None or bias is not None or out is not None:
         raise ValueError("weight, bias and out belong to the second norm")
     _call("om_block_norm", device, stream, shape[0], width, y.data_ptr(), y.stride(0) if shape[0] > 1 else width, DTYPES[dtype], rp, ldr,
-          DTYPES[stream_dtype], gp, ldg, GATES[activation], scale, NORMS[norm], post, eps, *pointers, DTYPES[weight_dtype], sp, lds, op, ldo)
+          DTYPES[stream_dtype], gp, ldg, GATES[activation], scale, NORMS[norm], post, eps, pwp, pbp, wp, bp, DTYPES[weight_dtype], sp, lds, op, ldo)
     return sum_out, out
 
 
