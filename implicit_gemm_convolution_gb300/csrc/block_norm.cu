@@ -8,7 +8,7 @@
 // Split. A row stays in the registers of its threads between the reductions (a warp, or a block of up to 1024 threads
 // with up to 32 elements each), so every operand is read once. Few rows take as many threads as leave each eight
 // elements: what counts is the latency of the loads and reductions. Many rows take up to 32 elements a thread; residual and gate wait in shared
-// memory (asynchronous copies, each thread's own), so that 64 registers do and four blocks of 256 threads an SM hide each other's reductions.
+// memory (asynchronous copies, each thread's own), so that 80 registers do and three blocks of 256 threads an SM hide each other's reductions.
 //
 // Alignment. Vectors of eight elements start at 16-byte boundaries. Rows that do not (odd widths) are taken from the boundary before
 // them, the same one for all operands as they lie in rows of the same width; their first and last vectors go element by element.
@@ -356,7 +356,7 @@ cudaError_t by_width(const NormProblem &p, int offset, int advance, cudaStream_t
     const int64_t vectors = (p.width + kVector - 1) / kVector + (LIE == kShifted);
     auto warps = [&](int v) { return static_cast<int>((vectors + 32 * v - 1) / (32 * v)); };
     auto args = [&](int v) { return NormArgs{p, warps(v), offset, advance, false, p.tokens > 1 && p.ldg == 0}; };
-    // eight elements a thread where all rows are in flight at once (153 rows of 4096: 4.1 us, with 32 elements 5.4; 192 of 8177: 9.8 against 7.8)
+    // eight elements a thread where all rows are in flight at once (153 rows of 4096: 4.1 us, with 32 elements 5.4; 192 of 8177: 8.3 against 7.8)
     if ((warps(1) <= 32 && p.tokens * warps(1) <= 36 * num_sms()) || warps(1) == 1) return launch<T, R, 1, 1024, LIE>(args(1), s);
     if (warps(2) == 1) return launch<T, R, 2, 512, LIE>(args(2), s);
     if (warps(4) <= 8) return launch<T, R, 4, 256, LIE>(args(4), s);

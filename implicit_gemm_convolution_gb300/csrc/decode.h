@@ -1,7 +1,7 @@
-// decode.h -- problems of the decoding operators (4-bit matrix-vector product,
-// paged 8-bit cache: append, attention, read back), validated by
-// decode_api.cu and run by w4_matvec.cuh, kv_cache.cu and kv_attention.cuh. Not
-// installed; not part of the public ABI.
+// decode.h -- problems of the decoding operators (4-bit matrix-vector product, norms around a
+// block, paged 8-bit cache: append, attention, attention to shared prefixes, read back), validated by
+// decode_api.cu and run by w4_matvec.cuh, block_norm.cu, kv_cache.cu, kv_attention.cuh, kv_shared.cuh and
+// kv_shared_join.cu. Not installed; not part of the public ABI.
 #pragma once
 
 #include <atomic>

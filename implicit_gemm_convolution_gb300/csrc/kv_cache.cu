@@ -10,7 +10,9 @@
 // Bound and measured (GB300; 6 790 GB/s is the measured copy bandwidth): HBM. Prompts of 12031 tokens in all, 32 query
 // and 8 key heads of 128, 32-bit: 93 us for 525 MB (5 600 GB/s, 83 %). Reading 76166 tokens of 8 heads of 128 back as
 // bfloat16: 79 us, 5 930 GB/s (87 %); with 16-byte loads whose lanes stored 32 or 64 bytes each it took 108 us. One
-// token for each of 192 sequences: 15 us, the latency of the lookups, the page's old codes and its barrier.
+// token for each of 192 sequences: 15 us, the latency of the lookups, the page's old codes and its barrier. Positions of three axes: prompts of 12031
+// tokens in all, with their tokens read back, 122 us (one position a token 119 us; with 8 bytes of the table at a time, whether a unit's
+// pairs differ in their axes or not, 133 us).
 
 #include <type_traits>
 
@@ -34,21 +36,6 @@ __device__ __forceinline__ int unit_offset(int u, int rot, bool interleaved, int
     return 8 * u;
 }
 
-// Cos and sin of unit u's four pairs where each pair has the position of its own axis (token t's); NaN for axes there
-// are not and positions the table does not hold. The pairs' rows differ: 8 bytes each.
-__device__ __forceinline__ void load_turn_of_axes(float *cs, const KvAppendProblem &p, int64_t t, int u) {
-    const int rot = static_cast<int>(p.rot);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const int64_t axis = p.pair_axis ? p.pair_axis[4 * u + i] : 0;
-        const int64_t pos = axis >= 0 && axis < p.axes ? p.positions[axis * p.axis_stride + t] : -1;
-        const float2 x = pos >= 0 && pos < p.rows ? __ldg(reinterpret_cast<const float2 *>(p.table + pos * rot + 8 * u + 2 * i))
-                                                  : make_float2(__int_as_float(0x7FC00000), __int_as_float(0x7FC00000));
-        cs[2 * i] = x.x;
-        cs[2 * i + 1] = x.y;
-    }
-}
-
 // The table's cos and sin of unit u's four pairs at position pos; NaN for positions the table does not hold.
 __device__ __forceinline__ void load_turn(float *cs, const float *table, int64_t rows, int rot, int64_t pos, int u) {
     if (pos >= 0 && pos < rows) {
@@ -59,6 +46,28 @@ __device__ __forceinline__ void load_turn(float *cs, const float *table, int64_t
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) cs[i] = __int_as_float(0x7FC00000);
+    }
+}
+
+// The same where each pair has the position of its own axis (token t's); NaN for axes there are not. Four pairs of one axis are 32 bytes
+// of one row, others 8 bytes of a row each.
+__device__ __forceinline__ void load_turn_of_axes(float *cs, const KvAppendProblem &p, int64_t t, int u) {
+    const int rot = static_cast<int>(p.rot);
+    int axis[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) axis[i] = p.pair_axis ? __ldg(p.pair_axis + 4 * u + i) : 0;
+    auto position = [&](int64_t a) -> int64_t { return a >= 0 && a < p.axes ? __ldg(p.positions + a * p.axis_stride + t) : -1; };
+    if (axis[0] == axis[1] && axis[0] == axis[2] && axis[0] == axis[3]) {
+        load_turn(cs, p.table, p.rows, rot, position(axis[0]), u);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int64_t pos = position(axis[i]);
+        const float2 x = pos >= 0 && pos < p.rows ? __ldg(reinterpret_cast<const float2 *>(p.table + pos * rot + 8 * u + 2 * i))
+                                                  : make_float2(__int_as_float(0x7FC00000), __int_as_float(0x7FC00000));
+        cs[2 * i] = x.x;
+        cs[2 * i + 1] = x.y;
     }
 }
 

@@ -1,6 +1,7 @@
 """Decoding operators of a language model: products of a few rows with 4-bit
-weights, and a paged 8-bit cache of keys and values with its append (the
-position rotation applied on the way), attention and read back.
+weights, the norms around a block with its gate and residual, and a paged 8-bit
+cache of keys and values with its append (the position rotation applied on the way, on one
+axis or several), attention (within a window, or to a prefix that sequences share) and read back.
 
 Argument marshalling over include/om.h, like the rest of the binding: every
 step of the computation is a kernel of the library. Tensors are CUDA tensors
@@ -466,8 +467,9 @@ def kv_attention(cache, q, block_table, ctx_len, cu, max_new: int, scale=None, w
         if workspace.get_device() != device or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous tensor on the cache's device")
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
-    _call("om_kv_attention_sinks", device, stream, cache._ref, seqs, tokens, max_new, q_heads, q.data_ptr(), ts, hs, DTYPES[dtype], *batch,
-          dim ** -0.5 if scale is None else scale, window, sinks, *oa, lp, ws, ws_bytes)
+    name, visible = ("om_kv_attention_sinks", (window, sinks)) if sinks else ("om_kv_attention", (window,))
+    _call(name, device, stream, cache._ref, seqs, tokens, max_new, q_heads, q.data_ptr(), ts, hs, DTYPES[dtype], *batch,
+          dim ** -0.5 if scale is None else scale, *visible, *oa, lp, ws, ws_bytes)
     return out
 
 
