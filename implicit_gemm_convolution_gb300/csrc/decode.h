@@ -179,8 +179,10 @@ struct SharedProblem {
     const int32_t *prefix_len, *group_at, *cu;
     float scale;
     int64_t blocks, slot_rows;
+    int64_t most_tiles;                // of a block's part of an item, for tables of this width
     float2 *whole_state, *slot_state;  // [tokens][q_heads], [2 blocks][slot_rows]
     float *whole, *slots;              // and their values, [dim] each
+    float *kept;                       // [blocks][slot_rows][dim]: a part's sums beyond what stays in tensor memory, in the blocks' own order
     const float2 *own_state;           // of the sequences' own tokens, [tokens][q_heads]
     const float *own;
     Heads out;

@@ -1,5 +1,6 @@
 // decode_api.cu -- the C ABI of the decoding operators: argument validation and launch
 // on the caller's stream. Nothing is launched by a call that fails validation.
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
@@ -125,7 +126,7 @@ struct BatchBlocks {
 // Where a call on shared prefixes keeps what its kernels hand on, behind the scratch of the attention to own tokens.
 struct SharedPlaces {
     float2 *whole_state, *own_state, *slot_state;
-    float *whole, *own, *slots;
+    float *whole, *own, *slots, *kept;
     int64_t slot_rows;
     size_t bytes;
 };
@@ -147,6 +148,7 @@ SharedPlaces shared_places(void *workspace, int64_t group, int64_t q_heads, int6
     p.whole = reinterpret_cast<float *>(take(rows * dim * 4));
     p.own = reinterpret_cast<float *>(take(rows * dim * 4));
     p.slots = reinterpret_cast<float *>(take(slots * dim * 4));
+    p.kept = reinterpret_cast<float *>(take(slots / 2 * dim * 4));
     p.bytes = used;
     return p;
 }
@@ -446,8 +448,9 @@ int om_kv_shared_attention(const om_kv_cache *cache, int64_t groups, const int32
     p.prefix_table = prefix_table; p.prefix_width = prefix_width; p.prefix_len = prefix_len; p.group_at = group_offsets; p.cu = cu;
     p.scale = scale;
     p.blocks = blocks;
+    p.most_tiles = groups < 1 ? 0 : std::min(prefix_width * c.page / om::kSharedTile + 1, static_cast<int64_t>(prefix_units) / blocks + 1);
     p.slot_rows = at.slot_rows;
-    p.whole_state = at.whole_state; p.slot_state = at.slot_state; p.whole = at.whole; p.slots = at.slots;
+    p.whole_state = at.whole_state; p.slot_state = at.slot_state; p.whole = at.whole; p.slots = at.slots; p.kept = at.kept;
     p.own_state = at.own_state; p.own = at.own;
     p.out = ho;
     p.lse = lse;

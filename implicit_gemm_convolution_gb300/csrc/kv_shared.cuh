@@ -12,7 +12,8 @@
 //
 // Block (16 warps, two blocks an SM for heads of up to 128), on tiles of 64 positions:
 //   warps 0-3   a row of scores a thread: the tile's maximum from tensor memory, then weights, whose parts replace the scores as the
-//               second product's operand; rows of sums are multiplied only when a unit or maximum changes; queries in, sums out.
+//               second product's operand; rows of sums are multiplied only when a unit or maximum changes; queries in, sums out. 32-bit calls' sums, and those
+//               of long parts, leave tensor memory every few tiles: the tensor cores cut sums off, the more the longer they grow.
 //   warps 4-11  codes of keys (4-7) and values from the pages, the next tile's on their way, to 16-bit floats in shared memory: rows of
 //               128 bytes with the tensor cores' exclusive-or, the same layout for both (k-major and n-major operands).
 //   warp 12     tensor memory, and one lane that issues the products: the next tile's scores beside the rows' work on this one.
@@ -27,7 +28,8 @@
 // difference between them, and two blocks an SM fill each other's waits. 64 sequences behind a prefix of 32768 tokens (8 key heads of 128, 8 query
 // heads each, bfloat16): this kernel 118 us, with the own tokens and the join 154 us; the tensor cores are busy 56 % of it, issue slots 66 %. The
 // prefix is read once (67 MB of keys and values, 10 us at the copy bandwidth). One token of each sequence over the same prefix by kv_attention.cuh
-// reads it 64 times. 40 sequences with drafts of 32-bit queries, which go in two parts, behind three prefixes of 8001 tokens: 53 us of 90. Tiles of 128 positions with one block an SM ran
+// reads it 64 times. 40 sequences with drafts of 32-bit queries, which go in two parts, behind three prefixes of 8001 tokens: 90 us of 127 (with all of a part's sums
+// in tensor memory 53 of 90, and errors to 9e-6 behind long prefixes, where they are 2e-6 now). Tiles of 128 positions with one block an SM ran
 // slower (nothing to fill the waits of the rows). Registers by warpgroup (88 for rows, 56 for copies): with equal shares the rows spill, and loads
 // that wait for a spilled register no longer run ahead.
 #pragma once
@@ -49,6 +51,7 @@ constexpr int kRowWarps = 4, kCopyWarps = 4;  // copy warps: of keys, and as man
 constexpr int kProductWarp = kRowWarps + 2 * kCopyWarps, kWalkWarp = kProductWarp + 1, kScaleWarp = kWalkWarp + 1;
 constexpr int kThreads = 512;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kSharedFold = 4;  // tiles of 32-bit calls whose sums stay in tensor memory
 // as in kv_attention.cuh
 constexpr float kBias = 8.0f, kMost = 32768.0f, kLeast = 0.5f, kMostExp = 1099511627776.0f;
 constexpr float kNone = -FLT_MAX;
@@ -267,7 +270,8 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t *at, bool there) {
     return x;
 }
 
-template <int KV, int DIM, int PARTS>
+// FOLD: tiles whose sums stay in tensor memory before they are added to those in global memory, as rounded 32-bit sums (0: all of a part's)
+template <int KV, int DIM, int PARTS, int FOLD>
 __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel(const __grid_constant__ SharedProblem p) {
     using C = Config<DIM, PARTS>;
     constexpr int kPos = C::kPos, kGroups = C::kGroups, kBlocks = DIM / 64;
@@ -422,6 +426,11 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
 
             float m = kNone, l = 0.0f, per_unit = 1.0f;
             const int from = it.from, to = it.to;
+            // four columns of the lane's row, of the sums that no longer are in tensor memory
+            auto kept = [&](int c) {
+                const int rows = static_cast<int>(p.slot_rows), first = warp * 32;
+                return reinterpret_cast<float4 *>(p.kept + (static_cast<int64_t>(blockIdx.x) * rows + first) * DIM) + (c / 4 * min(rows - first, 32) + lane);
+            };
 #pragma unroll 1
             for (int u = from; u < to; ++u, ++n) {
                 const uint32_t scores = tmem + lanes + (n & 1) * kPos;
@@ -480,7 +489,8 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                 const bool live = heavy > -INFINITY;
                 const float most_w = __fmul_rn(ex2(heavy - less), per_unit);
                 const bool fits = (!live || most_w >= kLeast) && most_w <= kMost && ex2(top - less) <= kMostExp;
-                if (!__all_sync(0xffffffffu, fits)) {
+                const bool fold = FOLD > 0 && u > from && (u - from) % (FOLD > 0 ? FOLD : 1) == 0;  // this tile's product starts new sums
+                if (fold || !__all_sync(0xffffffffu, fits)) {
                     float by = 1.0f;  // what the sums are multiplied by
                     int raise = 0;    // the unit goes down by so many powers of two
                     if (!fits && top > kNone) {
@@ -496,6 +506,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                         }
                     }
                     if (u > from) {
+                        const bool keeps = FOLD > 0 && u - from > FOLD && row < it.rows;
                         // earlier tiles' sums are complete before they are touched
                         ok = wait_tile(at_once, bars->summed, n - 1);
                         if (!ok) break;
@@ -510,19 +521,48 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) most = max(most, o[i] & 0x7fffffffu);
                             }
+#pragma unroll 1
+                            for (int c = 0; keeps && c < DIM; c += 4) {
+                                const float4 o = __ldcg(kept(c));
+                                most = max(most, max(max(__float_as_uint(o.x) & 0x7fffffffu, __float_as_uint(o.y) & 0x7fffffffu),
+                                                     max(__float_as_uint(o.z) & 0x7fffffffu, __float_as_uint(o.w) & 0x7fffffffu)));
+                            }
+                            __syncwarp();
                             most = __float_as_uint(__fmul_rn(__uint_as_float(most), by));
                             raise = min(raise, max(227 - static_cast<int>(most >> 23), 0));
                         }
                         const int k = raise / 2;  // up to 2^252 either way: in two steps
                         const float one = __fmul_rn(by, power_of_two(k)), two = power_of_two(raise - k);
+                        auto times = [&](float x) { return __fmul_rn(__fmul_rn(x, one), two); };
+                        if (by != 1.0f || raise != 0) {
+#pragma unroll 1
+                            for (int c = 0; keeps && c < DIM; c += 4) {
+                                const float4 o = __ldcg(kept(c));
+                                __stcg(kept(c), make_float4(times(o.x), times(o.y), times(o.z), times(o.w)));
+                            }
+                        }
+                        __syncwarp();
 #pragma unroll 1
                         for (int c = 0; c < DIM; c += 16) {
                             uint32_t o[16];
                             tmem_load(sums + lanes + c, o);
                             tmem_loaded(o);
 #pragma unroll
-                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(o[i]), one), two));
-                            tmem_store(sums + lanes + c, o);
+                            for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(times(__uint_as_float(o[i])));
+                            if (!fold) {
+                                tmem_store(sums + lanes + c, o);
+                            } else if (row < it.rows) {
+#pragma unroll
+                                for (int i = 0; i < 16; i += 4) {
+                                    const float4 x = make_float4(__uint_as_float(o[i]), __uint_as_float(o[i + 1]), __uint_as_float(o[i + 2]), __uint_as_float(o[i + 3]));
+                                    // nobody else adds to them: their order is the thread's, which does not wait for the sums
+                                    if (keeps)
+                                        atomicAdd(kept(c + i), x);
+                                    else
+                                        __stcg(kept(c + i), x);
+                                }
+                            }
+                            __syncwarp();
                         }
                         tmem_stored();
                     }
@@ -604,11 +644,26 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
             }
             constexpr int kPitch = 20;  // floats of a row of 16, free of bank conflicts
             float *const stage = reinterpret_cast<float *>(smem + warp * 4096);  // where the warp's own queries were
+            const bool keeps = FOLD > 0 && to - 1 - from >= FOLD && row < it.rows;
+            float4 more[4];
+            if (keeps)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) more[i] = __ldcg(kept(4 * i));
 #pragma unroll 1
             for (int c = 0; c < DIM; c += 16) {
                 uint32_t o[16];
                 tmem_load(sums + lanes + c, o);
                 tmem_loaded(o);
+                if (keeps) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        o[4 * i] = __float_as_uint(__fadd_rn(__uint_as_float(o[4 * i]), more[i].x));
+                        o[4 * i + 1] = __float_as_uint(__fadd_rn(__uint_as_float(o[4 * i + 1]), more[i].y));
+                        o[4 * i + 2] = __float_as_uint(__fadd_rn(__uint_as_float(o[4 * i + 2]), more[i].z));
+                        o[4 * i + 3] = __float_as_uint(__fadd_rn(__uint_as_float(o[4 * i + 3]), more[i].w));
+                        if (c + 16 < DIM) more[i] = __ldcg(kept(c + 16 + 4 * i));
+                    }
+                }
                 __syncwarp();
 #pragma unroll
                 for (int i = 0; i < 16; i += 4) {
@@ -779,7 +834,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                     const uint32_t values = v_at + stage * C::kTile, weights = tmem + (n & 1) * kPos;
 #pragma unroll
                     for (int k = 0; k < kPos / 16; ++k) {  // small parts first
-                        mma_tmem(sums, weights + k * 16 + 8, operand(values + k * 2048, kPos * 128), C::kSums, k > 0 || u > from, leader);
+                        mma_tmem(sums, weights + k * 16 + 8, operand(values + k * 2048, kPos * 128), C::kSums, k > 0 || (FOLD > 0 ? (u - from) % (FOLD > 0 ? FOLD : 1) != 0 : u > from), leader);
                         mma_tmem(sums, weights + k * 16, operand(values + k * 2048, kPos * 128), C::kSums, true, leader);
                     }
                     commit(&bars->summed[n & 1], leader);
@@ -801,25 +856,32 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
     if (warp == kProductWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kColumns) : "memory");
 }
 
-template <int KV, int DIM, int PARTS>
+template <int KV, int DIM, int PARTS, int FOLD>
 cudaError_t launch(const SharedProblem &p, cudaStream_t s) {
     constexpr int kSmem = Config<DIM, PARTS>::kSmem;
     static PerDevice ready;
     std::atomic<int> *const kept = ready.here();
     if (!kept || kept->load(std::memory_order_relaxed) == 0) {
-        const cudaError_t e = cudaFuncSetAttribute(kv_shared_kernel<KV, DIM, PARTS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        const cudaError_t e = cudaFuncSetAttribute(kv_shared_kernel<KV, DIM, PARTS, FOLD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         if (kept) kept->store(1, std::memory_order_relaxed);
     }
-    return launch_behind(kv_shared_kernel<KV, DIM, PARTS>, dim3(static_cast<unsigned>(p.blocks)), dim3(kThreads), kSmem, s, p);
+    return launch_behind(kv_shared_kernel<KV, DIM, PARTS, FOLD>, dim3(static_cast<unsigned>(p.blocks)), dim3(kThreads), kSmem, s, p);
+}
+
+// The tensor cores cut their sums off. 16-bit calls leave a part's sums to them up to 256 tiles (values of one sign, weights alike: 3e-5 off);
+// with the code for longer ones, 64 tiles at a time, 64 sequences behind 32768 tokens took 170 us instead of 157. 32-bit calls: see above.
+template <int KV, int DIM>
+cudaError_t by_type(const SharedProblem &p, cudaStream_t s) {
+    constexpr int64_t kLong = 256;
+    if (p.dtype == OM_F32) return launch<KV, DIM, 2, kSharedFold>(p, s);
+    return p.most_tiles > kLong ? launch<KV, DIM, 1, 64>(p, s) : launch<KV, DIM, 1, 0>(p, s);
 }
 
 template <int KV>
 cudaError_t run_kv_shared(const SharedProblem &p, cudaStream_t s) {
-    const bool two = p.dtype == OM_F32;
-    if (p.c.dim == 64) return two ? launch<KV, 64, 2>(p, s) : launch<KV, 64, 1>(p, s);
-    if (p.c.dim == 128) return two ? launch<KV, 128, 2>(p, s) : launch<KV, 128, 1>(p, s);
-    return two ? launch<KV, 256, 2>(p, s) : launch<KV, 256, 1>(p, s);
+    if (p.c.dim == 64) return by_type<KV, 64>(p, s);
+    return p.c.dim == 128 ? by_type<KV, 128>(p, s) : by_type<KV, 256>(p, s);
 }
 
 }  // namespace

@@ -574,7 +574,7 @@ OM_API size_t om_kv_shared_workspace_bytes(int64_t kv_heads, int64_t q_heads, in
  * Rows that see nothing, scores that are NaN, table entries outside the cache, tokens that no sequence owns, the precision of queries and
  * weights: as there. Products over the prefix run on the tensor cores (sums of 32 bits).
  * workspace: device memory, 16-byte aligned, of om_kv_shared_workspace_bytes for this call's heads, max_new and tokens or more (8 dim + 16 bytes a
- * token and query head, and up to 101 MB for the blocks' parts), zeroed once before its first use; calls that may run at the same time need
+ * token and query head, and up to 141 MB for the blocks' parts), zeroed once before its first use; calls that may run at the same time need
  * distinct ones. A bounded device wait that runs out is recorded in its
  * status word (om_workspace_status), and the outputs are then incomplete. Results do not depend on timing.
  */

@@ -363,3 +363,77 @@ def test_empty_calls_and_refusals():
         om.kv_shared_attention(s.cache, q, s.ptable, s.plen.long(), s.at, s.table, s.lens, s.cu, 2)
     with pytest.raises(ValueError):
         om.new_shared_workspace(s.cache, 3, 1, 4)
+
+
+def long_parts(x, dim, tokens, hq, prefix, own, same_sign, seed, tiles=4):
+    """One sequence of many new tokens behind a long prefix: blocks whose parts are longer than the tiles whose sums stay in tensor
+    memory (`tiles`: 4 for 32-bit queries, for others 256, or 64 where parts may be longer). Pages' scales of keys grow with the position, so that maxima rise until the end; those of
+    values go up and down over 10^4. Without a sign or scales of keys: every weight is the same, and errors of a sum add up."""
+    s = Shared([prefix], [0, 1], [own], [tokens], 1, dim, 64, "int8", seed)
+    g = gen(seed + 1)
+    q = torch.randn(tokens, hq, dim, generator=g, device="cuda")
+    pages = torch.from_numpy(s.ptable_np[0]).cuda()[: -(-prefix // 64)]
+    if same_sign:
+        s.v = torch.randint(1, 128, s.v.shape, generator=g, device="cuda").to(torch.int8)
+        s.vs[:] = 0.013
+        q.zero_()
+    else:
+        s.ks[pages, 0] = torch.linspace(0.002, 0.06, len(pages), device="cuda")
+        s.vs[pages, 0] = 10.0 ** (2 * torch.sin(0.1 * torch.arange(len(pages), device="cuda")))
+    q = q.to(ref.TORCH[x])
+    s.device()
+    lse = torch.empty(tokens, hq, device="cuda")
+    out = s.attend(q, lse=lse, workspace=s.workspace(hq))
+    # the formula in 64 bits, a thousand rows at a time
+    pos = torch.arange(prefix, device="cuda")
+    opos = torch.arange(own, device="cuda")
+    otable = torch.from_numpy(s.table_np[0]).cuda()
+    ids, rows = torch.cat((pages[pos // 64], otable[opos // 64])), torch.cat((pos, opos)) % 64
+    k, v = (c[ids, 0, rows].double() * sc[ids, 0][:, None].double() for c, sc in ((s.k, s.ks), (s.v, s.vs)))
+    at = torch.cat((pos - prefix, opos))
+    scale, worst = dim ** -0.5, 0.0
+    for t0 in range(0, tokens, max(1, 1024 // hq)):
+        qq = q[t0: t0 + max(1, 1024 // hq)].double()
+        n = qq.shape[0]
+        y = scale * (qq.reshape(-1, dim) @ k.T)
+        here = (own - tokens + torch.arange(t0, t0 + n, device="cuda")).repeat_interleave(hq)
+        y.masked_fill_(at > here[:, None], float("-inf"))
+        top = y.amax(1, keepdim=True)
+        big = scale * (qq.abs().reshape(-1, dim) @ k.abs().T).amax(1, keepdim=True)
+        e = torch.exp(y - top)
+        total = e.sum(1, keepdim=True)
+        want, mag = e @ v / total, e @ v.abs() / total
+        ds = (dim + 16) * 2.0 ** -22 * big
+        # cut sums: 8 steps a tile over the tiles that stay, then one rounding a fold and part; own tokens as in check()
+        steps = 8 * tiles + prefix / 64 / tiles + (0 if x == "f32" else own / 8) + 64
+        tol = (2 * ds + 2.0 ** -19 + steps * 2.0 ** -22) * mag + 1.01 * ref.UNIT[x] * want.abs() + ref.TINY[x] + 1e-30
+        off = (out[t0: t0 + n].reshape(-1, dim).double() - want).abs()
+        assert bool((off <= tol).all()), f"outputs {float((off / tol).max())} of the tolerance at tokens from {t0}"
+        worst = max(worst, float((off / mag).max()))
+        wl = (top + total.log()).reshape(n, hq)
+        # a tile's weights are added up in 32 bits, then the tiles
+        tl = ds.reshape(n, hq) + (prefix / 64 + own / 8 + 128) * 2.0 ** -22 + 2.0 ** -20 + 2.0 ** -22 * wl.abs()
+        assert bool(((lse[t0: t0 + n].double() - wl).abs() <= tl).all()), "lse"
+    return worst
+
+
+@pytest.mark.parametrize("x,dim,tokens,hq,prefix,own,tiles", [
+    ("f32", 64, 1000, 8, 8192, 1000, 4),     # cut items of some 26 tiles
+    ("f32", 128, 500, 8, 20000, 700, 4),
+    ("f32", 256, 333, 4, 20001, 333, 4),     # a last block of few rows
+    ("f32", 64, 2500, 16, 1500, 2500, 4),    # whole items among them
+    ("bf16", 128, 1024, 16, 17000, 1024, 256),
+    ("f16", 64, 4096, 16, 4500, 4096, 256),
+    ("f16", 64, 4096, 10, 17300, 4096, 64),  # whole items of 271 tiles
+    ("bf16", 256, 2100, 10, 17300, 2100, 64),
+])
+def test_parts_longer_than_sums_stay(x, dim, tokens, hq, prefix, own, tiles):
+    long_parts(x, dim, tokens, hq, prefix, own, False, 40 + dim, tiles)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_long_sums_of_one_sign(dim):
+    """Before sums were taken out of tensor memory every few tiles, they were 2.5e-5 (heads of 256: 1e-4) off here."""
+    worst = long_parts("f32", dim, 512, 8, 131072, 600, True, 50)
+    # 32 cut steps and some 100 folds, no score error: queries are zero
+    assert worst <= 2.0 ** -19 + (64 + 32 + 16) * 2.0 ** -23
