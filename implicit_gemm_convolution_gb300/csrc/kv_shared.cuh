@@ -806,8 +806,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                 const SharedItem &it = take();
                 if (!ok || it.rows == 0) break;
                 const int from = it.from, to = it.to;
-                // the scores of tile i. They take the place of weights whose products were issued before: products are executed in
-                // their order
+                // the scores of tile i
                 auto score = [&](int i) {
                     const int stage = i % C::kTiles;
                     ok = wait<40>(bars, &bars->k_full[stage], i / C::kTiles & 1, status);
@@ -826,7 +825,15 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                 if (ok) score(n);
 #pragma unroll 1
                 for (int u = from; ok && u < to; ++u, ++n) {
-                    if (u + 1 < to) score(n + 1);  // the next tile's, beside the rows' work on this one
+                    // The next tile's scores, beside the rows' work on this one. They take the place of the weights of the tile before, which its
+                    // product reads until it is complete: products of one thread keep their order only where accumulator and shape are
+                    // the same, and these differ in both. (Scores of an item's first tile follow its queries, which the rows bring after
+                    // all products of the item before.)
+                    if (u + 1 < to) {
+                        ok = n == 0 || wait_tile(soon, bars->summed, n - 1);
+                        if (!ok) break;
+                        score(n + 1);
+                    }
                     const int stage = n % C::kTiles;
                     ok = ok && wait_tile(soon, bars->weighed, n);
                     if (!ok) break;
