@@ -64,6 +64,14 @@ def quantize4(w, group: int):
     return (codes[:, 0::2] | (codes[:, 1::2] << 4)).contiguous(), scale, zero.to(torch.uint8)
 
 
+def places(ctx_len, cu, tokens: int):
+    """The place of each of a call's tokens in its sequence, int32 (tokens,), found on the device: the sequence's new tokens are its
+    last ones. Rows behind the last sequence's tokens, which a padded batch has, count on from it."""
+    token = torch.arange(tokens, dtype=torch.int32, device=cu.device)
+    seq = torch.searchsorted(cu[1:], token, right=True).clamp_(max=max(ctx_len.shape[0] - 1, 0))
+    return token + (ctx_len - cu[1:])[seq]
+
+
 class AttentionLayer:
     """x + W_o attention(W_qkv x), or x + scale gate N_post(W_o attention(W_qkv N(x))) with norms, over a batch of sequences
     that each own the pages of ``capacity`` tokens, behind a common prefix of up to ``prefix`` tokens."""
@@ -107,7 +115,8 @@ class AttentionLayer:
 
     def run(self, x, counts=None, cu=None, positions=None):
         """x (tokens, model), the new tokens of each sequence one after the other: counts (int32 [seqs]) of
-        them with their offsets cu (int32 [seqs + 1]), or one each. positions (int32 [axes, tokens]): the tokens' rotary
+        them with their offsets cu (int32 [seqs + 1]; rows of x behind them are nobody's, and what comes back there is not
+        defined), or one each. positions (int32 [axes, tokens]): the tokens' rotary
         positions on each axis, for a layer with sections (None: their places, on all axes). Returns x's successor."""
         step = cu is None
         if step:
@@ -118,12 +127,8 @@ class AttentionLayer:
             self.ctx_len += counts
         if positions is None and (self.axis is not None or self.prefix_table.shape[1]):
             # places in the sequence, the prefix among them
-            if step:
-                places = self.ctx_len - 1
-            else:
-                first = self.ctx_len - counts - cu[:-1]
-                places = torch.repeat_interleave(first, counts, output_size=x.shape[0]) + torch.arange(x.shape[0], dtype=torch.int32, device=x.device)
-            positions = (places + self.prefix_len).expand(len(self.shape.sections) or 1, -1).contiguous()
+            own = self.ctx_len - 1 if step else places(self.ctx_len, cu, x.shape[0])
+            positions = (own + self.prefix_len).expand(len(self.shape.sections) or 1, -1).contiguous()
         return self._block(x, self.block_table, self.ctx_len, cu, most, positions, self.prefix_table.shape[1] > 0)
 
     def run_prefix(self, x, positions=None):
