@@ -85,7 +85,7 @@ class AttentionLayer:
             raise ValueError("post_norm, gate and residual_scale belong to a layer with norms")
         if s.sections and 2 * sum(s.sections) != s.rot:
             raise ValueError("sections must have an axis for each rotated pair")
-        self.seqs, self.dtype, self.max_new = seqs, dtype, max_new
+        self.seqs, self.dtype, self.max_new, self.prefix = seqs, dtype, max_new, prefix
         g = torch.Generator(device=device).manual_seed(seed)
 
         def weights(n, k):
@@ -135,7 +135,8 @@ class AttentionLayer:
         """The prefix that all sequences share, x (tokens, model): computed and kept once, before the sequences' own
         tokens. Returns x's successor."""
         tokens = x.shape[0]
-        if not 0 < tokens <= self.prefix_table.shape[1] * self.shape.page:
+        # the last page may have room for more, but the rotation's table has none for the own tokens behind them
+        if not 0 < tokens <= self.prefix:
             raise ValueError("the layer has no room for such a prefix")
         if positions is None and self.axis is not None:
             positions = torch.arange(tokens, dtype=torch.int32, device=x.device).expand(len(self.shape.sections), -1).contiguous()

@@ -27,3 +27,15 @@ def test_rows_behind_the_last_sequence(prefix, kw):
     assert torch.equal(got[:137], want) and torch.isfinite(want).all()
     assert torch.equal(a.cache.k, b.cache.k) and torch.equal(a.cache.v_scale, b.cache.v_scale) and torch.equal(a.ctx_len, b.ctx_len)
     assert torch.equal(a.run(step_of(a)), b.run(step_of(b)))
+
+
+def test_the_longest_prefix_and_the_longest_sequence_behind_it():
+    """A prefix that ends inside a page: the sequence's last token is at the table's last row. One token more is refused, where it had been
+    taken into the page's room and the last own tokens came out NaN."""
+    layer = layer_of(prefix=40, capacity=20, max_new=20)
+    with pytest.raises(ValueError):
+        layer.run_prefix(prompt_of(layer, [41], 2)[0])
+    assert layer.prefix_len.tolist() == [0]
+    layer.run_prefix(prompt_of(layer, [40], 2)[0])
+    layer.run(*prompt_of(layer, [19, 3, 19]))
+    assert torch.isfinite(layer.run(step_of(layer))).all() and layer.ctx_len.tolist() == [20, 4, 20]
