@@ -273,7 +273,7 @@ __device__ __forceinline__ void normalise(float (&x)[V][kVector], const NormProb
 }
 
 // 1 / (1 + e^-g) within 2^-21: e^-g = 2^h (1 + l ln 2) with h + l = -g log2(e), the product's rounding in l; both approximate instructions are
-// within 2^-22. Factors below e^-87 are e^-87, and 0 times g.
+// within 2^-22. Factors of gates below -87, which leave the range of 32 bits, are 0.
 __device__ __forceinline__ float gate_factor(float g, int activation) {
     if (activation == OM_GATE_NONE) return g;
     const float c = g > 88.0f ? 88.0f : (g < -87.0f ? -87.0f : g);  // NaN stays
@@ -283,8 +283,8 @@ __device__ __forceinline__ float gate_factor(float g, int activation) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(h));
     e = __fmaf_rn(e, __fmul_rn(l, 0.693147182f), e);
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(t) : "f"(__fadd_rn(1.0f, e)));
-    if (activation == OM_GATE_SIGMOID) return t;
-    return g < -87.0f ? 0.0f : __fmul_rn(g, t);
+    if (g < -87.0f) return 0.0f;
+    return activation == OM_GATE_SIGMOID ? t : __fmul_rn(g, t);
 }
 
 template <typename T, typename R, int V, int THREADS, int LIE>

@@ -395,7 +395,8 @@ typedef enum om_gate {
  * sum and out may each be y or the residual itself (same address, type and stride); other overlaps with inputs are
  * OM_ERR_ALIAS. Everything is computed in 32 bits; out is taken from the sum before that
  * is rounded to its type, and each output is rounded once. Squares above the range of 32 bits
- * (elements of 2^64 and more) make their row's norm 0 or NaN. Results do not depend on timing.
+ * (elements of 2^64 and more) make their row's norm 0 or NaN. The sigmoid and silu of gates below -87, minus infinity
+ * among them, are 0. Results do not depend on timing.
  */
 OM_API int om_block_norm(int64_t tokens, int64_t width, const void *y, int64_t ldy, int dtype,
                          const void *residual, int64_t ldr, int stream_dtype,

@@ -56,3 +56,18 @@ def test_rows_of_one_value(width):
     # differences are at most 64 u of the value before their mean is taken out, 65 u of that after
     tol = 66 * U * 64 * U * np.abs(ref.f64(y)) * 1e3 + 1e-37
     assert (np.abs(ref.f64(h)) <= tol).all()
+
+
+@pytest.mark.parametrize("act", ["sigmoid", "silu"])
+@pytest.mark.parametrize("width", [64, 1000, 4096])
+def test_a_gate_that_is_shut(act, width):
+    """Gates of minus infinity and far below 0 let nothing through, however large the block's output is; the sigmoid is e^-g below
+    about 2^-125, where the factor counts as 0."""
+    gates = [float("-inf"), -1e4, -200.0, -89.0, -86.0, 0.0, 200.0]
+    y = torch.full((len(gates), width), 1e30, device="cuda")
+    g = torch.tensor(gates, device="cuda")[:, None].expand(-1, width).contiguous()
+    x = om.block_norm(y, torch.zeros_like(y), gate=g, activation=act, normed=False)[0]
+    assert (x[:4] == 0).all()
+    v = ref.f64(g[4:])
+    want = 1e30 / (1 + np.exp(-v)) * (v if act == "silu" else 1.0)
+    assert (np.abs(ref.f64(x[4:]) - want) <= 10 * U * np.abs(want)).all()
