@@ -38,6 +38,7 @@
 #include <climits>
 #include <type_traits>
 
+#include "attention_range.cuh"
 #include "decode_device.cuh"
 #include "kv_shared_items.cuh"
 #include "om_device.cuh"
@@ -50,21 +51,7 @@ namespace {
 constexpr int kRowWarps = 4, kCopyWarps = 4;  // copy warps: of keys, and as many of values
 constexpr int kProductWarp = kRowWarps + 2 * kCopyWarps, kWalkWarp = kProductWarp + 1, kScaleWarp = kWalkWarp + 1;
 constexpr int kThreads = 512;
-constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kSharedFold = 4;  // tiles of 32-bit calls whose sums stay in tensor memory
-// as in kv_attention.cuh
-constexpr float kBias = 8.0f, kMost = 32768.0f, kLeast = 0.5f, kMostExp = 1099511627776.0f;
-constexpr float kNone = -FLT_MAX;
-constexpr float kLeastUnit = FLT_MIN, kLeastOfScale = 7.8886090522101181e-31f;
-constexpr unsigned kMostUnit = 253u << 23;
-__device__ __forceinline__ float in_units(float value, float per_unit) { return fminf(fmaxf(__fmul_rn(value, per_unit), -FLT_MAX), FLT_MAX); }
-__device__ __forceinline__ float power_of_two(int e) { return __uint_as_float(static_cast<unsigned>(e + 127) << 23); }
-__device__ __forceinline__ float reciprocal(float power) { return __uint_as_float((254u << 23) - __float_as_uint(power)); }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 
 // Instruction descriptor of tcgen05.mma kind::f16: D fp32 (bit 4), A and B fp16 (0), B n-major where
 // asked (bit 16), N >> 3 in bits 17-22, M >> 4 in bits 24-28.
@@ -143,18 +130,6 @@ __device__ __forceinline__ void tmem_store(uint32_t at, const uint32_t (&r)[16])
                  : "memory");
 }
 __device__ __forceinline__ void tmem_stored() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-__device__ __forceinline__ uint32_t pack_half(float a, float b) {
-    const __half2 h = __floats2half2_rn(a, b);
-    uint32_t r;
-    memcpy(&r, &h, 4);
-    return r;
-}
-__device__ __forceinline__ float2 unpack_half(uint32_t x) {
-    __half2 h;
-    memcpy(&h, &x, 4);
-    return __half22float2(h);
-}
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float y;
@@ -631,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
             ok = wait_tile(at_once, bars->summed, n - 1);
             if (!ok) break;
             fence_after();
-            const float inv = shared_inverse(l), back = reciprocal(per_unit);
+            const float inv = inverse(l), back = reciprocal(per_unit);
             const bool whole = it.from == 0 && it.to == it.units;
             const int slot = 2 * static_cast<int>(blockIdx.x) + !it.at_start;
             auto place = [&](int r) -> int64_t {

@@ -119,11 +119,4 @@ struct SharedItems {
     }
 };
 
-// 1 / x to a unit in the last place, and 0 for a sum of nothing.
-__device__ __forceinline__ float shared_inverse(float x) {
-    float y;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return x == 0.0f ? 0.0f : y;
-}
-
 }  // namespace om

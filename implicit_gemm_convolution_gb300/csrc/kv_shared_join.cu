@@ -10,6 +10,7 @@
 
 #include <type_traits>
 
+#include "attention_range.cuh"
 #include "decode_device.cuh"
 #include "kv_shared_items.cuh"
 #include "om_internal.h"
@@ -18,15 +19,6 @@ namespace om {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr float kBias = 8.0f;  // sums are 2^8 times the exponentials'
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// Without a maximum a part saw nothing (its sum is 0) or scores that are all NaN (its sum is NaN, and stays).
-__device__ __forceinline__ float joined(float sum, float top, float best) { return top == -INFINITY ? sum : __fmul_rn(sum, ex2(top - best)); }
 
 template <int N>
 __device__ __forceinline__ void load_values(const float *from, float (&v)[N]) {
@@ -151,7 +143,7 @@ __global__ void __launch_bounds__(kThreads) kv_shared_join_kernel(const __grid_c
                 }
             }
         }
-        const float inv = shared_inverse(mass);
+        const float inv = inverse(mass);
 #pragma unroll
         for (int e = 0; e < kEach; ++e) o[e] = __fmul_rn(o[e], inv);
         T *const to = static_cast<T *>(const_cast<void *>(p.out.p)) + t * p.out.ts + head * p.out.hs + lane * kEach;
