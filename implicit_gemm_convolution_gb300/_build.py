@@ -26,7 +26,7 @@ SOURCES = ["om_api.cu", "simple_kernels.cu", "sgemm_tiled.cu", "conv_implicit.cu
            "conv_direct.cu", "gemv.cu", "gemm_tf32x3.cu", "gemm_no_alloc.cu", "selftest.cu",
            "decode_api.cu", "w4_matvec_f32.cu", "w4_matvec_f16.cu", "w4_matvec_bf16.cu", "kv_cache.cu", "block_norm.cu", "kv_attention_f32.cu",
            "kv_attention_f16.cu", "kv_attention_bf16.cu", "kv_attention_sinks_f32.cu", "kv_attention_sinks_f16.cu", "kv_attention_sinks_bf16.cu",
-           "kv_shared_i8.cu", "kv_shared_e4m3.cu", "kv_shared_join.cu", "kv_attention_part_f32.cu", "kv_attention_part_f16.cu", "kv_attention_part_bf16.cu"]
+           "kv_shared_i8.cu", "kv_shared_e4m3.cu", "kv_shared_pages_i8.cu", "kv_shared_pages_e4m3.cu", "kv_shared_join.cu", "kv_attention_part_f32.cu", "kv_attention_part_f16.cu", "kv_attention_part_bf16.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-lineinfo", "-O3", "-std=c++17", "-fmad=false", "-Xptxas", "--fmad=false",
                      "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

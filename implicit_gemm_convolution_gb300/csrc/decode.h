@@ -191,6 +191,9 @@ struct SharedProblem {
 };
 cudaError_t launch_kv_shared_i8(const SharedProblem &p, cudaStream_t s);
 cudaError_t launch_kv_shared_e4m3(const SharedProblem &p, cudaStream_t s);
+// pages smaller than a tile
+cudaError_t launch_kv_shared_pages_i8(const SharedProblem &p, cudaStream_t s);
+cudaError_t launch_kv_shared_pages_e4m3(const SharedProblem &p, cudaStream_t s);
 cudaError_t launch_kv_shared_join(const SharedProblem &p, cudaStream_t s);
 
 cudaError_t launch_rope_table(int64_t rows, int64_t rot, double base, int scaling, double factor,

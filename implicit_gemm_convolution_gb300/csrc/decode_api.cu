@@ -456,7 +456,9 @@ int om_kv_shared_attention(const om_kv_cache *cache, int64_t groups, const int32
     p.lse = lse;
     p.status = static_cast<unsigned *>(workspace) + om::kWsStatusWord;
     if (groups > 0) {
-        const cudaError_t e = c.dtype == OM_I8 ? om::launch_kv_shared_i8(p, s) : om::launch_kv_shared_e4m3(p, s);
+        const bool pages = c.page < om::kSharedTile;
+        const cudaError_t e = c.dtype == OM_I8 ? (pages ? om::launch_kv_shared_pages_i8(p, s) : om::launch_kv_shared_i8(p, s))
+                                               : (pages ? om::launch_kv_shared_pages_e4m3(p, s) : om::launch_kv_shared_e4m3(p, s));
         if (e != cudaSuccess) return OM_ERR_CUDA;
     }
     const om::KvAttentionProblem own{c, seqs, tokens, max_new, q_heads, hq, {at.own, q_heads * c.dim, c.dim}, dtype, reinterpret_cast<float *>(at.own_state),

@@ -8,7 +8,8 @@
 // for 128 rows and a tile of 64 positions, sums in tensor memory. Codes are exact in 16-bit floats, queries are scaled
 // by a power of two for each row (32-bit ones in two parts of 11 bits), weights 2^(x - m) s / u go in two parts of 11 bits
 // with a power-of-two unit u for each row, set anew when a tile's largest weight leaves [2^-1, 2^15]: a weight is off by no more
-// than 2^-22 of itself or 2^-24 of its tile's largest.
+// than 2^-22 of itself or 2^-24 of its tile's largest. Pages of one tile whose value scales are too far apart for one unit are
+// taken one after the other: the tile comes again for each, with the others hidden.
 //
 // Block (16 warps, two blocks an SM for heads of up to 128), on tiles of 64 positions:
 //   warps 0-3   a row of scores a thread: the tile's maximum from tensor memory, then weights, whose parts replace the scores as the
@@ -188,8 +189,12 @@ __device__ __forceinline__ uint2 widen(uint32_t w) {
 struct TileScales {
     float4 group[kSharedTile / 16];
     float largest;  // magnitude of a visible group's value scale
-    int plain;      // every position is visible, and larger products are larger scores
+    int kind;
 };
+// What kind of tile it is. kPlain: every position is visible, and larger products are larger scores. kAgain: the same positions' tile comes again, for
+// pages of other scales. From kApart on: how many powers of two the value scales are apart. They share a unit up to kSpread; its largest
+// weight has to stay so much higher for the weights of the smaller scales to keep their bits.
+constexpr int kPlain = 1, kAgain = 2, kApart = 2, kSpread = 8;
 // Barriers of what there are two of (tiles by their number's parity, items) belong to one of them: a wait for a phase never
 // meets the phase after the next.
 struct Bars {
@@ -197,6 +202,7 @@ struct Bars {
     uint64_t item_full[2], item_free[2];
     SharedItem item[2];  // rows 0: there are no more
     TileScales scales[2];
+    int again[4];  // kAgain of the last tiles, for the other roles: tile n + 4's replaces tile n's once the rows are done with tile n + 2
     uint32_t tmem;
     int abort;
 };
@@ -245,8 +251,9 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t *at, bool there) {
     return x;
 }
 
+// SEVERAL: pages are smaller than a tile, which then can come again. (As a choice at run time 64 conversations in pages of 64 took 163 us instead of 157.)
 // FOLD: tiles whose sums stay in tensor memory before they are added to those in global memory, as rounded 32-bit sums (0: all of a part's)
-template <int KV, int DIM, int PARTS, int FOLD>
+template <int KV, int DIM, int PARTS, int FOLD, bool SEVERAL>
 __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel(const __grid_constant__ SharedProblem p) {
     using C = Config<DIM, PARTS>;
     constexpr int kPos = C::kPos, kGroups = C::kGroups, kBlocks = DIM / 64;
@@ -400,20 +407,22 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
             if (lane == 0) mbar_arrive(&bars->q_full);
 
             float m = kNone, l = 0.0f, per_unit = 1.0f;
-            const int from = it.from, to = it.to;
+            const int first_tile = n;
             // four columns of the lane's row, of the sums that no longer are in tensor memory
             auto kept = [&](int c) {
                 const int rows = static_cast<int>(p.slot_rows), first = warp * 32;
                 return reinterpret_cast<float4 *>(p.kept + (static_cast<int64_t>(blockIdx.x) * rows + first) * DIM) + (c / 4 * min(rows - first, 32) + lane);
             };
 #pragma unroll 1
-            for (int u = from; u < to; ++u, ++n) {
+            for (int left = it.to - it.from; left > 0; ++n) {
                 const uint32_t scores = tmem + lanes + (n & 1) * kPos;
                 const float4 *const groups = bars->scales[n & 1].group;
                 ok = wait_tile(at_once, bars->scored, n);
                 if (!ok) break;
                 fence_after();
-                const bool plain = bars->scales[n & 1].plain;
+                const int kind = bars->scales[n & 1].kind;
+                const bool plain = (kind & kPlain) != 0;
+                left -= !SEVERAL || !(kind & kAgain);
                 // the tile's largest score, and the largest log of a score's weight times its value scale; scores that are all NaN leave none
                 float top = -INFINITY, heavy = -INFINITY;
                 auto note = [&](float x, float log_scale) {
@@ -463,8 +472,8 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                 float less = m - kBias;
                 const bool live = heavy > -INFINITY;
                 const float most_w = __fmul_rn(ex2(heavy - less), per_unit);
-                const bool fits = (!live || most_w >= kLeast) && most_w <= kMost && ex2(top - less) <= kMostExp;
-                const bool fold = FOLD > 0 && u > from && (u - from) % (FOLD > 0 ? FOLD : 1) == 0;  // this tile's product starts new sums
+                const bool fits = (!live || most_w >= (SEVERAL ? power_of_two((kind >> kApart) - 1) : kLeast)) && most_w <= kMost && ex2(top - less) <= kMostExp;
+                const bool fold = FOLD > 0 && n > first_tile && (n - first_tile) % (FOLD > 0 ? FOLD : 1) == 0;  // this tile's product starts new sums
                 if (fold || !__all_sync(0xffffffffu, fits)) {
                     float by = 1.0f;  // what the sums are multiplied by
                     int raise = 0;    // the unit goes down by so many powers of two
@@ -480,8 +489,8 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                             raise = (static_cast<int>((254u << 23) - unit) - static_cast<int>(__float_as_uint(per_unit))) >> 23;
                         }
                     }
-                    if (u > from) {
-                        const bool keeps = FOLD > 0 && u - from > FOLD && row < it.rows;
+                    if (n > first_tile) {
+                        const bool keeps = FOLD > 0 && n - first_tile > FOLD && row < it.rows;
                         // earlier tiles' sums are complete before they are touched
                         ok = wait_tile(at_once, bars->summed, n - 1);
                         if (!ok) break;
@@ -619,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
             }
             constexpr int kPitch = 20;  // floats of a row of 16, free of bank conflicts
             float *const stage = reinterpret_cast<float *>(smem + warp * 4096);  // where the warp's own queries were
-            const bool keeps = FOLD > 0 && to - 1 - from >= FOLD && row < it.rows;
+            const bool keeps = FOLD > 0 && n - 1 - first_tile >= FOLD && row < it.rows;
             float4 more[4];
             if (keeps)
 #pragma unroll
@@ -708,15 +717,30 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
             load(codes, it.from * kPos, ids, x);
             ids = page_of((it.from + 1) * kPos);
 #pragma unroll 1
-            for (int u = it.from; u < to; ++u, ++n) {
+            for (int u = it.from; u < to; ++n) {  // n counts a tile that comes again, u does not
                 // the products that read what this takes the place of
                 const int last = n - C::kTiles, stage = n % C::kTiles;
                 ok = last < 0 || wait_tile(ahead, values ? bars->summed : bars->scored, last);
                 if (!ok) break;
                 store(smem + C::kQBytes + ((values ? C::kTiles : 0) + stage) * C::kTile, x);
-                if (lane == 0) mbar_arrive(values ? &bars->weighed[n & 1] : &bars->k_full[stage]);
+                if (lane == 0 && !(SEVERAL && values)) mbar_arrive(values ? &bars->weighed[n & 1] : &bars->k_full[stage]);
                 if (u + 1 < to) load(codes, (u + 1) * kPos, ids, x);
                 ids = page_of((u + 2) * kPos);
+                if constexpr (SEVERAL) {
+                    // Whether the tile comes again is known with its scores. Values are given away after that has been read: what is
+                    // read is not replaced before.
+                    ok = wait_tile(soon, bars->scored, n);
+                    if (!ok) break;
+                    const bool again = bars->again[n & 3] != 0;
+                    __syncwarp();
+                    if (lane == 0 && values) mbar_arrive(&bars->weighed[n & 1]);
+                    if (again) {
+                        load(codes, u * kPos, page_of(u * kPos), x);
+                        ids = page_of((u + 1) * kPos);
+                        continue;
+                    }
+                }
+                ++u;
             }
             if (!ok) break;
             done();
@@ -751,25 +775,56 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                 auto page_of = [&](int pos0) { return load_page(table, pos0 + lane * 16, lane < kGroups ? len : 0, page_log); };
                 int id = page_of(it.from * kPos);
 #pragma unroll 1
-                for (int u = it.from; u < to; ++u, ++n) {
+                for (int u = it.from; u < to; ++u) {
                     const int id_next = page_of((u + 1) * kPos);
                     const int64_t at = static_cast<int64_t>(id) * heads + it.h;
                     const float ka = there(id) ? p.c.k_scale[at] : 0.0f, va = there(id) ? p.c.v_scale[at] : 0.0f;
                     const int many = there(id) ? min(max(len - (u * kPos + lane * 16), 0), 16) : 0;
                     const bool finite = fabsf(va) <= FLT_MAX;  // an infinite scale counts as NaN, and sets no unit
                     const float magnitude = finite ? fabsf(va) : 0.0f;
-                    const bool plain = __all_sync(0xffffffffu, lane >= kGroups || (many == 16 && __fmul_rn(ka, p.scale) >= 0.0f));
-                    const unsigned largest = __reduce_max_sync(0xffffffffu, many > 0 ? __float_as_uint(magnitude) : 0u);
-                    ok = n < 2 || wait_tile(ahead, bars->weighed, n - 2);
-                    if (!ok) break;
-                    TileScales &s = bars->scales[n & 1];
-                    if (lane < kGroups) s.group[lane] = make_float4(ka, finite ? va : __int_as_float(0x7FC00000), log2f(magnitude), __int_as_float(many));
-                    if (lane == 0) {
-                        s.largest = __uint_as_float(largest);
-                        s.plain = plain;
+                    const bool grows = __fmul_rn(ka, p.scale) >= 0.0f;
+                    // scales too far apart are taken one after the other, by their exponents below the largest one; groups without a magnitude with the first
+                    const unsigned mine = many > 0 ? __float_as_uint(magnitude) : 0u;
+                    unsigned largest = __reduce_max_sync(0xffffffffu, mine);
+                    int below = 0;
+                    unsigned passes = 1;  // a bit for each
+                    int spread = 0;
+                    if constexpr (SEVERAL) {
+                        if (mine > 0) below = static_cast<int>(largest >> 23) - static_cast<int>(mine >> 23);
+                        spread = 1 + __reduce_max_sync(0xffffffffu, below);
+                        if (spread > kSpread) {
+                            spread = kSpread;
+                            below /= kSpread;
+                            passes = __reduce_or_sync(0xffffffffu, 1u << below);
+                        }
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->scored[n & 1]);
+                    const bool several = passes != 1;
+#pragma unroll 1
+                    do {
+                        int here = many;
+                        if constexpr (SEVERAL) {
+                            if (several) {
+                                const bool takes = below == __ffs(passes) - 1;
+                                here = takes ? many : 0;
+                                largest = __reduce_max_sync(0xffffffffu, takes ? mine : 0u);
+                            }
+                            passes &= passes - 1;
+                        }
+                        const bool plain = __all_sync(0xffffffffu, lane >= kGroups || (here == 16 && grows));
+                        ok = n < 2 || wait_tile(ahead, bars->weighed, n - 2);
+                        if (!ok) break;
+                        TileScales &s = bars->scales[n & 1];
+                        if (lane < kGroups) s.group[lane] = make_float4(ka, finite ? va : __int_as_float(0x7FC00000), log2f(magnitude), __int_as_float(here));
+                        if (lane == 0) {
+                            s.largest = __uint_as_float(largest);
+                            s.kind = (plain ? kPlain : 0) | (SEVERAL && passes != 0 ? kAgain : 0) | spread << kApart;
+                            if constexpr (SEVERAL) bars->again[n & 3] = passes != 0;
+                        }
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars->scored[n & 1]);
+                        ++n;
+                    } while (SEVERAL && passes != 0);
+                    if (!ok) break;
                     id = id_next;
                 }
                 if (!ok) break;
@@ -798,13 +853,22 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                 };
                 ok = wait<40>(bars, &bars->q_full, items & 1, status);
                 if (ok) score(n);
+                const int first_tile = n;
 #pragma unroll 1
-                for (int u = from; ok && u < to; ++u, ++n) {
+                for (int u = from; ok && u < to; ++n) {
+                    bool again = false;  // the same positions' tile
+                    if constexpr (SEVERAL) {
+                        ok = wait_tile(soon, bars->scored, n);
+                        if (!ok) break;
+                        again = bars->again[n & 3] != 0;
+                        __syncwarp();
+                    }
+                    u += !again;
                     // The next tile's scores, beside the rows' work on this one. They take the place of the weights of the tile before, which its
                     // product reads until it is complete: products of one thread keep their order only where accumulator and shape are
                     // the same, and these differ in both. (Scores of an item's first tile follow its queries, which the rows bring after
                     // all products of the item before.)
-                    if (u + 1 < to) {
+                    if (u < to) {
                         ok = n == 0 || wait_tile(soon, bars->summed, n - 1);
                         if (!ok) break;
                         score(n + 1);
@@ -816,7 +880,7 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
                     const uint32_t values = v_at + stage * C::kTile, weights = tmem + (n & 1) * kPos;
 #pragma unroll
                     for (int k = 0; k < kPos / 16; ++k) {  // small parts first
-                        mma_tmem(sums, weights + k * 16 + 8, operand(values + k * 2048, kPos * 128), C::kSums, k > 0 || (FOLD > 0 ? (u - from) % (FOLD > 0 ? FOLD : 1) != 0 : u > from), leader);
+                        mma_tmem(sums, weights + k * 16 + 8, operand(values + k * 2048, kPos * 128), C::kSums, k > 0 || (FOLD > 0 ? (n - first_tile) % (FOLD > 0 ? FOLD : 1) != 0 : n > first_tile), leader);
                         mma_tmem(sums, weights + k * 16, operand(values + k * 2048, kPos * 128), C::kSums, true, leader);
                     }
                     commit(&bars->summed[n & 1], leader);
@@ -838,32 +902,32 @@ __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel
     if (warp == kProductWarp) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(C::kColumns) : "memory");
 }
 
-template <int KV, int DIM, int PARTS, int FOLD>
+template <int KV, int DIM, int PARTS, int FOLD, bool SEVERAL>
 cudaError_t launch(const SharedProblem &p, cudaStream_t s) {
     constexpr int kSmem = Config<DIM, PARTS>::kSmem;
     static PerDevice ready;
     std::atomic<int> *const kept = ready.here();
     if (!kept || kept->load(std::memory_order_relaxed) == 0) {
-        const cudaError_t e = cudaFuncSetAttribute(kv_shared_kernel<KV, DIM, PARTS, FOLD>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+        const cudaError_t e = cudaFuncSetAttribute(kv_shared_kernel<KV, DIM, PARTS, FOLD, SEVERAL>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
         if (e != cudaSuccess) return e;
         if (kept) kept->store(1, std::memory_order_relaxed);
     }
-    return launch_behind(kv_shared_kernel<KV, DIM, PARTS, FOLD>, dim3(static_cast<unsigned>(p.blocks)), dim3(kThreads), kSmem, s, p);
+    return launch_behind(kv_shared_kernel<KV, DIM, PARTS, FOLD, SEVERAL>, dim3(static_cast<unsigned>(p.blocks)), dim3(kThreads), kSmem, s, p);
 }
 
 // The tensor cores cut their sums off. 16-bit calls leave a part's sums to them up to 256 tiles (values of one sign, weights alike: 3e-5 off);
 // with the code for longer ones, 64 tiles at a time, 64 sequences behind 32768 tokens took 170 us instead of 157. 32-bit calls: see above.
-template <int KV, int DIM>
+template <int KV, bool SEVERAL, int DIM>
 cudaError_t by_type(const SharedProblem &p, cudaStream_t s) {
     constexpr int64_t kLong = 256;
-    if (p.dtype == OM_F32) return launch<KV, DIM, 2, kSharedFold>(p, s);
-    return p.most_tiles > kLong ? launch<KV, DIM, 1, 64>(p, s) : launch<KV, DIM, 1, 0>(p, s);
+    if (p.dtype == OM_F32) return launch<KV, DIM, 2, kSharedFold, SEVERAL>(p, s);
+    return p.most_tiles > kLong ? launch<KV, DIM, 1, 64, SEVERAL>(p, s) : launch<KV, DIM, 1, 0, SEVERAL>(p, s);
 }
 
-template <int KV>
+template <int KV, bool SEVERAL>
 cudaError_t run_kv_shared(const SharedProblem &p, cudaStream_t s) {
-    if (p.c.dim == 64) return by_type<KV, 64>(p, s);
-    return p.c.dim == 128 ? by_type<KV, 128>(p, s) : by_type<KV, 256>(p, s);
+    if (p.c.dim == 64) return by_type<KV, SEVERAL, 64>(p, s);
+    return p.c.dim == 128 ? by_type<KV, SEVERAL, 128>(p, s) : by_type<KV, SEVERAL, 256>(p, s);
 }
 
 }  // namespace

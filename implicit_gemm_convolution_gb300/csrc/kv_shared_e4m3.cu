@@ -2,5 +2,5 @@
 #include "kv_shared.cuh"
 
 namespace om {
-cudaError_t launch_kv_shared_e4m3(const SharedProblem &p, cudaStream_t s) { return run_kv_shared<OM_E4M3>(p, s); }
+cudaError_t launch_kv_shared_e4m3(const SharedProblem &p, cudaStream_t s) { return run_kv_shared<OM_E4M3, false>(p, s); }
 }  // namespace om

@@ -1,0 +1,6 @@
+// kv_shared_pages_i8.cu -- attention to shared prefixes, whole numbers, in pages smaller than a tile.
+#include "kv_shared.cuh"
+
+namespace om {
+cudaError_t launch_kv_shared_pages_i8(const SharedProblem &p, cudaStream_t s) { return run_kv_shared<OM_I8, true>(p, s); }
+}  // namespace om

@@ -572,8 +572,9 @@ OM_API size_t om_kv_shared_workspace_bytes(int64_t kv_heads, int64_t q_heads, in
  * own tokens start a page of their own; its positions go on from the prefix only in the rotation of its queries and keys, which is
  * the caller's). The query at a sequence's own position p sees its whole prefix and its own positions 0 .. p:
  *   out[t][h] = sum_i softmax_i(scale * q[t][h] . key_i) value_i over both;  lse as in om_kv_attention.
- * Rows that see nothing, scores that are NaN, table entries outside the cache, tokens that no sequence owns, the precision of queries and
- * weights: as there. Products over the prefix run on the tensor cores (sums of 32 bits).
+ * Rows that see nothing, scores that are NaN, table entries outside the cache, tokens that no sequence owns: as there. Products over the prefix
+ * run on the tensor cores. Elements of 32-bit queries are held to 2^-22 of their row's largest, softmax weights over the prefix to 2^-22 of themselves
+ * or 2^-24 of the largest among 64 neighbouring positions; a page's scales take no bits from another page's.
  * workspace: device memory, 16-byte aligned, of om_kv_shared_workspace_bytes for this call's heads, max_new and tokens or more (8 dim + 16 bytes a
  * token and query head, and up to 141 MB for the blocks' parts), zeroed once before its first use; calls that may run at the same time need
  * distinct ones. A bounded device wait that runs out is recorded in its

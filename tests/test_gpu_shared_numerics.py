@@ -45,3 +45,74 @@ def test_scores_leave_weights_that_are_still_read(dim, x):
     # cut sums: as far as the fold (32-bit queries) or the whole prefix goes
     tol = {"f32": 2.0 ** -18, "f16": 2.0 ** -15 + ref.UNIT["f16"], "bf16": 2.0 ** -15 + ref.UNIT["bf16"]}[x]
     assert float((outs[0].double() - want).abs().max()) <= tol * want
+
+
+def one_token_each(prefix, seqs, hq, dim, page, kind, seed):
+    """Sequences of one token of their own behind one prefix, one key head."""
+    return Shared([prefix], [0, seqs], [1] * seqs, [1] * seqs, 1, dim, page, kind, seed, extra=0)
+
+
+def against_64_bits(s, q, x):
+    """check() of test_gpu_shared_attention.py on the device, with its tolerance, for one_token_each."""
+    prefix, (tokens, hq, dim), scale = s.prefixes[0], q.shape, s.dim ** -0.5
+    s.device()
+    ws, lse = s.workspace(hq), torch.empty(tokens, hq, device="cuda")
+    out = s.attend(q, lse=lse, workspace=ws)
+    assert om.workspace_status(ws) == 0
+    assert torch.equal(s.attend(q, workspace=ws), out)
+    pos = torch.arange(prefix, device="cuda")
+    ids, rows = torch.from_numpy(s.ptable_np[0]).cuda()[pos // s.page], pos % s.page
+    own = torch.from_numpy(s.table_np[:, 0]).cuda()
+    k, v = (c.float()[ids, 0, rows].double() * t[ids, 0][:, None].double() for c, t in ((s.k, s.ks), (s.v, s.vs)))
+    ko, vo = (c.float()[own, 0, 0].double() * t[own, 0][:, None].double() for c, t in ((s.k, s.ks), (s.v, s.vs)))
+    qq = q.double()
+    y = scale * torch.cat((torch.einsum("thd,ld->thl", qq, k), torch.einsum("thd,td->th", qq, ko)[..., None]), -1)
+    big = scale * torch.cat((torch.einsum("thd,ld->thl", qq.abs(), k.abs()), torch.einsum("thd,td->th", qq.abs(), ko.abs())[..., None]), -1).amax(-1)
+    total = torch.logsumexp(y, -1)
+    w = (y - total[..., None]).exp()
+    mix = lambda a, b: w[..., :-1] @ a + w[..., -1:] * b[:, None]
+    want, mag = mix(v, vo), mix(v.abs(), vo.abs())
+    steps = prefix / 8 + 64
+    ds = (dim + 16) * 2.0 ** -22 * big
+    tol = (2 * ds + 2.0 ** -19 + steps * 2.0 ** -22)[..., None] * mag + 1.01 * ref.UNIT[x] * want.abs() + ref.TINY[x] + 1e-30
+    off = (out.double() - want).abs()
+    assert bool((off <= tol).all()), f"outputs {float((off / tol).max())} of the tolerance"
+    assert bool(((lse.double() - total).abs() <= ds + (steps + 64) * 2.0 ** -22 + 2.0 ** -20 + 2.0 ** -22 * total.abs()).all()), "lse"
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("far", [1, 7, 8, 9, 20, 40, 90])
+@pytest.mark.parametrize("page,dim", [(16, 64), (32, 128), (16, 256), (64, 128)])
+def test_scales_far_apart_in_one_tile(page, dim, far, kind, x):
+    """Pages of one tile whose tokens weigh about the same, their value scales 2^far apart. In odd dimensions the pages of the large scale
+    hold zeros, so what comes out there is the others', to the precision that they would have alone."""
+    s = one_token_each(333, 5, 8, dim, page, kind, far + page)
+    large = torch.arange(s.pages, device="cuda") % 2 == 0
+    s.vs[:, 0] = torch.where(large, 1.0, 2.0 ** -far) * (0.5 + torch.rand(s.pages, device="cuda"))
+    odd = torch.arange(dim, device="cuda") % 2 == 1
+    s.v.view(torch.int8)[large[:, None, None, None] & odd[None, None, None, :].expand(s.v.shape[0], 1, page, dim)] = 0
+    s.vs[torch.from_numpy(s.table_np[:, 0]).cuda()] = 2.0 ** -far  # the own tokens: as small
+    s.v.view(torch.int8)[torch.from_numpy(s.table_np[:, 0]).cuda()] = 0
+    q = 0.1 * torch.randn(5, 8, dim, generator=torch.Generator(device="cuda").manual_seed(far), device="cuda")
+    against_64_bits(s, q.to(ref.TORCH[x]), x)
+    against_64_bits(s, torch.zeros_like(q).to(ref.TORCH[x]), x)
+
+
+@pytest.mark.parametrize("x", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("page,dim,prefix", [(16, 64, 16003), (32, 128, 9000), (16, 256, 5000)])
+def test_scales_of_all_sizes_over_long_parts(page, dim, prefix, kind, x):
+    """Several tiles a block (sums of 32-bit queries leave tensor memory among them), value scales of every page anywhere in 2^50, some 0 or
+    negative, large ones with zeros in odd dimensions; maxima that rise towards the end."""
+    s = one_token_each(prefix, 260, 10, dim, page, kind, prefix)
+    g = torch.Generator(device="cuda").manual_seed(3)
+    power = torch.randint(-45, 6, (s.pages,), generator=g, device="cuda")
+    sign = torch.randint(-1, 2, (s.pages,), generator=g, device="cuda") | 1
+    s.vs[:, 0] = torch.exp2(power.float()) * sign * (torch.rand(s.pages, generator=g, device="cuda") > 0.05)
+    odd = torch.arange(dim, device="cuda") % 2 == 1
+    s.v.view(torch.int8)[(power > -20)[:, None, None, None] & odd[None, None, None, :].expand(s.v.shape[0], 1, page, dim)] = 0
+    pages = torch.from_numpy(s.ptable_np[0]).cuda()[: -(-prefix // page)]
+    s.ks[pages, 0] = torch.linspace(1e-5, 1e-2, len(pages), device="cuda")
+    q = torch.randn(260, 10, dim, generator=g, device="cuda")
+    against_64_bits(s, q.to(ref.TORCH[x]), x)
