@@ -436,7 +436,8 @@ def new_kv_workspace(cache, q_heads: int, max_new: int):
 def kv_attention(cache, q, block_table, ctx_len, cu, max_new: int, scale=None, window: int = 0, out=None, lse=None,
                  workspace=None, stream=None, sinks: int = 0):
     """Attention of each sequence's last tokens' queries, q (tokens, q heads, dim),
-    to its cached tokens, causal, within `window` positions (0: all) and the sequence's first `sinks` ones.
+    to its cached tokens, causal, within `window` positions (0: all) and the sequence's first `sinks` ones (a mask: they keep the
+    rotation that they were stored with).
 
     scale: default dim ** -0.5. lse: float32 (tokens, q heads), receives the natural log of the sums
     of exponentials. workspace: from new_kv_workspace; without one each sequence
@@ -475,7 +476,8 @@ def kv_attention(cache, q, block_table, ctx_len, cu, max_new: int, scale=None, w
 
 def new_shared_workspace(cache, q_heads: int, max_new: int, tokens: int):
     """A device tensor usable as the workspace of kv_shared_attention for calls of these heads
-    with at most `tokens` tokens and max_new queries a sequence; one per stream."""
+    with at most `tokens` tokens and max_new queries a sequence; one per stream. It holds 8 dim + 16 bytes for each token and
+    query head: 2.2 GB for 65536 tokens of 32 heads of 128."""
     n = lib().om_kv_shared_workspace_bytes(cache.heads, q_heads, cache.dim, max_new, tokens)
     if n == 0:
         raise ValueError("q_heads must be a multiple of the cache's heads, max_new and tokens positive")
@@ -489,7 +491,8 @@ def kv_shared_attention(cache, q, prefix_table, prefix_len, groups, block_table,
     groups (int32 [prefixes + 1], not decreasing): sequences groups[j] .. groups[j + 1] - 1 begin with the prefix_len[j] tokens
     (int32 [prefixes]) in the pages prefix_table[j] (int32 [prefixes, width]); block_table, ctx_len and cu are
     the sequences' own tokens behind it, which start on a page of their own. A query sees its whole
-    prefix and its sequence's own tokens up to itself. workspace: from new_shared_workspace (None: a new one). scale, lse,
+    prefix and its sequence's own tokens up to itself. workspace: from new_shared_workspace (None: a new one, zeroed as a whole in
+    every call). A prefix_table that is no wider than its prefixes need does best. scale, lse,
     and what is returned, as in kv_attention.
     """
     device = cache.device

@@ -547,7 +547,9 @@ OM_API int om_kv_attention(const om_kv_cache *cache, int64_t seqs, int64_t token
 /*
  * om_kv_attention whose window leaves a sequence's first `sinks` tokens visible: the query at position p sees
  * the positions t <= p with t > p - window or t < sinks. With window 0, or sinks 0, it is om_kv_attention.
- * What lies between is neither read nor counted as work.
+ * This is a mask and nothing more: first tokens keep the rotation that they were stored with, and there are no learned scores beside the keys'.
+ * What lies between the first tokens and the window of a sequence's first query is neither read nor counted as work. With several queries the
+ * positions from there on count for all of them: a long prompt's later queries cost more than with the window alone.
  */
 OM_API int om_kv_attention_sinks(const om_kv_cache *cache, int64_t seqs, int64_t tokens, int64_t max_new,
                                  int64_t q_heads,
@@ -573,12 +575,15 @@ OM_API size_t om_kv_shared_workspace_bytes(int64_t kv_heads, int64_t q_heads, in
  * the caller's). The query at a sequence's own position p sees its whole prefix and its own positions 0 .. p:
  *   out[t][h] = sum_i softmax_i(scale * q[t][h] . key_i) value_i over both;  lse as in om_kv_attention.
  * Rows that see nothing, scores that are NaN, table entries outside the cache, tokens that no sequence owns: as there. Products over the prefix
- * run on the tensor cores. Elements of 32-bit queries are held to 2^-22 of their row's largest, softmax weights over the prefix to 2^-22 of themselves
+ * run on the tensor cores, whose 32-bit sums are cut off instead of rounded: for 32-bit queries every 256 positions are added with rounding (errors
+ * of some 2e-6 of the magnitudes), for 16-bit ones up to 16384, or 4096 where a block's part may be longer (3e-5). Elements of 32-bit queries are held to 2^-22 of their row's largest, softmax weights over the prefix to 2^-22 of themselves
  * or 2^-24 of the largest among 64 neighbouring positions; a page's scales take no bits from another page's.
  * workspace: device memory, 16-byte aligned, of om_kv_shared_workspace_bytes for this call's heads, max_new and tokens or more (8 dim + 16 bytes a
  * token and query head, and up to 141 MB for the blocks' parts), zeroed once before its first use; calls that may run at the same time need
  * distinct ones. A bounded device wait that runs out is recorded in its
- * status word (om_workspace_status), and the outputs are then incomplete. Results do not depend on timing.
+ * status word (om_workspace_status), and the outputs are then incomplete. Results do not depend on timing; how the work is
+ * cut, and so their last bits, follows from prefix_width too: a table cut to its prefixes does best (one far wider takes the kernel for long
+ * parts: 64 sequences of 64 heads behind 32768 tokens 8 % more).
  */
 OM_API int om_kv_shared_attention(const om_kv_cache *cache, int64_t groups,
                                   const int32_t *prefix_table, int64_t prefix_width, const int32_t *prefix_len,

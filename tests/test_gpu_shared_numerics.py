@@ -5,7 +5,7 @@ torch = pytest.importorskip("torch")
 
 import implicit_gemm_convolution_gb300 as om  # noqa: E402
 from tests import decode_ref as ref  # noqa: E402
-from tests.test_gpu_shared_attention import Shared  # noqa: E402
+from tests.test_gpu_shared_attention import Shared, long_parts  # noqa: E402
 
 pytestmark = pytest.mark.gpu
 
@@ -116,3 +116,15 @@ def test_scales_of_all_sizes_over_long_parts(page, dim, prefix, kind, x):
     s.ks[pages, 0] = torch.linspace(1e-5, 1e-2, len(pages), device="cuda")
     q = torch.randn(260, 10, dim, generator=g, device="cuda")
     against_64_bits(s, q.to(ref.TORCH[x]), x)
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_sums_of_one_sign_are_cut_for_four_tiles_only(dim):
+    """32-bit queries of zero behind 131072 tokens: weights are equal, values of one sign, so what the tensor cores cut off adds up. A step of 16
+    positions and one of two parts cuts at most a unit in the last place of the sum so far, 2^-23 of it: 32 steps in four tiles, on
+    average half of the sum, 16.5 of them. Then each fold rounds half a unit of the sum so far, half of the part's on average; the rest
+    (weights in two parts, means, the join of some ten parts) is 2^-21. Sums that stayed for 16 tiles would be 66 units off."""
+    worst = long_parts("f32", dim, 512, 8, 131072, 600, True, 50)
+    blocks = torch.cuda.get_device_properties(0).multi_processor_count * (1 if dim == 256 else 2)
+    tiles = -(-(131072 // 64) * (512 * 8 // 128) // blocks)  # of a block
+    assert worst <= 16.5 * 2.0 ** -23 + tiles / 4 / 2 * 2.0 ** -24 + 2.0 ** -21, worst
