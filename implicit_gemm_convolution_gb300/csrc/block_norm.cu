@@ -18,9 +18,9 @@
 // Operands whose rows lie differently to the boundaries go element by element throughout.
 //
 // Bound and measured (GB300; 6 786 GB/s is the measured copy bandwidth). HBM for many rows: 16000 x 8192, bfloat16 with a 32-bit stream, a gate of
-// each token and both norms 314 us (5 840 GB/s, 86 %), without gate and first norm 232 us (100 %), all of it bfloat16 158 us (98 %). Residual and
+// each token and both norms 311 us (5 890 GB/s, 87 %), without gate and first norm 232 us (100 %), all of it bfloat16 156 us (99 %). Residual and
 // gate in registers from the start (124 of them, two blocks an SM) took 447 us of the first; pieces of 32 bytes a lane instead of 16 for 32-bit streams
-// 381 us (each copy took half of a sector). Latency for few: one token 3.2 us in a row of calls in a graph; 192 rows of 8177, layer norm, float16, 8.9 us.
+// 381 us (each copy took half of a sector). Latency for few: one token 2.8 us in a row of calls in a graph; 192 rows of 8177, layer norm, float16, 8.7 us.
 
 #include <type_traits>
 
@@ -392,7 +392,7 @@ cudaError_t by_width(const NormProblem &p, int offset, int advance, cudaStream_t
     const int64_t vectors = (p.width + kVector - 1) / kVector + (LIE == kShifted);
     auto warps = [&](int v) { return static_cast<int>((vectors + 32 * v - 1) / (32 * v)); };
     auto args = [&](int v) { return NormArgs{p, warps(v), offset, advance, false, p.tokens > 1 && p.ldg == 0}; };
-    // eight elements a thread where all rows are in flight at once (153 rows of 4096: 4.1 us, with 32 elements 5.4; 192 of 8177: 8.3 against 7.8)
+    // eight elements a thread where all rows are in flight at once (153 rows of 4096: 3.1 us, with 32 elements 4.8; 192 of 8177, which are not: 8.3 with 32, 9.7 with eight)
     if ((warps(1) <= 32 && p.tokens * warps(1) <= 36 * num_sms()) || warps(1) == 1) return launch<T, R, 1, 1024, LIE>(args(1), s);
     if (warps(2) == 1) return launch<T, R, 2, 512, LIE>(args(2), s);
     if (warps(4) <= 8) return launch<T, R, 4, 256, LIE>(args(4), s);

@@ -39,7 +39,7 @@
 // blocks an SM about 4 us until the first product, 45 us in the loop, 9 us for the joins. One of 331 tokens: 7.8 us, latency. 25
 // rows of 32-bit queries over a window of 4096: 73 us, 31 %: latency, at two warps a scheduler (255 registers), with
 // the tensor pipe 34 % and the ALU 34 % busy; rows are in two blocks that each copy and widen the codes. First tokens that stay visible before
-// a window are tiles of the same loop: 64 sequences of up to 17000 tokens, a window of 8192 behind 4 first tokens: 177 us, 89 %.
+// a window are tiles of the same loop: 64 sequences of up to 17000 tokens, a window of 8192 behind 4 first tokens: 176 us, 90 %.
 #pragma once
 
 #include <cfloat>

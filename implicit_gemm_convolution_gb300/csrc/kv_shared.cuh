@@ -27,9 +27,9 @@
 //
 // Bound and measured (GB300). What the rows issue: a score costs a maximum, an exponential, its part of a sum, two conversions to 16 bits and the
 // difference between them, and two blocks an SM fill each other's waits. 64 sequences behind a prefix of 32768 tokens (8 key heads of 128, 8 query
-// heads each, bfloat16): this kernel 118 us, with the own tokens and the join 154 us; the tensor cores are busy 56 % of it, issue slots 66 %. The
+// heads each, bfloat16): this kernel 118 us, with the own tokens and the join 154 us; the tensor cores are busy 57 % of it, issue slots 66 %. The
 // prefix is read once (67 MB of keys and values, 10 us at the copy bandwidth). One token of each sequence over the same prefix by kv_attention.cuh
-// reads it 64 times. 40 sequences with drafts of 32-bit queries, which go in two parts, behind three prefixes of 8001 tokens: 90 us of 127 (with all of a part's sums
+// reads it 64 times. 40 sequences with drafts of 32-bit queries, which go in two parts, behind three prefixes of 8001 tokens: 92 us of 132 (with all of a part's sums
 // in tensor memory 53 of 90, and errors to 9e-6 behind long prefixes, where they are 2e-6 now). Tiles of 128 positions with one block an SM ran
 // slower (nothing to fill the waits of the rows). Registers by warpgroup (88 for rows, 56 for copies): with equal shares the rows spill, and loads
 // that wait for a spilled register no longer run ahead.
@@ -251,7 +251,7 @@ __device__ __forceinline__ uint4 load_codes(const uint8_t *at, bool there) {
     return x;
 }
 
-// SEVERAL: pages are smaller than a tile, which then can come again. (As a choice at run time 64 conversations in pages of 64 took 163 us instead of 157.)
+// SEVERAL: pages are smaller than a tile, which then can come again. (As a choice at run time 64 conversations in pages of 64 took 163 us instead of 154.)
 // FOLD: tiles whose sums stay in tensor memory before they are added to those in global memory, as rounded 32-bit sums (0: all of a part's)
 template <int KV, int DIM, int PARTS, int FOLD, bool SEVERAL>
 __global__ void __launch_bounds__(kThreads, DIM == 256 ? 1 : 2) kv_shared_kernel(const __grid_constant__ SharedProblem p) {
@@ -916,7 +916,7 @@ cudaError_t launch(const SharedProblem &p, cudaStream_t s) {
 }
 
 // The tensor cores cut their sums off. 16-bit calls leave a part's sums to them up to 256 tiles (values of one sign, weights alike: 3e-5 off);
-// with the code for longer ones, 64 tiles at a time, 64 sequences behind 32768 tokens took 170 us instead of 157. 32-bit calls: see above.
+// with the code for longer ones, 64 tiles at a time, 64 sequences behind 32768 tokens take 166 us instead of 154. 32-bit calls: see above.
 template <int KV, bool SEVERAL, int DIM>
 cudaError_t by_type(const SharedProblem &p, cudaStream_t s) {
     constexpr int64_t kLong = 256;
