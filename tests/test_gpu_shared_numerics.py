@@ -89,12 +89,13 @@ def test_scales_far_apart_in_one_tile(page, dim, far, kind, x):
     hold zeros, so what comes out there is the others', to the precision that they would have alone."""
     s = one_token_each(333, 5, 8, dim, page, kind, far + page)
     large = torch.arange(s.pages, device="cuda") % 2 == 0
-    s.vs[:, 0] = torch.where(large, 1.0, 2.0 ** -far) * (0.5 + torch.rand(s.pages, device="cuda"))
+    g = torch.Generator(device="cuda").manual_seed(far)
+    s.vs[:, 0] = torch.where(large, 1.0, 2.0 ** -far) * (0.5 + torch.rand(s.pages, generator=g, device="cuda"))
     odd = torch.arange(dim, device="cuda") % 2 == 1
     s.v.view(torch.int8)[large[:, None, None, None] & odd[None, None, None, :].expand(s.v.shape[0], 1, page, dim)] = 0
     s.vs[torch.from_numpy(s.table_np[:, 0]).cuda()] = 2.0 ** -far  # the own tokens: as small
     s.v.view(torch.int8)[torch.from_numpy(s.table_np[:, 0]).cuda()] = 0
-    q = 0.1 * torch.randn(5, 8, dim, generator=torch.Generator(device="cuda").manual_seed(far), device="cuda")
+    q = 0.1 * torch.randn(5, 8, dim, generator=g, device="cuda")
     against_64_bits(s, q.to(ref.TORCH[x]), x)
     against_64_bits(s, torch.zeros_like(q).to(ref.TORCH[x]), x)
 
