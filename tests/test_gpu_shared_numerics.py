@@ -129,3 +129,30 @@ def test_sums_of_one_sign_are_cut_for_four_tiles_only(dim):
     blocks = torch.cuda.get_device_properties(0).multi_processor_count * (1 if dim == 256 else 2)
     tiles = -(-(131072 // 64) * (512 * 8 // 128) // blocks)  # of a block
     assert worst <= 16.5 * 2.0 ** -23 + tiles / 4 / 2 * 2.0 ** -24 + 2.0 ** -21, worst
+
+
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+def test_what_is_not_finite_beside_scales_far_apart(x):
+    """Tiles that come again: NaN codes behind the prefix's end and pages that are not there stay hidden in every pass, a scale or a visible code that
+    is NaN shows."""
+    s = Shared([200, 200], [0, 2, 4], [1] * 4, [1] * 4, 1, 64, 16, "e4m3", 5, extra=0)
+    first, last = s.ptable_np[0], s.ptable_np[1]
+    s.vs[torch.from_numpy(first[::2].copy()).cuda()] *= 2.0 ** -40
+    s.vs[torch.from_numpy(last[1::2].copy()).cuda()] *= 2.0 ** -60
+    for t in (s.k, s.v):
+        t.view(torch.int8)[int(first[12]), :, 8:] = 0x7F  # positions 200 .. 207 of the first prefix
+    s.ptable_np[0, 3] = -1
+    s.device()
+    q = torch.randn(4, 8, 64, generator=torch.Generator(device="cuda").manual_seed(2), device="cuda").to(ref.TORCH[x])
+    ws = s.workspace(8)
+    out = s.attend(q, workspace=ws)
+    assert torch.isfinite(out).all()
+    for change in (lambda: s.vs.__setitem__((int(last[4]), 0), float("inf")), lambda: s.ks.__setitem__((int(last[7]), 0), float("nan")),
+                   lambda: s.v.view(torch.int8).__setitem__((int(last[5]), 0, 3), 0x7F)):
+        keep = [t.view(torch.int8).clone() if t.element_size() == 1 else t.clone() for t in (s.vs, s.ks, s.v)]
+        change()
+        got = s.attend(q, workspace=ws)
+        assert torch.equal(got[:2], out[:2]) and torch.isnan(got[2:]).all()
+        for t, k in zip((s.vs, s.ks, s.v), keep):
+            (t.view(torch.int8) if t.element_size() == 1 else t).copy_(k)
+    assert torch.equal(s.attend(q, workspace=ws), out) and om.workspace_status(ws) == 0
